@@ -7,7 +7,10 @@
  * plus moe_plan_replicas (a replica plan for the next layer from moe_stats'
  * prediction, made before that layer routes), moe_prediction_quality (how
  * well the prediction and the plan matched the routing that followed),
- * moe_stats_load_state (window variants) and moe_backward (the gradients).
+ * moe_stats_load_state (window variants) and moe_backward (the gradients);
+ * moe_gate in the place of moe_route (biased, grouped, sigmoid gates),
+ * moe_layer_norm after the combine (residual sum and norm), and moe_grad_norm
+ * and moe_clip_grads after the backward pass.
  *
  * Sources (page title, section):
  *   [PF]   "PopFetcher: Towards Accelerated Mixture-of-Experts Training Via
@@ -66,18 +69,21 @@ typedef enum {
 
 /* Bits of the device-check word (see the conventions above). */
 enum {
-    MOE_CHECK_LOGITS = 1,     /* moe_route: a NaN or infinite router logit */
-    MOE_CHECK_INDEX = 2,      /* moe_stats, moe_dispatch: an expert index outside [0, E) */
+    MOE_CHECK_LOGITS = 1,     /* moe_route: a NaN or infinite router logit; moe_gate: NaN or +inf */
+    MOE_CHECK_INDEX = 2,      /* moe_stats, moe_dispatch, moe_gate_backward: an expert index outside [0, E) */
     MOE_CHECK_DUPLICATE = 4,  /* moe_stats, moe_dispatch: one token names the same expert twice */
     MOE_CHECK_COUNTS = 8,     /* moe_dispatch: `counts` differs from the counts of topk_idx */
     MOE_CHECK_REPLICAS = 16,  /* moe_dispatch: a negative replica count, or copies beyond max_slots */
     MOE_CHECK_SLOTS = 32,     /* moe_expert_ffn: slot table not ascending inside [0, M], n_slots
                                  outside [0, max_slots], or an expert outside [0, E) */
-    MOE_CHECK_ROWS = 64       /* moe_combine: an inv_pos entry outside [0, M) */
+    MOE_CHECK_ROWS = 64,      /* moe_combine: an inv_pos entry outside [0, M) */
+    MOE_CHECK_GRADS = 128     /* moe_grad_norm, moe_clip_grads: the norm is infinite or NaN */
 };
 
 typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;       /* activations and weights */
 typedef enum { MOE_SWIGLU = 0, MOE_GELU = 1 } moe_act;
+typedef enum { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 } moe_score;        /* moe_gate: an expert's score of its logit */
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
 typedef enum { MOE_GEMM_AUTO = 0, MOE_GEMM_GROUPED = 1, MOE_GEMM_DENSE = 2, MOE_GEMM_GROUPED_SMALL = 3 } moe_gemm_path;
 
 /* ---------------------------------------------------------------- routing
@@ -95,6 +101,55 @@ typedef enum { MOE_GEMM_AUTO = 0, MOE_GEMM_GROUPED = 1, MOE_GEMM_DENSE = 2, MOE_
  */
 int moe_route(const float* logits, int64_t T, int E, int k, int32_t* topk_idx, float* topk_w,
               int32_t* check, void* stream);
+
+/*
+ * moe_gate -- the gates beyond moe_route's renormalised softmax: sigmoid
+ * scores, a selection bias that balances the experts' load, a choice among
+ * groups of experts first (a token reaches few devices or nodes), weights that
+ * are not renormalised, a scale.
+ *   logits     [T, E] in dtype `dt`.  A logit that is NaN or at most -1e38 masks
+ *              its expert (-inf, or either dtype's lowest value); +inf counts as
+ *              the largest float.
+ *   score      s[e]: softmax of the row over the unmasked experts, or
+ *              1 / (1 + exp(-logit)); 0 for a masked expert.
+ *   bias       fp32 [E] or NULL: added to the scores for the selection only.
+ *              NaN counts as the lowest value.
+ *   n_groups, keep_groups, group_score   the experts in n_groups contiguous
+ *              groups of E / n_groups; a group's score is the largest s + b of
+ *              its unmasked experts (GROUP_MAX) or the sum of its two largest
+ *              (GROUP_TOP2; one, where there is only one).  Only the keep_groups
+ *              groups of the highest score take part; keep_groups == n_groups
+ *              leaves all in.
+ *   topk_idx   int32 [T, k] out: the k experts with the largest s + b,
+ *              descending.  Without a bias an expert's place is its logit's.
+ *              Masked experts come after all others, in index order.  Ties, of
+ *              groups and of experts, go to the lower index; scores are compared
+ *              in double, so two that differ only there do not tie.
+ *   topk_w     fp32 [T, k] out: scale * s, or with `renorm` scale * s / (sum of
+ *              the k chosen s).  0 for a masked expert (a row with nothing
+ *              unmasked gets zeros).
+ * With score SOFTMAX, renorm, one group, no bias and scale 1 it is moe_route.
+ * Limits: 1 <= E <= 256, 1 <= k <= min(E, 8), n_groups <= 64 divides E,
+ * k <= keep_groups * (E / n_groups), 0 <= T, T*k < 2^31, scale finite.
+ * check: MOE_CHECK_LOGITS for a NaN or +inf logit.
+ *
+ * moe_gate_backward -- d_logits [T, E] in dtype `dt`, written whole, from
+ * d_topk_w fp32 [T, k], the loss's gradient of moe_gate's weights for the
+ * experts topk_idx (with g = scale * d_topk_w, r the chosen scores over their sum):
+ *   SOFTMAX, renorm   r_i (g_i - sum_j g_j r_j) at topk_idx[i], 0 elsewhere
+ *   SIGMOID, renorm   the same times (1 - s_i)
+ *   SIGMOID           g_i s_i (1 - s_i) at topk_idx[i], 0 elsewhere
+ *   SOFTMAX           g_i s_i at topk_idx[i], minus s[e] * sum_j g_j s_j at every e
+ * The selection and its bias have no gradient; masked experts get 0.  An
+ * expert named twice gets both slots' parts.  Entries outside [0, E) are
+ * skipped (MOE_CHECK_INDEX).  Limits: those of moe_gate.
+ */
+int moe_gate(const void* logits, moe_dtype dt, int64_t T, int E, int k, moe_score score, const float* bias,
+             int n_groups, int keep_groups, moe_group_score group_score, int renorm, float scale,
+             int32_t* topk_idx, float* topk_w, int32_t* check, void* stream);
+int moe_gate_backward(const void* logits, moe_dtype dt, int64_t T, int E, int k, moe_score score, int renorm,
+                      float scale, const int32_t* topk_idx, const float* d_topk_w, void* d_logits,
+                      int32_t* check, void* stream);
 
 /* ------------------------------------------------------------- statistics
  * Sliding-window routing statistics of a chain of L MoE layers ([PF] method:
@@ -417,6 +472,73 @@ int moe_backward(const void* x_perm, const void* y_perm, moe_dtype dt, int64_t T
                  const void* w_gate, const void* w_up, const void* w_down, moe_act act, const void* d_out,
                  void* d_x, float* d_logits, void* d_w_gate, void* d_w_up, void* d_w_down, void* workspace,
                  size_t workspace_bytes, void* stream);
+
+/*
+ * moe_backward_gated -- moe_backward for a layer routed by moe_gate: the same
+ * arguments, with d_topk_w fp32 [T, k] = dw[t, i] in the place of d_logits
+ * (moe_gate_backward takes it on to the logits).
+ */
+int moe_backward_gated(const void* x_perm, const void* y_perm, moe_dtype dt, int64_t T, int k, int H, int I, int E,
+                       const int32_t* topk_idx, const float* topk_w, const int32_t* inv_pos,
+                       const int32_t* expert_off, const void* w_gate, const void* w_up, const void* w_down,
+                       moe_act act, const void* d_out, void* d_x, float* d_topk_w, void* d_w_gate, void* d_w_up,
+                       void* d_w_down, void* workspace, size_t workspace_bytes, void* stream);
+
+/* --------------------------------------------------------------- layer norm
+ * moe_layer_norm -- the residual sum and layer norm that follow a layer:
+ *   s = x + residual, rounded to `dt` and written to x_sum (residual and x_sum
+ *   both NULL: s = x);  y = (s - mean) / sqrt(var + eps) * weight + bias
+ * over the H elements of each of the T rows; mean, var and the products in
+ * fp32, y rounded once.  weight and bias [H] in `w_dt` (fp32, or `dt`); either
+ * may be NULL (1 and 0).  A row with a NaN or infinity gives NaN in that row
+ * alone; squares of |s - mean| beyond 1e18 overflow.  y or x_sum may be x or
+ * residual itself (the same buffer), not each other.
+ * Limits: 1 <= H <= 16384, 0 <= T < 2^40, eps > 0; rows need only the
+ * alignment of their elements.
+ *
+ * moe_layer_norm_backward -- from d_y, x (the norm's input: x_sum where there
+ * was a residual) and weight:
+ *   d_x = rstd (g - mean(g) - n mean(g n)) + d_skip, g = d_y weight,
+ *         n = (x - mean) rstd, mean over the row; d_skip (may be NULL) is the
+ *         gradient that reaches s past the norm.  d_x is the gradient of x and
+ *         of residual alike;
+ *   d_weight = sum over rows of d_y n, d_bias = sum over rows of d_y, in
+ *         `w_dt`, summed in fp32 in an order that only T and H decide; either
+ *         may be NULL.
+ * The row's mean and rstd are formed again from x.  d_x may be d_y or d_skip
+ * itself, not x.  Workspace (only where d_weight or d_bias is asked for and T > 0):
+ * moe_layer_norm_backward_workspace_bytes(T, H) bytes, 16-byte aligned.
+ */
+int moe_layer_norm(const void* x, const void* residual, moe_dtype dt, int64_t T, int H, const void* weight,
+                   const void* bias, moe_dtype w_dt, float eps, void* x_sum, void* y, void* stream);
+size_t moe_layer_norm_backward_workspace_bytes(int64_t T, int H); /* [host] */
+int moe_layer_norm_backward(const void* d_y, const void* x, moe_dtype dt, int64_t T, int H, const void* weight,
+                            moe_dtype w_dt, float eps, const void* d_skip, void* d_x, void* d_weight, void* d_bias,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* -------------------------------------------------------- gradient clipping
+ * moe_grad_norm -- the global norm of n gradients:
+ *   norm  fp32 [1] out: sqrt of the sum of all squares of all tensors, summed
+ *         in double in an order that only the sizes decide.
+ * moe_clip_grads -- the norm, and each gradient scaled to it:
+ *   out[i] = grads[i] * min(1, max_norm / (norm + eps)), rounded once.
+ * The lists are [host] arrays, read before the call returns: grads (and out)
+ * hold device pointers, numel element counts (0 is fine), dt dtypes; types may
+ * be mixed and tensors need only the alignment of their elements.  out[i] may
+ * be grads[i] (in place; nothing is written where the factor is 1); otherwise
+ * an output overlaps no other tensor of the call.  norm and workspace are
+ * buffers of their own.  An infinite or NaN norm raises
+ * MOE_CHECK_GRADS and scales by what the formula gives (0 or NaN).
+ * The lists travel in the kernels' arguments, 96 tensors a launch.
+ * Limits: numel < 2^37, max_norm >= 0 and finite, eps > 0; workspace of
+ * moe_grad_norm_workspace_bytes() bytes, 16-byte aligned.
+ */
+size_t moe_grad_norm_workspace_bytes(void); /* [host] */
+int moe_grad_norm(const void* const* grads, const int64_t* numel, const moe_dtype* dt, int n, float* norm,
+                  void* workspace, size_t workspace_bytes, int32_t* check, void* stream);
+int moe_clip_grads(const void* const* grads, void* const* out, const int64_t* numel, const moe_dtype* dt, int n,
+                   float max_norm, float eps, float* norm, void* workspace, size_t workspace_bytes,
+                   int32_t* check, void* stream);
 
 /* ---------------------------------------------------------------- errors */
 const char* moe_status_string(int status); /* [host] static text */

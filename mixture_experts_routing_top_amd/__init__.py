@@ -13,6 +13,12 @@ call fails, an exception is raised.
     d      = moe_dispatch(x, idx, E, replicas, max_slots)
     y_perm = moe_expert_ffn(d["x_perm"], d["slot_off"], ..., w_gate, w_up, w_down)
     out    = moe_combine(y_perm, d["inv_pos"], w)
+    y, s   = moe_layer_norm(out, weight, bias, residual=x)   # s = out + x, y its norm
+
+moe_gate routes in moe_route's place where the gate has a bias, groups, sigmoid
+scores or weights that are not renormalised.  In training, moe_backward (or
+moe_backward_gated and moe_gate_backward) and moe_layer_norm_backward give the
+gradients, and moe_clip_grads bounds their global norm.
 
 Every hot-path call takes `check`: an int32 device tensor of one element
 (zeroed by the caller) that the kernels flag invalid input into;
@@ -32,16 +38,24 @@ __all__ = ["moe_route", "moe_stats_state_bytes", "moe_stats_init", "moe_stats", 
            "moe_prediction_quality", "moe_dispatch_workspace_bytes",
            "moe_dispatch", "moe_expert_ffn_workspace_bytes", "moe_expert_ffn", "moe_combine", "moe_layer_forward",
            "moe_layer_forward_pipelined", "moe_backward_workspace_bytes", "moe_backward", "moe_check_device_error",
+           "moe_gate", "moe_gate_backward", "moe_backward_gated", "moe_layer_norm",
+           "moe_layer_norm_backward_workspace_bytes", "moe_layer_norm_backward", "moe_grad_norm_workspace_bytes",
+           "moe_grad_norm", "moe_clip_grads", "moe_layer_backward",
            "moe_expert_ffn_profiled", "new_check_word", "CHECK_BITS", "moe_dispatch_noalloc",
-           "MoEError", "LIB_PATH", "MOE_F32", "MOE_BF16", "SWIGLU", "GELU", "GEMM_AUTO", "GEMM_GROUPED",
-           "GEMM_DENSE", "GEMM_GROUPED_SMALL"]
+           "MoEError", "LIB_PATH", "MOE_F32", "MOE_BF16", "SWIGLU", "GELU", "SOFTMAX", "SIGMOID", "GROUP_MAX",
+           "GROUP_TOP2", "GEMM_AUTO", "GEMM_GROUPED", "GEMM_DENSE", "GEMM_GROUPED_SMALL"]
 
 MOE_F32, MOE_BF16 = 0, 1
 SWIGLU, GELU = 0, 1
+SOFTMAX, SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
 GEMM_AUTO, GEMM_GROUPED, GEMM_DENSE, GEMM_GROUPED_SMALL = 0, 1, 2, 3
+_SCORE = {"softmax": SOFTMAX, "sigmoid": SIGMOID, SOFTMAX: SOFTMAX, SIGMOID: SIGMOID}
+_GROUP_SCORE = {"max": GROUP_MAX, "top2": GROUP_TOP2, GROUP_MAX: GROUP_MAX, GROUP_TOP2: GROUP_TOP2}
 _ACT = {"swiglu": SWIGLU, "gelu": GELU, SWIGLU: SWIGLU, GELU: GELU}
 # bits of the device-check word (include/moe.h MOE_CHECK_*)
-CHECK_BITS = {"logits": 1, "index": 2, "duplicate": 4, "counts": 8, "replicas": 16, "slots": 32, "rows": 64}
+CHECK_BITS = {"logits": 1, "index": 2, "duplicate": 4, "counts": 8, "replicas": 16, "slots": 32, "rows": 64,
+              "grads": 128}
 _PATH = {"auto": GEMM_AUTO, "grouped": GEMM_GROUPED, "dense": GEMM_DENSE, "grouped_small": GEMM_GROUPED_SMALL,
          GEMM_AUTO: GEMM_AUTO, GEMM_GROUPED: GEMM_GROUPED, GEMM_DENSE: GEMM_DENSE,
          GEMM_GROUPED_SMALL: GEMM_GROUPED_SMALL}
@@ -106,6 +120,46 @@ def _bytes_of(t, need, name):
     return t
 
 
+def _same(t, dev, dtype, shape, name):
+    """A tensor of exactly this device, dtype and shape (None passes)."""
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if t.dtype != dtype or t.device != dev or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+
+
+def _call_on(dev, stream, name, *args):
+    """_call with the stream last: the device's current one, or `stream`; the
+    tensors' device is made current for the call where it is not."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(name, *args, _stream(stream))
+    _call(name, *args, _stream(stream))
+
+
+def _workspace(t, need, dev, stream, name):
+    """A given workspace, checked, or one for this call: memory that goes back to
+    the allocator when the call returns, so a call on another stream than the
+    current one tells the allocator who still uses it."""
+    if t is not None:
+        if _bytes_of(t, need, name).device != dev:
+            raise ValueError(f"{name}: on another device than the call's tensors")
+        return t
+    t = torch.empty(need, dtype=torch.uint8, device=dev)
+    if stream is not None:
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                        torch.cuda.ExternalStream(int(stream), device=dev))
+    return t
+
+
+def _check_ptr(check, dev):
+    _same(check, dev, torch.int32, (1,), "check")
+    return _ptr(check)
+
+
 def new_check_word(device="cuda"):
     """A zeroed device-check word (int32 [1]) for the `check` argument."""
     return torch.zeros(1, dtype=torch.int32, device=device)
@@ -132,6 +186,40 @@ def moe_route(logits: torch.Tensor, k: int, topk_idx=None, topk_w=None, stream=N
     _call("moe_route", _ptr(logits), ctypes.c_int64(T), E, k, _ptr(topk_idx), _ptr(topk_w), _ptr(check),
           _stream(stream))
     return topk_idx, topk_w
+
+
+def moe_gate(logits: torch.Tensor, k: int, score="softmax", bias=None, n_groups: int = 1, keep_groups=None,
+             group_score="max", renorm: bool = True, scale: float = 1.0, topk_idx=None, topk_w=None, stream=None,
+             check=None):
+    """The k experts of each token and their weights (include/moe.h moe_gate): logits
+    [T, E] in float32 or bfloat16, scores by softmax or sigmoid, bias (float32 [E])
+    added for the selection only, the keep_groups best of n_groups groups
+    (group_score "max" or "top2"; keep_groups None: all), weights renormalised over
+    the k or not, times scale."""
+    dt, dev = _dtype_code(logits), logits.device
+    T, E = logits.shape
+    _same(bias, dev, torch.float32, (E,), "bias")
+    idx = _out(topk_idx, (T, k), torch.int32, dev, "topk_idx")
+    w = _out(topk_w, (T, k), torch.float32, dev, "topk_w")
+    _call_on(dev, stream, "moe_gate", _ptr(logits), dt, T, E, k, _SCORE[score], _ptr(bias), n_groups,
+             n_groups if keep_groups is None else keep_groups, _GROUP_SCORE[group_score], 1 if renorm else 0, scale,
+             _ptr(idx), _ptr(w), _check_ptr(check, dev))
+    return idx, w
+
+
+def moe_gate_backward(logits: torch.Tensor, topk_idx: torch.Tensor, d_topk_w: torch.Tensor, score="softmax",
+                      renorm: bool = True, scale: float = 1.0, d_logits=None, stream=None, check=None):
+    """d_logits [T, E] (of the logits' dtype) from the gradient d_topk_w (float32 [T, k])
+    of moe_gate's weights, for the experts topk_idx it chose."""
+    dt, dev = _dtype_code(logits), logits.device
+    T, E = logits.shape
+    k = topk_idx.shape[-1]
+    _same(topk_idx, dev, torch.int32, (T, k), "topk_idx")
+    _same(d_topk_w, dev, torch.float32, (T, k), "d_topk_w")
+    d_logits = _out(d_logits, (T, E), logits.dtype, dev, "d_logits")
+    _call_on(dev, stream, "moe_gate_backward", _ptr(logits), dt, T, E, k, _SCORE[score], 1 if renorm else 0, scale,
+             _ptr(topk_idx), _ptr(d_topk_w), _ptr(d_logits), _check_ptr(check, dev))
+    return d_logits
 
 
 # --------------------------------------------------------------- statistics
@@ -357,11 +445,8 @@ def moe_backward_workspace_bytes(dtype, T: int, k: int, H: int, I: int, E: int, 
     return int(lib().moe_backward_workspace_bytes(code, ctypes.c_int64(T), k, H, I, E, _ACT[act]))
 
 
-def moe_backward(x_perm, y_perm, topk_idx, topk_w, inv_pos, expert_off, w_gate, w_up, w_down, d_out, act="swiglu",
-                 out=None, workspace=None, stream=None):
-    """Gradients of the layer given d_out: dict(d_x, d_logits, d_w_gate, d_w_up, d_w_down).
-    x_perm, inv_pos, expert_off from moe_dispatch; y_perm from moe_expert_ffn; the
-    routing from moe_route."""
+def _backward(name, gate_grad, x_perm, y_perm, topk_idx, topk_w, inv_pos, expert_off, w_gate, w_up, w_down, d_out,
+              act, out, workspace, stream):
     T, k = topk_idx.shape
     M, H = x_perm.shape
     E, I, _ = w_gate.shape
@@ -370,7 +455,7 @@ def moe_backward(x_perm, y_perm, topk_idx, topk_w, inv_pos, expert_off, w_gate, 
         raise ValueError("x_perm and y_perm must be [T*k, H] and d_out [T, H] of the activation dtype")
     o = dict(out or {})
     o["d_x"] = _out(o.get("d_x"), (T, H), x_perm.dtype, dev, "d_x")
-    o["d_logits"] = _out(o.get("d_logits"), (T, E), torch.float32, dev, "d_logits")
+    o[gate_grad] = _out(o.get(gate_grad), (T, E) if gate_grad == "d_logits" else (T, k), torch.float32, dev, gate_grad)
     o["d_w_gate"] = _out(o.get("d_w_gate"), tuple(w_gate.shape), w_gate.dtype, dev, "d_w_gate")
     if w_up is not None:
         o["d_w_up"] = _out(o.get("d_w_up"), tuple(w_up.shape), w_up.dtype, dev, "d_w_up")
@@ -378,18 +463,158 @@ def moe_backward(x_perm, y_perm, topk_idx, topk_w, inv_pos, expert_off, w_gate, 
     need = moe_backward_workspace_bytes(x_perm.dtype, T, k, H, I, E, act)
     workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else \
         _bytes_of(workspace, need, "backward workspace")
-    _call("moe_backward", _ptr(x_perm), _ptr(y_perm), _dtype_code(x_perm), ctypes.c_int64(T), k, H, I, E,
+    _call(name, _ptr(x_perm), _ptr(y_perm), _dtype_code(x_perm), ctypes.c_int64(T), k, H, I, E,
           _ptr(topk_idx), _ptr(topk_w), _ptr(inv_pos), _ptr(expert_off), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
-          _ACT[act], _ptr(d_out), _ptr(o["d_x"]), _ptr(o["d_logits"]), _ptr(o["d_w_gate"]), _ptr(o.get("d_w_up")),
+          _ACT[act], _ptr(d_out), _ptr(o["d_x"]), _ptr(o[gate_grad]), _ptr(o["d_w_gate"]), _ptr(o.get("d_w_up")),
           _ptr(o["d_w_down"]), _ptr(workspace), ctypes.c_size_t(workspace.numel() * workspace.element_size()),
           _stream(stream))
     return o
 
 
+def moe_backward(x_perm, y_perm, topk_idx, topk_w, inv_pos, expert_off, w_gate, w_up, w_down, d_out, act="swiglu",
+                 out=None, workspace=None, stream=None):
+    """Gradients of the layer given d_out: dict(d_x, d_logits, d_w_gate, d_w_up, d_w_down).
+    x_perm, inv_pos, expert_off from moe_dispatch; y_perm from moe_expert_ffn; the
+    routing from moe_route."""
+    return _backward("moe_backward", "d_logits", x_perm, y_perm, topk_idx, topk_w, inv_pos, expert_off, w_gate, w_up,
+                     w_down, d_out, act, out, workspace, stream)
+
+
+def moe_backward_gated(x_perm, y_perm, topk_idx, topk_w, inv_pos, expert_off, w_gate, w_up, w_down, d_out,
+                       act="swiglu", out=None, workspace=None, stream=None):
+    """moe_backward for a routing from moe_gate: d_topk_w (float32 [T, k]), the gradient
+    of the gate's weights, in the place of d_logits (moe_gate_backward takes it on)."""
+    return _backward("moe_backward_gated", "d_topk_w", x_perm, y_perm, topk_idx, topk_w, inv_pos, expert_off, w_gate,
+                     w_up, w_down, d_out, act, out, workspace, stream)
+
+
+# --------------------------------------------------------------- layer norm
+def _norm_vectors(x, weight, bias):
+    """The dtype code of weight and bias (float32 or the rows' dtype, both alike)."""
+    if x.dim() != 2:
+        raise ValueError("layer norm takes rows [T, H]")
+    given = [t for t in (weight, bias) if t is not None]
+    w_dtype = given[0].dtype if given else x.dtype
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        _same(t, x.device, w_dtype, (x.shape[1],), name)
+    if w_dtype != x.dtype and w_dtype != torch.float32:
+        raise TypeError("weight and bias must be float32 or of the rows' dtype")
+    return MOE_F32 if w_dtype == torch.float32 else MOE_BF16
+
+
+def moe_layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, residual=None, y=None, x_sum=None,
+                   stream=None):
+    """(y, x_sum): the layer norm y of the rows of x [T, H], or with `residual` of
+    x_sum = x + residual (None without one).  y and x_sum may be given buffers,
+    x or residual among them."""
+    dt, dev = _dtype_code(x), x.device
+    w_dt = _norm_vectors(x, weight, bias)
+    T, H = x.shape
+    _same(residual, dev, x.dtype, x.shape, "residual")
+    y = _out(y, (T, H), x.dtype, dev, "y")
+    if residual is not None:
+        x_sum = _out(x_sum, (T, H), x.dtype, dev, "x_sum")
+    elif x_sum is not None:
+        raise ValueError("x_sum is written with a residual only")
+    _call_on(dev, stream, "moe_layer_norm", _ptr(x), _ptr(residual), dt, T, H, _ptr(weight), _ptr(bias), w_dt, eps,
+             _ptr(x_sum), _ptr(y))
+    return y, x_sum
+
+
+def moe_layer_norm_backward_workspace_bytes(T: int, H: int) -> int:
+    return int(lib().moe_layer_norm_backward_workspace_bytes(T, H))
+
+
+def moe_layer_norm_backward(d_y: torch.Tensor, x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5,
+                            d_skip=None, out=None, workspace=None, stream=None):
+    """dict(d_x, d_weight, d_bias) of moe_layer_norm, given its input x (x_sum where it
+    summed).  d_weight and d_bias are None where there is no weight or bias (the
+    bias's values are not needed, only whether there is one).  d_skip: the gradient
+    that reaches x past the norm, added to d_x."""
+    dt, dev = _dtype_code(x), x.device
+    w_dt = _norm_vectors(x, weight, bias)
+    T, H = x.shape
+    _same(d_y, dev, x.dtype, x.shape, "d_y")
+    _same(d_skip, dev, x.dtype, x.shape, "d_skip")
+    o = dict(out or {})
+    o["d_x"] = _out(o.get("d_x"), (T, H), x.dtype, dev, "d_x")
+    for key, t in (("d_weight", weight), ("d_bias", bias)):
+        if t is None and o.get(key) is not None:
+            raise ValueError(f"{key}: there is no such parameter")
+        o[key] = None if t is None else _out(o.get(key), (H,), t.dtype, dev, key)
+    nbytes = 0
+    if weight is not None or bias is not None:
+        nbytes = moe_layer_norm_backward_workspace_bytes(T, H)
+        workspace = _workspace(workspace, nbytes, dev, stream, "layer norm workspace")
+    _call_on(dev, stream, "moe_layer_norm_backward", _ptr(d_y), _ptr(x), dt, T, H, _ptr(weight), w_dt, eps,
+             _ptr(d_skip), _ptr(o["d_x"]), _ptr(o["d_weight"]), _ptr(o["d_bias"]), _ptr(workspace) if nbytes else None,
+             nbytes)
+    return o
+
+
+# -------------------------------------------------------- gradient clipping
+def _grad_list(grads, dev, what):
+    """ctypes arrays (pointers, element counts, dtype codes) of a list of tensors."""
+    n = len(grads)
+    ptrs, counts, types = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int * n)()
+    for i, g in enumerate(grads):
+        if not isinstance(g, torch.Tensor):
+            raise TypeError(f"{what}: expected torch tensors")
+        if g.device != dev or not g.is_contiguous():
+            raise ValueError(f"{what}[{i}]: must be contiguous and on {dev}")
+        ptrs[i], counts[i], types[i] = g.data_ptr(), g.numel(), _dtype_code(g)
+    return ptrs, counts, types
+
+
+def _norm_buffers(grads, norm, workspace, stream):
+    if len(grads) == 0 and norm is None:
+        raise ValueError("an empty list of gradients names no device: pass norm")
+    dev = norm.device if norm is not None else grads[0].device
+    if dev.type != "cuda":
+        raise ValueError("tensors passed to the MoE library must live on the GPU")
+    norm = _out(norm, (1,), torch.float32, dev, "norm")
+    need = moe_grad_norm_workspace_bytes()
+    return dev, norm, _workspace(workspace, need, dev, stream, "gradient norm workspace"), need
+
+
+def moe_grad_norm_workspace_bytes() -> int:
+    return int(lib().moe_grad_norm_workspace_bytes())
+
+
+def moe_grad_norm(grads, norm=None, workspace=None, stream=None, check=None):
+    """float32 [1] on the device: the square root of the sum of all squares of a list
+    of float32 or bfloat16 tensors."""
+    dev, norm, workspace, need = _norm_buffers(grads, norm, workspace, stream)
+    ptrs, counts, types = _grad_list(grads, dev, "grads")
+    _call_on(dev, stream, "moe_grad_norm", ptrs, counts, types, len(grads), _ptr(norm), _ptr(workspace), need,
+             _check_ptr(check, dev))
+    return norm
+
+
+def moe_clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, norm=None, workspace=None, stream=None,
+                   check=None):
+    """(norm, out): the global norm of the gradients (before clipping) and the gradients
+    times min(1, max_norm / (norm + eps)), in place unless `out` gives other tensors
+    of the same shapes and dtypes."""
+    dev, norm, workspace, need = _norm_buffers(grads, norm, workspace, stream)
+    ptrs, counts, types = _grad_list(grads, dev, "grads")
+    outs = ptrs
+    if out is not None:
+        if len(out) != len(grads):
+            raise ValueError("out: one tensor for each gradient")
+        for i, (o, g) in enumerate(zip(out, grads)):
+            _same(o, dev, g.dtype, g.shape, f"out[{i}]")
+        outs = _grad_list(out, dev, "out")[0]
+    _call_on(dev, stream, "moe_clip_grads", ptrs, outs, counts, types, len(grads), max_norm, eps, _ptr(norm),
+             _ptr(workspace), need, _check_ptr(check, dev))
+    return norm, list(grads) if out is None else list(out)
+
+
 # ------------------------------------------------------ one layer, composed
 def moe_layer_forward(x, logits, k, w_gate, w_up, w_down, act="swiglu", replica_budget=0, stats_state=None,
                       stats_dims=None, layer=0, it=0, prev_topk_idx=None, path="grouped", bufs=None, stream=None,
-                      planned_replicas=None, check=None, ffn_events=None, copy_rows=False):
+                      planned_replicas=None, check=None, ffn_events=None, copy_rows=False, gate=None, residual=None,
+                      norm=None):
     """route -> stats -> dispatch -> FFN -> combine, all on `stream`.
 
     The dispatch writes the row map and the slot table but copies no rows: the
@@ -408,18 +633,29 @@ def moe_layer_forward(x, logits, k, w_gate, w_up, w_down, act="swiglu", replica_
     workspaces between calls; they are reallocated when the shapes change.
     `check`: the device-check word passed to all five calls.  ffn_events:
     three torch.cuda.Event objects recorded around the two GEMM launches
-    (moe_expert_ffn_profiled)."""
+    (moe_expert_ffn_profiled).
+
+    gate: a dict of moe_gate's options (score, bias, n_groups, ...): moe_gate
+    routes in moe_route's place.  norm: a dict of moe_layer_norm's weight, bias
+    and eps (may be empty): the layer's output is normed, after the sum with
+    `residual` (e.g. x) where that is given; the result then holds `normed` and
+    `x_sum`."""
     T, E = logits.shape
     H = x.shape[1]
     I = w_gate.shape[1]
     dev = x.device
+    if residual is not None and norm is None:
+        raise ValueError("residual: the sum is taken before a norm (pass norm)")
     max_slots = E + replica_budget
     b = bufs if bufs is not None else {}
     key = (T, k, E, H, I, max_slots, x.dtype, str(dev), copy_rows)
     if b.get("_key") != key:
         b.clear()
         b["_key"] = key
-    idx, w = moe_route(logits, k, b.get("idx"), b.get("w"), stream, check)
+    if gate is None:
+        idx, w = moe_route(logits, k, b.get("idx"), b.get("w"), stream, check)
+    else:
+        idx, w = moe_gate(logits, k, topk_idx=b.get("idx"), topk_w=b.get("w"), stream=stream, check=check, **gate)
     b["idx"], b["w"] = idx, w
     res = {"idx": idx, "w": w}
     replicas, counts = None, None
@@ -462,6 +698,51 @@ def moe_layer_forward(x, logits, k, w_gate, w_up, w_down, act="swiglu", replica_
     b["out"] = out
     res.update(d)
     res.update(y_perm=y, out=out)
+    if norm is not None:
+        b["normed"], x_sum = moe_layer_norm(out, residual=residual, y=b.get("normed"),
+                                            x_sum=b.get("x_sum") if residual is not None else None, stream=stream,
+                                            **norm)
+        res.update(normed=b["normed"], x_sum=x_sum)
+        if x_sum is not None:
+            b["x_sum"] = x_sum
+    return res
+
+
+def moe_layer_backward(fwd, logits, w_gate, w_up, w_down, d_out, act="swiglu", gate=None, norm=None, d_x_sum=None,
+                       max_norm=None, eps: float = 1e-6, workspace=None, stream=None, check=None):
+    """The backward pass of moe_layer_forward(copy_rows=True), whose result is `fwd`:
+    norm -> combine, experts and dispatch -> gate.
+
+    d_out is the gradient of fwd["normed"] where the layer had a norm (pass the
+    same `norm` and `gate` dicts), else of fwd["out"]; d_x_sum the gradient that
+    reaches fwd["x_sum"] otherwise (e.g. the next layer's residual).  Returns
+    dict(d_x, d_logits, d_w_gate, d_w_up, d_w_down), with a norm also d_weight,
+    d_bias and, if the forward pass summed a residual, d_residual (d_x does not
+    hold it).  max_norm: the weights' gradients (experts and norm) are clipped in
+    place to that global norm, and the result holds grad_norm."""
+    if fwd.get("x_perm") is None:
+        raise ValueError("the forward pass must keep its rows: moe_layer_forward(copy_rows=True)")
+    res = {}
+    if norm is not None:
+        summed = fwd.get("x_sum")
+        n = moe_layer_norm_backward(d_out, fwd["out"] if summed is None else summed, norm.get("weight"),
+                                    norm.get("bias"), norm.get("eps", 1e-5), d_skip=d_x_sum, stream=stream)
+        d_out = n["d_x"]
+        res.update({key: n[key] for key in ("d_weight", "d_bias") if n[key] is not None})
+        if summed is not None:
+            res["d_residual"] = d_out
+    elif d_x_sum is not None:
+        raise ValueError("d_x_sum: the layer had no norm")
+    run = moe_backward if gate is None else moe_backward_gated
+    res.update(run(fwd["x_perm"], fwd["y_perm"], fwd["idx"], fwd["w"], fwd["inv_pos"], fwd["expert_off"], w_gate, w_up,
+                   w_down, d_out, act, workspace=workspace, stream=stream))
+    if gate is not None:
+        opts = {key: gate[key] for key in ("score", "renorm", "scale") if key in gate}
+        res["d_logits"] = moe_gate_backward(logits, fwd["idx"], res["d_topk_w"], stream=stream, check=check, **opts)
+    if max_norm is not None:
+        names = ("d_w_gate", "d_w_up", "d_w_down", "d_weight", "d_bias")
+        res["grad_norm"], _ = moe_clip_grads([res[key] for key in names if key in res], max_norm, eps, stream=stream,
+                                             check=check)
     return res
 
 

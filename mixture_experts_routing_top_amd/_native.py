@@ -8,6 +8,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_mi35
 _lib = None
 
 _p, _i, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_f = ctypes.c_float
 SIGNATURES = {
     "moe_route": (_i, [_p, _i64, _i, _i, _p, _p, _p, _p]),
     "moe_stats_state_bytes": (_sz, [_i, _i, _i]),
@@ -29,6 +30,16 @@ SIGNATURES = {
     "moe_backward_workspace_bytes": (_sz, [_i, _i64, _i, _i, _i, _i, _i]),
     "moe_backward": (_i, [_p, _p, _i, _i64, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _i, _p, _p, _p, _p, _p, _p,
                           _p, _sz, _p]),
+    "moe_backward_gated": (_i, [_p, _p, _i, _i64, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _i, _p, _p, _p, _p, _p,
+                                _p, _p, _sz, _p]),
+    "moe_gate": (_i, [_p, _i, _i64, _i, _i, _i, _p, _i, _i, _i, _i, _f, _p, _p, _p, _p]),
+    "moe_gate_backward": (_i, [_p, _i, _i64, _i, _i, _i, _i, _f, _p, _p, _p, _p, _p]),
+    "moe_layer_norm": (_i, [_p, _p, _i, _i64, _i, _p, _p, _i, _f, _p, _p, _p]),
+    "moe_layer_norm_backward_workspace_bytes": (_sz, [_i64, _i]),
+    "moe_layer_norm_backward": (_i, [_p, _p, _i, _i64, _i, _p, _i, _f, _p, _p, _p, _p, _p, _sz, _p]),
+    "moe_grad_norm_workspace_bytes": (_sz, []),
+    "moe_grad_norm": (_i, [_p, _p, _p, _i, _p, _p, _sz, _p, _p]),
+    "moe_clip_grads": (_i, [_p, _p, _p, _p, _i, _f, _f, _p, _p, _sz, _p, _p]),
     "moe_check_device_error": (_i, [_p, _p, _p]),
     "moe_status_string": (ctypes.c_char_p, [_i]),
     "moe_last_error": (ctypes.c_char_p, []),

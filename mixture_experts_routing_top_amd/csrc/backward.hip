@@ -47,7 +47,8 @@ __global__ __launch_bounds__(kTok) void gate_backward_kernel(const uint4* __rest
                                                              const float* __restrict__ topk_w,
                                                              const int32_t* __restrict__ inv_pos, int k, int E,
                                                              int chunks, uint4* __restrict__ d_y,
-                                                             float* __restrict__ d_logits) {
+                                                             float* __restrict__ d_logits,
+                                                             float* __restrict__ d_topk_w) {
   __shared__ float part[kTok / 64][moe::kMaxTopK];
   __shared__ float dw[moe::kMaxTopK];
   const int64_t t = blockIdx.x;
@@ -117,6 +118,10 @@ __global__ __launch_bounds__(kTok) void gate_backward_kernel(const uint4* __rest
     dw[tid] = v;
   }
   __syncthreads();
+  if (d_topk_w) {  // the gate's own backward takes dw on to the logits
+    if (tid < k) d_topk_w[t * k + tid] = dw[tid];
+    return;
+  }
   float s = 0.f;
   for (int i = 0; i < k; ++i) s = fmaf(wi[i], dw[i], s);
   for (int e = tid; e < E; e += kTok) {
@@ -273,7 +278,7 @@ template <bool kBf16>
 int run_backward(const void* x_perm, const void* y_perm, int64_t n_tok, int k, int H, int I, int E,
                  const int32_t* topk_idx, const float* topk_w, const int32_t* inv_pos, const int32_t* expert_off,
                  const void* w_gate, const void* w_up, const void* w_down, bool swiglu, const void* d_out,
-                 void* d_x, float* d_logits, void* d_w_gate, void* d_w_up, void* d_w_down, char* ws,
+                 void* d_x, float* d_logits, float* d_topk_w, void* d_w_gate, void* d_w_up, void* d_w_down, char* ws,
                  const BwdLayout& L, hipStream_t s) {
   using namespace moe;
   using T = typename Tr<kBf16>::T;
@@ -310,7 +315,7 @@ int run_backward(const void* x_perm, const void* y_perm, int64_t n_tok, int k, i
   if (n_tok > 0)
     gate_backward_kernel<kBf16><<<static_cast<unsigned>(n_tok), kTok, 0, s>>>(
         static_cast<const uint4*>(d_out), static_cast<const uint4*>(y_perm), M, topk_idx, topk_w, inv_pos, k, E,
-        chunks, reinterpret_cast<uint4*>(dy), d_logits);
+        chunks, reinterpret_cast<uint4*>(dy), d_logits, d_topk_w);
   if (int rc = check("moe_backward gate")) return rc;
 
   // fp32: transposed weights WdT [E, I, H]; WguT [E, H, 2I] = [Wg^T | Wu^T] (or W1^T [E, H, I])
@@ -456,26 +461,28 @@ extern "C" size_t moe_backward_workspace_bytes(moe_dtype dt, int64_t T, int k, i
   return bwd_layout(dt, T, k, H, I, E, act).bytes;
 }
 
-extern "C" int moe_backward(const void* x_perm, const void* y_perm, moe_dtype dt, int64_t T, int k, int H, int I,
+namespace {
+
+int backward(const char* who, const void* x_perm, const void* y_perm, moe_dtype dt, int64_t T, int k, int H, int I,
                             int E, const int32_t* topk_idx, const float* topk_w, const int32_t* inv_pos,
                             const int32_t* expert_off, const void* w_gate, const void* w_up, const void* w_down,
-                            moe_act act, const void* d_out, void* d_x, float* d_logits, void* d_w_gate,
+                            moe_act act, const void* d_out, void* d_x, float* d_logits, float* d_topk_w, void* d_w_gate,
                             void* d_w_up, void* d_w_down, void* workspace, size_t workspace_bytes, void* stream) {
   using namespace moe;
-  if (dt != MOE_F32 && dt != MOE_BF16) return fail(MOE_ERR_INVALID_ARG, "moe_backward: unknown dtype %d", (int)dt);
-  if (act != MOE_SWIGLU && act != MOE_GELU) return fail(MOE_ERR_INVALID_ARG, "moe_backward: unknown activation");
+  if (dt != MOE_F32 && dt != MOE_BF16) return fail(MOE_ERR_INVALID_ARG, "%s: unknown dtype %d", who, (int)dt);
+  if (act != MOE_SWIGLU && act != MOE_GELU) return fail(MOE_ERR_INVALID_ARG, "%s: unknown activation", who);
   if (E < 1 || E > kMaxExperts)
-    return fail(E < 1 ? MOE_ERR_INVALID_ARG : MOE_ERR_UNSUPPORTED, "moe_backward: E=%d outside [1, %d]", E,
+    return fail(E < 1 ? MOE_ERR_INVALID_ARG : MOE_ERR_UNSUPPORTED, "%s: E=%d outside [1, %d]", who, E,
                 kMaxExperts);
-  if (k < 1 || k > E || k > kMaxTopK) return fail(MOE_ERR_INVALID_ARG, "moe_backward: k=%d outside [1, min(E, 8)]", k);
-  if (T < 0 || T * k >= (int64_t(1) << 30)) return fail(MOE_ERR_INVALID_ARG, "moe_backward: T*k must stay below 2^30");
+  if (k < 1 || k > E || k > kMaxTopK) return fail(MOE_ERR_INVALID_ARG, "%s: k=%d outside [1, min(E, 8)]", who, k);
+  if (T < 0 || T * k >= (int64_t(1) << 30)) return fail(MOE_ERR_INVALID_ARG, "%s: T*k must stay below 2^30", who);
   if (H < 64 || I < 64 || H % 64 || I % 64)
-    return fail(MOE_ERR_UNSUPPORTED, "moe_backward: H and I must be positive multiples of 64 (H=%d I=%d)", H, I);
+    return fail(MOE_ERR_UNSUPPORTED, "%s: H and I must be positive multiples of 64 (H=%d I=%d)", who, H, I);
   const int nI = act == MOE_SWIGLU ? 2 * I : I;
   const BwdLayout L = bwd_layout(dt, T, k, H, I, E, act);
   if (static_cast<int64_t>(std::max(H, nI)) * elem_bytes(dt) * 256 >= (int64_t(1) << 31) ||
       L.ld * elem_bytes(dt) * 256 >= (int64_t(1) << 31))
-    return fail(MOE_ERR_UNSUPPORTED, "moe_backward: sizes too large for 32-bit tile offsets");
+    return fail(MOE_ERR_UNSUPPORTED, "%s: sizes too large for 32-bit tile offsets", who);
   {
     // block and tile indices are 32-bit in the kernels: bound every GEMM grid
     // (at most 128 output columns per column tile)
@@ -484,25 +491,49 @@ extern "C" int moe_backward(const void* x_perm, const void* y_perm, moe_dtype dt
     const int64_t rows_grid = static_cast<int64_t>(L.tiles_cap) * max_nt;
     const int64_t wgrad_blocks = static_cast<int64_t>(E) * (ceil_div(wide, 256) * max_nt + 8);
     if (std::max(rows_grid, wgrad_blocks) >= (int64_t(1) << 31) - 256)
-      return fail(MOE_ERR_UNSUPPORTED, "moe_backward: sizes exceed 32-bit grid indexing");
+      return fail(MOE_ERR_UNSUPPORTED, "%s: sizes exceed 32-bit grid indexing", who);
   }
-  if (act == MOE_SWIGLU && !w_up) return fail(MOE_ERR_INVALID_ARG, "moe_backward: SwiGLU needs w_up");
-  if (act == MOE_GELU && (w_up || d_w_up)) return fail(MOE_ERR_INVALID_ARG, "moe_backward: GELU takes no w_up/d_w_up");
+  if (act == MOE_SWIGLU && !w_up) return fail(MOE_ERR_INVALID_ARG, "%s: SwiGLU needs w_up", who);
+  if (act == MOE_GELU && (w_up || d_w_up)) return fail(MOE_ERR_INVALID_ARG, "%s: GELU takes no w_up/d_w_up", who);
   if (!expert_off || !w_gate || !w_down || !d_w_gate || !d_w_down || !workspace || (act == MOE_SWIGLU && !d_w_up))
-    return fail(MOE_ERR_INVALID_ARG, "moe_backward: null pointer");
-  if (T > 0 && (!x_perm || !y_perm || !topk_idx || !topk_w || !inv_pos || !d_out || !d_x || !d_logits))
-    return fail(MOE_ERR_INVALID_ARG, "moe_backward: null pointer");
+    return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (T > 0 && (!x_perm || !y_perm || !topk_idx || !topk_w || !inv_pos || !d_out || !d_x ||
+                !(d_logits || d_topk_w)))
+    return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
   const void* ptrs[] = {x_perm, y_perm, w_gate, w_up, w_down, d_out, d_x, d_w_gate, d_w_up, d_w_down, workspace};
   for (const void* p : ptrs)
-    if (p && !aligned16(p)) return fail(MOE_ERR_INVALID_ARG, "moe_backward: operands must be 16-byte aligned");
+    if (p && !aligned16(p)) return fail(MOE_ERR_INVALID_ARG, "%s: operands must be 16-byte aligned", who);
   if (workspace_bytes < L.bytes)
-    return fail(MOE_ERR_WORKSPACE, "moe_backward: workspace has %zu bytes, needs %zu", workspace_bytes, L.bytes);
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", who, workspace_bytes, L.bytes);
   const hipStream_t s = as_stream(stream);
   char* ws = static_cast<char*>(workspace);
   return dt == MOE_BF16
              ? run_backward<true>(x_perm, y_perm, T, k, H, I, E, topk_idx, topk_w, inv_pos, expert_off, w_gate, w_up,
-                                  w_down, act == MOE_SWIGLU, d_out, d_x, d_logits, d_w_gate, d_w_up, d_w_down, ws, L, s)
+                                  w_down, act == MOE_SWIGLU, d_out, d_x, d_logits, d_topk_w, d_w_gate, d_w_up, d_w_down, ws, L, s)
              : run_backward<false>(x_perm, y_perm, T, k, H, I, E, topk_idx, topk_w, inv_pos, expert_off, w_gate,
-                                   w_up, w_down, act == MOE_SWIGLU, d_out, d_x, d_logits, d_w_gate, d_w_up, d_w_down,
+                                   w_up, w_down, act == MOE_SWIGLU, d_out, d_x, d_logits, d_topk_w, d_w_gate, d_w_up, d_w_down,
                                    ws, L, s);
+}
+
+}  // namespace
+
+extern "C" int moe_backward(const void* x_perm, const void* y_perm, moe_dtype dt, int64_t T, int k, int H, int I,
+                            int E, const int32_t* topk_idx, const float* topk_w, const int32_t* inv_pos,
+                            const int32_t* expert_off, const void* w_gate, const void* w_up, const void* w_down,
+                            moe_act act, const void* d_out, void* d_x, float* d_logits, void* d_w_gate,
+                            void* d_w_up, void* d_w_down, void* workspace, size_t workspace_bytes, void* stream) {
+  return backward("moe_backward", x_perm, y_perm, dt, T, k, H, I, E, topk_idx, topk_w, inv_pos, expert_off, w_gate,
+                  w_up, w_down, act, d_out, d_x, d_logits, nullptr, d_w_gate, d_w_up, d_w_down, workspace,
+                  workspace_bytes, stream);
+}
+
+extern "C" int moe_backward_gated(const void* x_perm, const void* y_perm, moe_dtype dt, int64_t T, int k, int H,
+                                  int I, int E, const int32_t* topk_idx, const float* topk_w, const int32_t* inv_pos,
+                                  const int32_t* expert_off, const void* w_gate, const void* w_up,
+                                  const void* w_down, moe_act act, const void* d_out, void* d_x, float* d_topk_w,
+                                  void* d_w_gate, void* d_w_up, void* d_w_down, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  return backward("moe_backward_gated", x_perm, y_perm, dt, T, k, H, I, E, topk_idx, topk_w, inv_pos, expert_off,
+                  w_gate, w_up, w_down, act, d_out, d_x, nullptr, d_topk_w, d_w_gate, d_w_up, d_w_down, workspace,
+                  workspace_bytes, stream);
 }

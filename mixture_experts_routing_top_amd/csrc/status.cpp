@@ -59,6 +59,7 @@ extern "C" int moe_check_device_error(const int32_t* check, int32_t* bits, void*
       {MOE_CHECK_REPLICAS, "negative replica count or copies beyond max_slots"},
       {MOE_CHECK_SLOTS, "invalid slot table"},
       {MOE_CHECK_ROWS, "inv_pos entry outside [0, M)"},
+      {MOE_CHECK_GRADS, "non-finite gradient norm"},
   };
   char msg[400];
   int n = snprintf(msg, sizeof(msg), "device check 0x%x:", static_cast<unsigned>(word));

@@ -1,0 +1,173 @@
+"""moe_grad_norm and moe_clip_grads against the float64 oracle.
+
+Squares are exact in double and summed there: the norm is off by its rounding to
+float32 (2^-24 of it, 1 % more for double's sums).  A scaled value has the
+factor's rounding and its own: 2 * 2^-24 in float32; in bf16 half a step, 2^-8,
+more."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_routing_top_amd as moe
+from oracle import operators as oo
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -8}
+
+
+def _grads(sizes, seed, scale=0.01, types=(torch.float32, torch.bfloat16)):
+    gen = torch.Generator().manual_seed(seed)
+    return [(scale * torch.randn(n, generator=gen)).to(types[i % len(types)]).cuda() for i, n in enumerate(sizes)]
+
+
+def _f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _assert_clipped(norm, out, before, max_norm, eps=1e-6):
+    ref_norm, ref = oo.clip([_f64(g) for g in before], max_norm, eps)
+    assert abs(float(norm.double()) - ref_norm) <= 1.01 * U * ref_norm + 2.0 ** -149
+    for o, r, g in zip(out, ref, before):
+        assert o.dtype == g.dtype and o.shape == g.shape
+        tol = np.abs(r) * (2.02 * U + HALF[g.dtype]) + 2.0 ** -133
+        assert np.all(np.abs(_f64(o) - r) <= tol)
+
+
+SIZES = [[1], [1, 1, 1], [7, 0, 8, 9], [8191, 8192, 8193], [100_003], [0], [40_000, 3, 0, 12_345, 64, 65_537, 1]]
+
+
+@pytest.mark.parametrize("sizes", SIZES, ids=str)
+@pytest.mark.parametrize("max_norm", [0.5, 1e4, 0.0])
+def test_clip_sizes(sizes, max_norm):
+    for types in ((torch.float32,), (torch.bfloat16,), (torch.float32, torch.bfloat16)):
+        before = _grads(sizes, len(sizes), 1.0, types)
+        norm0 = moe.moe_grad_norm(before)
+        other = [torch.full_like(g, 9.0) for g in before]
+        norm, out = moe.moe_clip_grads(before, max_norm, out=other)
+        assert torch.equal(norm, norm0) and all(a is b for a, b in zip(out, other))
+        _assert_clipped(norm, out, before, max_norm)
+        mine = [g.clone() for g in before]
+        norm, same = moe.moe_clip_grads(mine, max_norm)
+        assert torch.equal(norm, norm0)
+        assert all(a is b and torch.equal(a, c) for a, b, c in zip(same, mine, out))
+
+
+@pytest.mark.parametrize("n", [95, 96, 97, 192, 193, 500])
+def test_clip_long_lists(n):
+    """Lists of more tensors than a launch takes, with empty ones between."""
+    rng = np.random.default_rng(n)
+    before = _grads([int(v) for v in rng.integers(0, 300, n)], n, 1.0)
+    norm, out = moe.moe_clip_grads(before, 1.0, out=[torch.empty_like(g) for g in before])
+    _assert_clipped(norm, out, before, 1.0)
+    # an uneven list: large tensors in the first and in the last launch
+    before[0], before[-1] = _grads([300_000, 700_001], 3, 1.0)
+    norm, out = moe.moe_clip_grads(before, 1.0, out=[torch.empty_like(g) for g in before])
+    _assert_clipped(norm, out, before, 1.0)
+
+
+def test_clip_views_of_a_flat_buffer():
+    """Neighbours in one buffer, each beginning anywhere; clipped in place, with the
+    buffer's ends left alone."""
+    for dtype in (torch.float32, torch.bfloat16):
+        sizes = [1, 31, 1023, 5, 20_011, 2, 64]
+        flat = torch.full((sum(sizes) + 4,), 3.0, dtype=dtype, device="cuda")
+        values = _grads(sizes, 5, 1.0, (dtype,))
+        at, views = 1, []
+        for v in values:
+            views.append(flat[at:at + v.numel()])
+            views[-1].copy_(v)
+            at += v.numel()
+        norm, out = moe.moe_clip_grads(views, 2.0)
+        _assert_clipped(norm, out, values, 2.0)
+        assert flat[0] == 3 and torch.all(flat[at:] == 3)
+
+
+def test_norm_neither_overflows_nor_vanishes():
+    big = torch.full((1000,), 3e38, device="cuda")
+    small = torch.full((1000,), 1e-30, device="cuda")
+    for g in (big, small, big.bfloat16(), small.bfloat16()):
+        ref = math.sqrt(1000.0) * float(g[0].double())
+        got = float(moe.moe_grad_norm([g]).double())
+        assert got == math.inf if ref > 3.4028235e38 else abs(got - ref) <= 1.01 * U * ref
+    # (3e38 sqrt(1000) is past a float; the factor is still the double's)
+    norm, out = moe.moe_clip_grads([big], 1.0, out=[torch.empty_like(big)])
+    assert torch.all(torch.isfinite(out[0])) and abs(float((out[0].double() ** 2).sum()) - 1.0) <= 1e-6
+
+
+def test_nonfinite_gradients_are_flagged_and_follow_the_formula():
+    for bad, at_bad, others in ((math.inf, "nan", 0.0), (math.nan, "nan", math.nan)):
+        g = _grads([50, 60], 1, 1.0, (torch.float32,))
+        g[1][7] = bad
+        check = moe.new_check_word()
+        norm, out = moe.moe_clip_grads(g, 1.0, check=check)
+        assert not math.isfinite(float(norm))
+        with pytest.raises(moe.MoEError, match="gradient norm"):
+            moe.moe_check_device_error(check)
+        assert int(check.item()) == moe.CHECK_BITS["grads"]
+        assert math.isnan(float(out[1][7]))
+        rest = torch.cat([out[0], out[1][:7]])
+        assert torch.all(torch.isnan(rest)) if math.isnan(others) else not torch.any(rest)
+    check = moe.new_check_word()
+    moe.moe_grad_norm(_grads([9], 2), check=check)
+    assert moe.moe_check_device_error(check) == 0
+
+
+def test_clip_is_the_same_bits_again():
+    before = _grads([1_000_003, 17, 2_000_001, 5000], 9)
+    a = moe.moe_clip_grads(before, 1.0, out=[torch.empty_like(g) for g in before])
+    b = moe.moe_clip_grads(before, 1.0, out=[torch.empty_like(g) for g in before])
+    assert torch.equal(a[0], b[0]) and all(torch.equal(x, y) for x, y in zip(a[1], b[1]))
+    _assert_clipped(a[0], a[1], before, 1.0)
+
+
+def test_clip_offsets_beyond_32_bits():
+    n = (1 << 31) + 13
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g[-3:] = torch.tensor([3.0, 0.0, 4.0])
+    norm, _ = moe.moe_clip_grads([g], 0.5)
+    assert float(norm) == 5.0
+    f = 0.5 / (5.0 + 1e-6)
+    assert torch.equal(g[-3:].cpu(), torch.tensor([3 * f, 0, 4 * f]).bfloat16()) and not torch.any(g[:1000])
+    del g
+    torch.cuda.empty_cache()
+
+
+def test_a_tensor_named_twice():
+    g = _grads([100], 3)[0]
+    one, two = float(moe.moe_grad_norm([g]).double()), float(moe.moe_grad_norm([g, g]).double())
+    assert abs(two - one * math.sqrt(2)) <= 3 * U * two
+    with pytest.raises(moe.MoEError, match="overlaps"):
+        moe.moe_clip_grads([g, g], 1.0)
+    with pytest.raises(moe.MoEError, match="overlaps"):
+        moe.moe_clip_grads([g[:60], g[40:]], 1.0)
+    other = torch.empty_like(g)
+    norm, _ = moe.moe_clip_grads([g, g], 1e-3, out=[other, torch.empty_like(g)])   # read twice, written apart
+    assert abs(float(norm.double()) - two) <= U * two
+
+
+def test_clip_empty_lists_and_refusals():
+    norm = torch.full((1,), 5.0, device="cuda")
+    assert float(moe.moe_grad_norm([], norm=norm)) == 0.0
+    norm.fill_(5.0)
+    assert float(moe.moe_clip_grads([], 1.0, norm=norm)[0]) == 0.0
+    g = _grads([64], 1)
+    with pytest.raises(TypeError):
+        moe.moe_grad_norm([g[0].half()])
+    with pytest.raises(TypeError):
+        moe.moe_grad_norm([g[0], None])
+    with pytest.raises(ValueError):
+        moe.moe_grad_norm([g[0].view(8, 8).t()])
+    with pytest.raises(ValueError):
+        moe.moe_clip_grads(g, 1.0, out=[])
+    with pytest.raises(ValueError):
+        moe.moe_clip_grads(g, 1.0, out=[g[0][:63]])
+    with pytest.raises(moe.MoEError):
+        moe.moe_clip_grads(g, -1.0)
+    with pytest.raises(moe.MoEError):
+        moe.moe_clip_grads(g, math.nan)
+    with pytest.raises(ValueError):
+        moe.moe_grad_norm(g, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))

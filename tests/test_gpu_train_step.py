@@ -1,0 +1,198 @@
+"""The operators together, as a training step runs them: gate -> experts ->
+residual sum and norm, and back again to clipped gradients; eager, captured into
+a graph, and on two streams at once."""
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_routing_top_amd as moe
+from oracle import operators as oo
+from _util import REL_FP32_GEMM, REL_BF16
+
+pytestmark = pytest.mark.gpu
+
+GATES = {"softmax": dict(score="softmax", renorm=False, n_groups=4, keep_groups=2, scale=2.0),
+         "sigmoid": dict(score="sigmoid", renorm=True, n_groups=4, keep_groups=2, group_score="top2", scale=1.5)}
+
+
+def _case(kind, dtype, T=150, E=16, H=128, I=192, k=3, seed=0):
+    gen = torch.Generator().manual_seed(seed)
+    rnd = lambda *s, f=1.0: (f * torch.randn(s, generator=gen))  # noqa: E731
+    gate = dict(GATES[kind])
+    if kind == "sigmoid":
+        gate["bias"] = rnd(E, f=0.1).cuda()
+    return dict(x=rnd(T, H).to(dtype).cuda(), logits=rnd(T, E).cuda(), k=k,
+                wts=[rnd(E, I, H, f=H ** -0.5).to(dtype).cuda(), rnd(E, I, H, f=H ** -0.5).to(dtype).cuda(),
+                     rnd(E, H, I, f=I ** -0.5).to(dtype).cuda()],
+                gate=gate, norm=dict(weight=(1 + rnd(H, f=0.1)).cuda(), bias=rnd(H, f=0.1).cuda(), eps=1e-5),
+                d_normed=rnd(T, H, f=0.1).to(dtype).cuda(), d_x_sum=rnd(T, H, f=0.1).to(dtype).cuda())
+
+
+def _step(c, bufs=None, max_norm=0.5, check=None):
+    f = moe.moe_layer_forward(c["x"], c["logits"], c["k"], *c["wts"], gate=c["gate"], norm=c["norm"],
+                              residual=c["x"], copy_rows=True, bufs=bufs, check=check)
+    b = moe.moe_layer_backward(f, c["logits"], *c["wts"], c["d_normed"], gate=c["gate"], norm=c["norm"],
+                               d_x_sum=c["d_x_sum"], max_norm=max_norm, check=check)
+    return f, b
+
+
+def _autograd(c, idx):
+    """The step in float64 by torch, with the experts the gate took."""
+    p = {name: t.double().cpu().requires_grad_() for name, t in
+         (("x", c["x"]), ("lg", c["logits"]), ("wg", c["wts"][0]), ("wu", c["wts"][1]), ("wd", c["wts"][2]),
+          ("nw", c["norm"]["weight"]), ("nb", c["norm"]["bias"]))}
+    s = torch.softmax(p["lg"], 1) if c["gate"]["score"] == "softmax" else torch.sigmoid(p["lg"])
+    w = torch.gather(s, 1, idx)
+    w = c["gate"]["scale"] * (w / w.sum(1, keepdim=True) if c["gate"]["renorm"] else w)
+    out = torch.zeros_like(p["x"])
+    for e in range(p["wg"].shape[0]):
+        t, i = torch.nonzero(idx == e, as_tuple=True)
+        if not len(t):
+            continue
+        xe = p["x"][t]
+        h = torch.nn.functional.silu(xe @ p["wg"][e].T) * (xe @ p["wu"][e].T)
+        out = out.index_add(0, t, w[t, i][:, None] * (h @ p["wd"][e].T))
+    x_sum = out + p["x"].detach()
+    r = x_sum.clone()
+    y = torch.nn.functional.layer_norm(r, (r.shape[1],), p["nw"], p["nb"], c["norm"]["eps"])
+    ((y * c["d_normed"].double().cpu()).sum() + (r * c["d_x_sum"].double().cpu()).sum()).backward()
+    return dict(normed=y, x_sum=x_sum, d_x=p["x"].grad, d_logits=p["lg"].grad, d_w_gate=p["wg"].grad,
+                d_w_up=p["wu"].grad, d_w_down=p["wd"].grad, d_weight=p["nw"].grad, d_bias=p["nb"].grad)
+
+
+def _rel(a, b):
+    a, b = a.detach().double().cpu(), b.detach()
+    return float((a - b).norm() / b.norm())
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_training_step_against_autograd(kind, dtype):
+    c = _case(kind, dtype)
+    check = moe.new_check_word()
+    f, b = _step(c, max_norm=None, check=check)
+    assert moe.moe_check_device_error(check) == 0
+    gate = {**c["gate"], "bias": None if "bias" not in c["gate"] else c["gate"]["bias"].double().cpu().numpy()}
+    idx, w = oo.gate(c["logits"].double().cpu().numpy(), c["k"], **gate)
+    assert np.array_equal(f["idx"].cpu().numpy(), idx)
+    ref = _autograd(c, torch.from_numpy(idx).long())
+    # the layer's own bars: fp32 products 1e-4; bf16 stores several roundings of
+    # 2^-9 rms each along the chain, each bar being 5e-3 for one stored result
+    bar = REL_FP32_GEMM if dtype == torch.float32 else 4 * REL_BF16
+    for key in ("normed", "x_sum"):
+        assert _rel(f[key], ref[key]) <= bar, key
+    for key in ("d_x", "d_logits", "d_w_gate", "d_w_up", "d_w_down", "d_weight", "d_bias"):
+        assert _rel(b[key], ref[key]) <= bar, (key, _rel(b[key], ref[key]))
+    # the same gradients, clipped
+    _, clipped = _step(c, max_norm=0.5)
+    names = ["d_w_gate", "d_w_up", "d_w_down", "d_weight", "d_bias"]
+    norm, scaled = oo.clip([b[n].double().cpu().numpy() for n in names], 0.5)
+    assert norm > 0.5 and abs(float(clipped["grad_norm"].double()) - norm) <= 2.0 ** -23 * norm
+    for n, s in zip(names, scaled):
+        half = 2.0 ** -8 if b[n].dtype == torch.bfloat16 else 0.0
+        assert np.all(np.abs(clipped[n].double().cpu().numpy() - s) <= np.abs(s) * (half + 2.0 ** -22) + 2.0 ** -133)
+    assert torch.equal(clipped["d_x"], b["d_x"]) and torch.equal(clipped["d_logits"], b["d_logits"])
+
+
+def test_plain_layer_is_untouched_by_the_options():
+    c = _case("softmax", torch.float32)
+    plain = moe.moe_layer_forward(c["x"], c["logits"], c["k"], *c["wts"], copy_rows=True)
+    normed = moe.moe_layer_forward(c["x"], c["logits"], c["k"], *c["wts"], copy_rows=True, norm=c["norm"])
+    same = moe.moe_layer_forward(c["x"], c["logits"], c["k"], *c["wts"], copy_rows=True, gate={})
+    assert torch.equal(plain["out"], normed["out"]) and torch.equal(plain["idx"], same["idx"])
+    assert "normed" not in plain and normed["x_sum"] is None
+    y, _ = moe.moe_layer_norm(plain["out"], **c["norm"])
+    assert torch.equal(normed["normed"], y)
+    # without a gate or norm the backward pass is moe_backward's
+    a = moe.moe_layer_backward(plain, c["logits"], *c["wts"], c["d_normed"])
+    b = moe.moe_backward(plain["x_perm"], plain["y_perm"], plain["idx"], plain["w"], plain["inv_pos"],
+                         plain["expert_off"], *c["wts"], c["d_normed"])
+    assert all(torch.equal(a[key], b[key]) for key in b)
+    # a renormalised softmax gate gives moe_backward's logit gradient (both float32)
+    g = moe.moe_layer_backward(plain, c["logits"], *c["wts"], c["d_normed"], gate={})
+    assert _rel(g["d_logits"], b["d_logits"].double().cpu()) <= 1e-5
+    with pytest.raises(ValueError):
+        moe.moe_layer_forward(c["x"], c["logits"], c["k"], *c["wts"], residual=c["x"])
+    with pytest.raises(ValueError):
+        moe.moe_layer_backward({**plain, "x_perm": None}, c["logits"], *c["wts"], c["d_normed"])
+    with pytest.raises(ValueError):
+        moe.moe_layer_backward(plain, c["logits"], *c["wts"], c["d_normed"], d_x_sum=c["d_x_sum"])
+
+
+def _kept(f, b):
+    keys_f = ("idx", "w", "out", "normed", "x_sum")
+    return {**{k: f[k].clone() for k in keys_f}, **{k: v.clone() for k, v in b.items()}}
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_training_step_captured_and_replayed(kind):
+    c = _case(kind, torch.bfloat16)
+    bufs = {}
+    _step(c, bufs)
+    eager = _kept(*_step(c, bufs))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _step(c, bufs)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        f, b = _step(c, bufs)
+    for rep in range(3):
+        for t in (f["normed"], f["x_sum"], b["d_logits"], b["d_weight"], b["grad_norm"]):
+            t.fill_(-7.0)
+        junk = torch.randn(4096, device="cuda")
+        assert float(moe.moe_grad_norm([junk])) > 0 and float(moe.moe_layer_norm(junk.view(16, 256))[0].abs().sum()) > 0
+        graph.replay()
+        torch.cuda.synchronize()
+        got = _kept(f, b)
+        for key, v in eager.items():
+            assert torch.equal(got[key], v), (rep, key)
+    # new values in the captured inputs: the replay follows them
+    other = _case(kind, torch.bfloat16, seed=1)
+    for key in ("x", "logits", "d_normed", "d_x_sum"):
+        c[key].copy_(other[key])
+    graph.replay()
+    torch.cuda.synchronize()
+    got, want = _kept(f, b), _kept(*_step(c))
+    for key, v in want.items():
+        assert torch.equal(got[key], v), key
+
+
+def test_calls_on_two_streams_at_once():
+    cases = [_case("sigmoid", torch.float32, T=900, seed=s) for s in (1, 2)]
+    ref = [_kept(*_step(c)) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(3):
+        got = [None, None]
+        for i, (c, s) in enumerate(zip(cases, streams)):
+            with torch.cuda.stream(s):
+                got[i] = _step(c)
+        torch.cuda.synchronize()
+        for g, r in zip(got, ref):
+            kept = _kept(*g)
+            assert all(torch.equal(kept[key], r[key]) for key in r)
+
+
+def test_a_stream_argument_other_than_the_current_one():
+    """The call's own workspaces stay reserved until that stream is done with them."""
+    gen = torch.Generator().manual_seed(3)
+    x, dy = (torch.randn((3000, 2048), generator=gen).cuda() for _ in range(2))
+    w = torch.randn(2048, generator=gen).cuda()
+    ref = moe.moe_layer_norm_backward(dy, x, w, w)
+    grads = [torch.randn(500_000, generator=gen).cuda() for _ in range(3)]
+    ref_norm = moe.moe_grad_norm(grads)
+    need = moe.moe_layer_norm_backward_workspace_bytes(3000, 2048)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(4):
+        d = moe.moe_layer_norm_backward(dy, x, w, w, stream=s)
+        norm = moe.moe_grad_norm(grads, stream=s)
+        junk = [torch.full((need // 4,), 9.0, device="cuda") for _ in range(3)]    # on the current stream, at once
+        s.synchronize()
+        assert torch.equal(d["d_weight"], ref["d_weight"]) and torch.equal(d["d_bias"], ref["d_bias"])
+        assert torch.equal(norm, ref_norm)
+        del junk
