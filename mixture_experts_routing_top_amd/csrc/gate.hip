@@ -12,6 +12,14 @@
 //
 // A masked expert (logit NaN or <= kMaskBelow) has score 0 and comes after
 // every other expert of the kept groups, in index order.
+//
+// Two steps.  gate_kernel gives a token to 16 lanes and selects in float32 on
+// 32-bit keys, 24 bits of the value in fixed point and 8 of the index, knowing
+// a bound on its own error: a token whose order two candidates closer than the
+// bound could turn (not if they are equal in logit and bias: then the index
+// decides, in double as well) is done again by the whole wave in double
+// (gate_token).  Doing every token in double costs ten times the time.
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 
@@ -191,13 +199,301 @@ __device__ void gate_token(const GateArgs& p, int64_t t, int lane, double* value
   }
 }
 
+// ------------------------------------------------------------ 16 lanes a token
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, __int_as_float(dpp_partner<1>(__float_as_int(v))));
+  v = fmaxf(v, __int_as_float(dpp_partner<2>(__float_as_int(v))));
+  v = fmaxf(v, __int_as_float(dpp_partner<4>(__float_as_int(v))));
+  return fmaxf(v, __int_as_float(dpp_partner<8>(__float_as_int(v))));
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  v = max(v, static_cast<uint32_t>(dpp_partner<1>(v)));
+  v = max(v, static_cast<uint32_t>(dpp_partner<2>(v)));
+  v = max(v, static_cast<uint32_t>(dpp_partner<4>(v)));
+  return max(v, static_cast<uint32_t>(dpp_partner<8>(v)));
+}
+template <int OFF>
+__device__ __forceinline__ double partner64(double v) {
+  return __hiloint2double(dpp_partner<OFF>(__double2hiint(v)), dpp_partner<OFF>(__double2loint(v)));
+}
+__device__ __forceinline__ double row_sum(double v) {
+  v += partner64<1>(v);
+  v += partner64<2>(v);
+  v += partner64<4>(v);
+  return v + partner64<8>(v);
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += __int_as_float(dpp_partner<1>(__float_as_int(v)));
+  v += __int_as_float(dpp_partner<2>(__float_as_int(v)));
+  v += __int_as_float(dpp_partner<4>(__float_as_int(v)));
+  return v + __int_as_float(dpp_partner<8>(__float_as_int(v)));
+}
+// the value of the lane one up in the 16 (lane 15: its own)
+__device__ __forceinline__ int next_lane(int v) { return __builtin_amdgcn_update_dpp(v, v, 0x101, 0xf, 0xf, false); }
+// the value of the lane N down, around the 16
+template <int N>
+__device__ __forceinline__ float rotated(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x120 + N, 0xf, 0xf, false));
+}
+
+// Groups ahead of this lane's: `rep` is the group's score in the first lane of
+// each group and NaN, ahead of nothing, in the others; bit N of `ties` is set
+// where the lane N down belongs to a group before this lane's.
+template <int N>
+__device__ __forceinline__ void count_ahead(float rep, float score, uint32_t ties, int& rank) {
+  if constexpr (N < 16) {
+    const float o = rotated<N>(rep);
+    rank += o > score || (o == score && ((ties >> N) & 1u));
+    count_ahead<N + 1>(rep, score, ties, rank);
+  }
+}
+
+// the k-th largest key and those after it: with unsigned wrap-around the keys
+// below `best` lie above those at or over it, so one subtraction and a maximum
+// give the next one and nothing has to be struck out
+template <int V>
+__device__ __forceinline__ uint32_t next_key(const uint32_t (&key)[V], uint32_t best) {
+  uint32_t d = key[0] - best;
+#pragma unroll
+  for (int j = 1; j < V; ++j) d = max(d, key[j] - best);
+  return best + row_max(d);
+}
+
+enum { kByLogit, kSigmoid, kSoftmax };  // what the selection compares
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTop = 16777200.f;     // the largest fixed-point value, below 2^24
+
+// Lane i of a token's 16 holds `per` consecutive experts (at most V) of one group:
+// groups begin at multiples of `lanes` lanes.
+template <bool kBf16, int V, int kBy>
+__global__ __launch_bounds__(256) void gate_kernel(GateArgs p, int lanes, int per) {
+  __shared__ double value[4][moe::kMaxExperts];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l16 = lane & 15;
+  const bool grouped = p.keep < p.n_groups;
+  const int group = l16 / lanes;                      // == p.n_groups or more: an idle lane
+  const int inside = (l16 % lanes) * per;
+  const int e0 = group * p.group_size + inside;
+  const int n = group < p.n_groups ? min(per, p.group_size - inside) : 0;   // this lane's experts
+  const int64_t total = p.T * p.E;
+
+  // the fixed-point scale, and the bound on the error of two values' difference
+  float b[V];
+  float scale = 0.f, offset = 0.f, near = 0.f, group_near = 0.f;
+  if constexpr (kBy != kByLogit) {
+    float lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      b[j] = j < n && p.bias ? p.bias[e0 + j] : 0.f;
+      if (!(fabsf(b[j]) <= 1e30f)) hi = INFINITY;     // left to the doubles
+      if (j < n) { lo = fminf(lo, b[j]); hi = fmaxf(hi, b[j]); }
+    }
+    lo = -row_max(-lo);
+    hi = row_max(hi);
+    const float range = 1.f + (hi - lo), big = fmaxf(fabsf(lo), fabsf(hi));
+    // s: exp2's argument, exp2, the sum and the reciprocal, 6 u in all (u = 2^-24);
+    // a softmax's sum of up to 32 values in sequence and 4 steps: 36 u more.
+    // s + b rounds once more.  In the key: half a unit of fma, one of the cut.
+    const float err = (kBy == kSigmoid ? 7.f : 43.f) + big;
+    scale = kTop / range;
+    offset = 2.f - lo * scale;
+    near = 2.f * (err / range + 2.f);
+    group_near = (4.f * err + 4.f * (1.f + big)) * 0x1p-24f;
+    if (!(hi < INFINITY)) near = group_near = INFINITY;
+  } else {
+    scale = kTop / 32.f;        // logits down to 32 below the largest: monotone, so only
+    offset = 2.f + kTop;        // equal keys of unequal logits are in doubt
+  }
+
+  for (int64_t base = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * 4; base < p.T;
+       base += static_cast<int64_t>(gridDim.x) * 16) {
+    const int64_t t = base + (lane >> 4);
+    const bool active = t < p.T;
+    const int64_t row = (active ? t : 0) * p.E;
+    float l[V];
+    bool bad = false;
+    float m = -INFINITY;
+    {
+      const int64_t at = row + e0;
+      if (n > 0 && at + V <= total) {
+        if constexpr (kBf16) {
+          uint16_t raw[V];
+          __builtin_memcpy(raw, static_cast<const uint16_t*>(p.logits) + at, sizeof(raw));
+#pragma unroll
+          for (int j = 0; j < V; ++j) l[j] = bf16_bits_to_f32(raw[j]);
+        } else {
+          __builtin_memcpy(l, static_cast<const float*>(p.logits) + at, sizeof(l));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) l[j] = j < n ? load_logit<kBf16>(p.logits, at + j) : -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (j >= n) l[j] = -INFINITY;
+      bad |= l[j] != l[j] || l[j] == INFINITY;
+      l[j] = is_live(l[j]) ? fminf(l[j], FLT_MAX) : -INFINITY;
+      m = fmaxf(m, l[j]);
+    }
+    if (p.check) raise_check(p.check, bad && active, MOE_CHECK_LOGITS);
+    m = row_max(m);
+    if (m == -INFINITY) m = 0.f;   // nothing unmasked
+
+    float v[V];
+    double sum64 = 1.0;
+    if constexpr (kBy == kByLogit) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = l[j];
+    } else if constexpr (kBy == kSigmoid) {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        v[j] = l[j] > -INFINITY ? __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l[j] * -kLog2e)) + b[j] : -INFINITY;
+    } else {
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        v[j] = __builtin_amdgcn_exp2f((l[j] - m) * kLog2e);
+        sum += v[j];
+      }
+      sum = row_sum(sum);
+      const float inv = sum > 0.f ? __builtin_amdgcn_rcpf(sum) : 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = l[j] > -INFINITY ? fmaf(v[j], inv, b[j]) : -INFINITY;
+    }
+    if (p.softmax && !p.renorm) {   // the weights' denominator
+      sum64 = 0.0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (j < n && l[j] > -INFINITY) sum64 += exp(static_cast<double>(l[j]) - static_cast<double>(m));
+        __builtin_amdgcn_sched_barrier(0);   // one exponential's registers at a time
+      }
+      sum64 = row_sum(sum64);
+    }
+
+    uint32_t key[V];   // (value + 2) << 8 | 255 - index; 1 in the value's place: masked; 0: not to be taken
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float x = kBy == kByLogit ? v[j] - m : v[j];
+      const uint32_t q = l[j] > -INFINITY ? static_cast<uint32_t>(fminf(fmaxf(fmaf(x, scale, offset), 2.f), 16777215.f)) : 1u;
+      key[j] = j < n ? (q << 8) + static_cast<uint32_t>(255 - e0 - j) : 0u;
+    }
+
+    bool doubt = false;
+    if (grouped) {
+      float m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        m2 = fmaxf(m2, fminf(m1, v[j]));
+        m1 = fmaxf(m1, v[j]);
+      }
+      auto join = [&](float o1, float o2) {
+        m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+        m1 = fmaxf(m1, o1);
+      };
+#define MOE_JOIN(OFF)                                                            \
+  if (lanes > OFF)                                                               \
+    join(__int_as_float(dpp_partner<OFF>(__float_as_int(m1))), __int_as_float(dpp_partner<OFF>(__float_as_int(m2))));
+      MOE_JOIN(1) MOE_JOIN(2) MOE_JOIN(4)
+#undef MOE_JOIN
+      const float score = p.top2 && m2 > -INFINITY ? m1 + m2 : m1;
+      const bool rep = l16 % lanes == 0 && group < p.n_groups;
+      int rank = 0;
+      count_ahead<1>(rep ? score : NAN, score, (2u << l16) - (2u << (l16 % lanes)), rank);
+      const bool kept = rank < p.keep;
+      if constexpr (kBy != kByLogit) {
+        // the last group kept against the first one left out
+        const float low = -row_max(rep && kept ? -score : -INFINITY);
+        const float high = row_max(rep && !kept ? score : -INFINITY);
+        doubt = high > -INFINITY && !(low - high > group_near);
+      }
+      if (!kept)
+#pragma unroll
+        for (int j = 0; j < V; ++j) key[j] = 0u;
+    }
+
+    // lane i takes the i-th key, lane k the best one left
+    uint32_t best = 0, mine = 0;
+#pragma unroll
+    for (int i = 0; i <= moe::kMaxTopK; ++i)
+      if (i <= p.k) {
+        best = next_key<V>(key, best);
+        if (l16 == i) mine = best;
+      }
+    const int e = min(255 - static_cast<int>(mine & 255u), p.E - 1);
+    const bool some = l16 <= p.k && mine >= 512u;      // an unmasked expert
+    float lk = some ? load_logit<kBf16>(p.logits, row + e) : -INFINITY;
+    lk = fminf(lk, FLT_MAX);
+    const uint32_t q = mine >> 8, q_next = static_cast<uint32_t>(next_lane(static_cast<int>(mine))) >> 8;
+    const float l_next = __int_as_float(next_lane(__float_as_int(lk)));
+    bool same = lk == l_next;
+    float bk = 0.f;
+    if constexpr (kBy != kByLogit) {
+      if (p.bias && some) bk = p.bias[e];
+      same = same && bk == __int_as_float(next_lane(__float_as_int(bk)));
+    }
+    doubt |= some && l16 < p.k && q_next >= 2u && static_cast<float>(q - q_next) <= near && !same;
+    const uint64_t doubts = __ballot(doubt && active);
+    const bool redo = (doubts >> (lane & 48)) & 0xffffu;
+
+    // weights in double, rounded once
+    const bool on = some && l16 < p.k;
+    double w;
+    if (p.softmax) {
+      const double top = p.renorm ? static_cast<double>(row_max(on ? lk : -INFINITY)) : static_cast<double>(m);
+      w = on ? exp(static_cast<double>(lk) - top) : 0.0;
+    } else {
+      // see gate_token
+      const double top = p.renorm ? fmin(static_cast<double>(row_max(on ? lk : -INFINITY)), 0.0) : 0.0;
+      const double x = lk;
+      w = !on ? 0.0 : x > 0.0 ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / (1.0 + exp(x));
+    }
+    const double sum = p.renorm ? row_sum(w) : sum64;
+    if (active && !redo && l16 < p.k) {
+      p.idx[t * p.k + l16] = e;
+      p.w[t * p.k + l16] = static_cast<float>(sum > 0.0 ? p.scale * (w / sum) : 0.0);
+    }
+    if (doubts)
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i)
+        if ((doubts >> (16 * i)) & 0xffffu) gate_token<kBf16>(p, base + i, lane, value[wave], true);
+  }
+}
+
+// One wave a token, in double throughout: more groups than 16 lanes hold.
 template <bool kBf16>
-__global__ __launch_bounds__(256) void gate_kernel(GateArgs p) {
+__global__ __launch_bounds__(256) void gate_wave_kernel(GateArgs p) {
   __shared__ double value[4][moe::kMaxExperts];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave;
   if (t >= p.T) return;
   gate_token<kBf16>(p, t, lane, value[wave], true);
+}
+
+template <bool kBf16, int kBy>
+void launch_slots(const GateArgs& p, hipStream_t s) {
+  int lanes = 16;
+  if (p.keep < p.n_groups)
+    while (16 / lanes < p.n_groups) lanes /= 2;
+  GateArgs q = p;
+  if (p.keep == p.n_groups) { q.n_groups = q.keep = 1; q.group_size = p.E; }
+  const int per = static_cast<int>(moe::ceil_div(q.group_size, lanes));
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(2048, moe::ceil_div(p.T, 16)));
+  if (per <= 2) gate_kernel<kBf16, 2, kBy><<<blocks, 256, 0, s>>>(q, lanes, per);
+  else if (per <= 4) gate_kernel<kBf16, 4, kBy><<<blocks, 256, 0, s>>>(q, lanes, per);
+  else if (per <= 8) gate_kernel<kBf16, 8, kBy><<<blocks, 256, 0, s>>>(q, lanes, per);
+  else if (per <= 12) gate_kernel<kBf16, 12, kBy><<<blocks, 256, 0, s>>>(q, lanes, per);
+  else if (per <= 16) gate_kernel<kBf16, 16, kBy><<<blocks, 256, 0, s>>>(q, lanes, per);
+  else gate_kernel<kBf16, 32, kBy><<<blocks, 256, 0, s>>>(q, lanes, per);
+}
+
+template <bool kBf16>
+void launch_gate(const GateArgs& p, hipStream_t s) {
+  if (p.keep < p.n_groups && p.n_groups > 16)
+    gate_wave_kernel<kBf16><<<static_cast<unsigned>(moe::ceil_div(p.T, 4)), 256, 0, s>>>(p);
+  else if (!p.bias && !(p.top2 && p.keep < p.n_groups)) launch_slots<kBf16, kByLogit>(p, s);
+  else if (p.softmax) launch_slots<kBf16, kSoftmax>(p, s);
+  else launch_slots<kBf16, kSigmoid>(p, s);
 }
 
 // ------------------------------------------------------------------ backward
@@ -342,9 +638,8 @@ extern "C" int moe_gate(const void* logits, moe_dtype dt, int64_t T, int E, int 
   if (!logits || !topk_idx || !topk_w) return fail(MOE_ERR_INVALID_ARG, "moe_gate: null pointer");
   GateArgs p{logits, bias, T, E, k, n_groups, keep_groups, size, group_score == MOE_GROUP_TOP2,
              score == MOE_SOFTMAX, renorm != 0, scale, topk_idx, topk_w, check};
-  const unsigned blocks = static_cast<unsigned>(ceil_div(T, 4));
-  if (dt == MOE_BF16) gate_kernel<true><<<blocks, 256, 0, as_stream(stream)>>>(p);
-  else gate_kernel<false><<<blocks, 256, 0, as_stream(stream)>>>(p);
+  if (dt == MOE_BF16) launch_gate<true>(p, as_stream(stream));
+  else launch_gate<false>(p, as_stream(stream));
   return hip_status(hipGetLastError(), "moe_gate launch");
 }
 
