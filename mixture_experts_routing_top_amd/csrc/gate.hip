@@ -24,6 +24,7 @@
 #include <cmath>
 
 #include "common.h"
+#include "rows.h"
 
 namespace {
 
@@ -57,21 +58,43 @@ __device__ __forceinline__ bool ahead(double v1, int i1, double v2, int i2) {
   return v1 > v2 || (v1 == v2 && i1 < i2);
 }
 
-template <typename V>
-__device__ __forceinline__ V wave_max(V v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    const V o = __shfl_xor(v, off);
-    v = o > v ? o : v;
-  }
-  return v;
+template <int OFF>
+__device__ __forceinline__ double partner64(double v) {
+  return __hiloint2double(dpp_partner<OFF>(__double2hiint(v)), dpp_partner<OFF>(__double2loint(v)));
 }
-
-template <typename V>
-__device__ __forceinline__ V wave_sum(V v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
-  return v;
+__device__ __forceinline__ double lane64(double v, int lane) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), lane),
+                          __builtin_amdgcn_readlane(__double2loint(v), lane));
+}
+__device__ __forceinline__ double row_max(double v) {
+  v = fmax(v, partner64<1>(v));
+  v = fmax(v, partner64<2>(v));
+  v = fmax(v, partner64<4>(v));
+  return fmax(v, partner64<8>(v));
+}
+__device__ __forceinline__ double row_sum(double v) {
+  v += partner64<1>(v);
+  v += partner64<2>(v);
+  v += partner64<4>(v);
+  return v + partner64<8>(v);
+}
+__device__ __forceinline__ double wave_max(double v) {
+  v = row_max(v);
+  return fmax(fmax(lane64(v, 0), lane64(v, 16)), fmax(lane64(v, 32), lane64(v, 48)));
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v = row_sum(v);
+  return (lane64(v, 0) + lane64(v, 16)) + (lane64(v, 32) + lane64(v, 48));
+}
+// the smallest of some lanes' values
+__device__ __forceinline__ int least_of(uint64_t lanes, int v) {
+  int least = INT32_MAX;
+  while (lanes) {
+    const int lane = __ffsll(static_cast<unsigned long long>(lanes)) - 1;
+    least = min(least, __builtin_amdgcn_readlane(v, lane));
+    lanes &= lanes - 1;
+  }
+  return least;
 }
 
 // LDS written by some lanes of a wave and read by others of the same wave
@@ -82,8 +105,8 @@ __device__ __forceinline__ void wave_lds_fence() {
 
 // One token by one wave: lane holds experts lane, lane + 64, ...  `value` is E
 // doubles of LDS of this wave.  Every lane of the wave calls it with the same t.
-template <bool kBf16>
-__device__ void gate_token(const GateArgs& p, int64_t t, int lane, double* value, bool write) {
+template <bool kBf16, typename Args>
+__device__ __forceinline__ void gate_token(const Args& p, int64_t t, int lane, double* value) {
   const int64_t row = t * p.E;
   float l[4];
   double key[4];
@@ -99,14 +122,14 @@ __device__ void gate_token(const GateArgs& p, int64_t t, int lane, double* value
     l[j] = live[j] ? fminf(l[j], FLT_MAX) : -INFINITY;
     m = fmaxf(m, l[j]);
   }
-  if (p.check) raise_check(p.check, bad && write, MOE_CHECK_LOGITS);
+  if (p.check) raise_check(p.check, bad, MOE_CHECK_LOGITS);
 
   // scores, where the selection or the weights need all of them
   const bool two = p.top2 && p.keep < p.n_groups;
   double s[4] = {0.0, 0.0, 0.0, 0.0};
   double total = 1.0;
   if (p.softmax && (!p.renorm || p.bias || two)) {
-    m = wave_max(m);
+    m = static_cast<float>(wave_max(static_cast<double>(m)));
     total = 0.0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -144,7 +167,7 @@ __device__ void gate_token(const GateArgs& p, int64_t t, int lane, double* value
     const double score = two && second > -INFINITY ? best + second : best;
     int rank = 0;
     for (int g = 0; g < p.n_groups; ++g) {
-      const double o = __shfl(score, g);
+      const double o = lane64(score, g);
       rank += g != lane && ahead(o, g, score, lane);
     }
     const uint64_t kept = __ballot(lane < p.n_groups && rank < p.keep);
@@ -159,17 +182,12 @@ __device__ void gate_token(const GateArgs& p, int64_t t, int lane, double* value
   // k rounds of an arg-max over the wave; lane i keeps the i-th expert
   int mine = 0;
   for (int i = 0; i < p.k; ++i) {
-    double bv = -INFINITY;
-    int bi = INT32_MAX;
+    double bv = key[0];
+    int bi = lane;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 1; j < 4; ++j)
       if (key[j] > bv) { bv = key[j]; bi = lane + 64 * j; }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      const double ov = __shfl_xor(bv, off);
-      const int oi = __shfl_xor(bi, off);
-      if (ahead(ov, oi, bv, bi)) { bv = ov; bi = oi; }
-    }
+    bi = least_of(__ballot(bv == wave_max(bv)), bi);
     if (lane == i) mine = bi;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -193,34 +211,36 @@ __device__ void gate_token(const GateArgs& p, int64_t t, int lane, double* value
     v = !on ? 0.0 : x > 0.0 ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / (1.0 + exp(x));
   }
   const double sum = p.renorm ? wave_sum(v) : total;
-  if (write && lane < p.k) {
+  if (lane < p.k) {
     p.idx[t * p.k + lane] = mine;
     p.w[t * p.k + lane] = static_cast<float>(sum > 0.0 ? p.scale * (v / sum) : 0.0);
   }
 }
 
+// gate_token called, not inlined, from a loop that few tokens leave: its double
+// constants would otherwise be kept in that loop's registers.  The arguments are
+// read from the kernel's own (its first parameter), so nothing is copied for it.
+using KernelArgs = const __attribute__((address_space(4))) GateArgs;
+template <bool kBf16>
+__device__ __noinline__ void gate_token_call(KernelArgs* p, int64_t t, double* value) {
+  gate_token<kBf16>(*p, t, threadIdx.x & 63, value);
+}
+
 // ------------------------------------------------------------ 16 lanes a token
+// (no NaN reaches it: the middle of two values and infinity is the larger one,
+// without fmaxf's instruction more that quiets a signalling NaN)
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
 __device__ __forceinline__ float row_max(float v) {
-  v = fmaxf(v, __int_as_float(dpp_partner<1>(__float_as_int(v))));
-  v = fmaxf(v, __int_as_float(dpp_partner<2>(__float_as_int(v))));
-  v = fmaxf(v, __int_as_float(dpp_partner<4>(__float_as_int(v))));
-  return fmaxf(v, __int_as_float(dpp_partner<8>(__float_as_int(v))));
+  v = larger(v, __int_as_float(dpp_partner<1>(__float_as_int(v))));
+  v = larger(v, __int_as_float(dpp_partner<2>(__float_as_int(v))));
+  v = larger(v, __int_as_float(dpp_partner<4>(__float_as_int(v))));
+  return larger(v, __int_as_float(dpp_partner<8>(__float_as_int(v))));
 }
 __device__ __forceinline__ uint32_t row_max(uint32_t v) {
   v = max(v, static_cast<uint32_t>(dpp_partner<1>(v)));
   v = max(v, static_cast<uint32_t>(dpp_partner<2>(v)));
   v = max(v, static_cast<uint32_t>(dpp_partner<4>(v)));
   return max(v, static_cast<uint32_t>(dpp_partner<8>(v)));
-}
-template <int OFF>
-__device__ __forceinline__ double partner64(double v) {
-  return __hiloint2double(dpp_partner<OFF>(__double2hiint(v)), dpp_partner<OFF>(__double2loint(v)));
-}
-__device__ __forceinline__ double row_sum(double v) {
-  v += partner64<1>(v);
-  v += partner64<2>(v);
-  v += partner64<4>(v);
-  return v + partner64<8>(v);
 }
 __device__ __forceinline__ float row_sum(float v) {
   v += __int_as_float(dpp_partner<1>(__float_as_int(v)));
@@ -236,21 +256,20 @@ __device__ __forceinline__ float rotated(float v) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x120 + N, 0xf, 0xf, false));
 }
 
-// Groups ahead of this lane's: `rep` is the group's score in the first lane of
-// each group and NaN, ahead of nothing, in the others; bit N of `ties` is set
-// where the lane N down belongs to a group before this lane's.
-template <int N>
-__device__ __forceinline__ void count_ahead(float rep, float score, uint32_t ties, int& rank) {
-  if constexpr (N < 16) {
-    const float o = rotated<N>(rep);
-    rank += o > score || (o == score && ((ties >> N) & 1u));
-    count_ahead<N + 1>(rep, score, ties, rank);
+// Groups ahead of this lane's, the groups being kLanes lanes each: `rep` is the
+// group's score in its lanes and NaN, ahead of nothing, in lanes without a group.
+template <int kLanes, int N = kLanes>
+__device__ __forceinline__ int count_ahead(float rep, float score, int l16) {
+  if constexpr (N >= 16) return 0;
+  else {
+    const float o = rotated<N>(rep);   // of the group N / kLanes before, around the 16
+    return (o > score || (o == score && l16 >= N)) + count_ahead<kLanes, N + kLanes>(rep, score, l16);
   }
 }
 
-// the k-th largest key and those after it: with unsigned wrap-around the keys
-// below `best` lie above those at or over it, so one subtraction and a maximum
-// give the next one and nothing has to be struck out
+// The largest key below `best`: with unsigned wrap-around the differences of the
+// keys below it exceed those of the keys at or over it, so nothing has to be
+// struck out between two rounds.
 template <int V>
 __device__ __forceinline__ uint32_t next_key(const uint32_t (&key)[V], uint32_t best) {
   uint32_t d = key[0] - best;
@@ -259,50 +278,71 @@ __device__ __forceinline__ uint32_t next_key(const uint32_t (&key)[V], uint32_t 
   return best + row_max(d);
 }
 
-enum { kByLogit, kSigmoid, kSoftmax };  // what the selection compares
+// a / b in double for b in the normal range, to about an ulp
+__device__ __forceinline__ double quotient(double a, double b) {
+  double r = __builtin_amdgcn_rcp(b);
+  r = fma(fma(-b, r, 1.0), r, r);
+  r = fma(fma(-b, r, 1.0), r, r);
+  const double q = a * r;
+  return fma(fma(-b, q, a), r, q);
+}
+
+enum By { kByLogit, kBySigmoid, kBySoftmax };          // what the selection compares
+enum Weights { kSoftmaxKept, kSoftmaxAll, kSigmoids };  // softmax over the kept logits, over all; sigmoids
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTop = 16777200.f;     // the largest fixed-point value, below 2^24
 
 // Lane i of a token's 16 holds `per` consecutive experts (at most V) of one group:
-// groups begin at multiples of `lanes` lanes.
-template <bool kBf16, int V, int kBy>
-__global__ __launch_bounds__(256) void gate_kernel(GateArgs p, int lanes, int per) {
+// groups begin at multiples of `lanes` lanes.  A wave takes 4 tokens at a time.
+template <bool kBf16, int V, By kBy, Weights kW>
+__global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, int lanes, int per) {
   __shared__ double value[4][moe::kMaxExperts];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l16 = lane & 15;
-  const bool grouped = p.keep < p.n_groups;
   const int group = l16 / lanes;                      // == p.n_groups or more: an idle lane
   const int inside = (l16 % lanes) * per;
   const int e0 = group * p.group_size + inside;
-  const int n = group < p.n_groups ? min(per, p.group_size - inside) : 0;   // this lane's experts
+  const int n = group < p.n_groups ? max(0, min(per, p.group_size - inside)) : 0;   // this lane's experts
   const int64_t total = p.T * p.E;
 
-  // the fixed-point scale, and the bound on the error of two values' difference
+  // A key is (fixed-point value << 8) + c: the value at least 3, 2 for a masked
+  // expert (-inf is cut to it), 1 where the group is not kept; c = 255 - index, or
+  // what takes a slot without an expert below the masked ones.
+  uint32_t c[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) c[j] = j < n ? static_cast<uint32_t>(255 - e0 - j) : static_cast<uint32_t>(-256);
+
+  // the bias, -inf in a slot without an expert; the fixed-point scale, and the
+  // bound on the error of two values' difference
   float b[V];
-  float scale = 0.f, offset = 0.f, near = 0.f, group_near = 0.f;
+  float scale = kTop / 32.f;    // logits down to 32 below the largest: the cut is monotone, so
+  float offset = 3.f + kTop;    // only equal keys of unequal logits are in doubt
+  float near = 0.f, group_near = 0.f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) b[j] = j >= n ? -INFINITY : kBy != kByLogit && p.bias ? p.bias[e0 + j] : 0.f;
   if constexpr (kBy != kByLogit) {
     float lo = INFINITY, hi = -INFINITY;
+    bool odd = false;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      b[j] = j < n && p.bias ? p.bias[e0 + j] : 0.f;
-      if (!(fabsf(b[j]) <= 1e30f)) hi = INFINITY;     // left to the doubles
-      if (j < n) { lo = fminf(lo, b[j]); hi = fmaxf(hi, b[j]); }
-    }
+    for (int j = 0; j < V; ++j)
+      if (j < n) {
+        odd |= !(fabsf(b[j]) <= 1e30f);
+        lo = fminf(lo, b[j]);
+        hi = fmaxf(hi, b[j]);
+      }
+    if (odd) lo = hi = INFINITY;     // left to the doubles
     lo = -row_max(-lo);
     hi = row_max(hi);
     const float range = 1.f + (hi - lo), big = fmaxf(fabsf(lo), fabsf(hi));
     // s: exp2's argument, exp2, the sum and the reciprocal, 6 u in all (u = 2^-24);
     // a softmax's sum of up to 32 values in sequence and 4 steps: 36 u more.
     // s + b rounds once more.  In the key: half a unit of fma, one of the cut.
-    const float err = (kBy == kSigmoid ? 7.f : 43.f) + big;
+    const float err = (kBy == kBySigmoid ? 7.f : 43.f) + big;
     scale = kTop / range;
-    offset = 2.f - lo * scale;
+    offset = 4.f - lo * scale;
     near = 2.f * (err / range + 2.f);
     group_near = (4.f * err + 4.f * (1.f + big)) * 0x1p-24f;
     if (!(hi < INFINITY)) near = group_near = INFINITY;
-  } else {
-    scale = kTop / 32.f;        // logits down to 32 below the largest: monotone, so only
-    offset = 2.f + kTop;        // equal keys of unequal logits are in doubt
   }
 
   for (int64_t base = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * 4; base < p.T;
@@ -311,105 +351,110 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs p, int lanes, int pe
     const bool active = t < p.T;
     const int64_t row = (active ? t : 0) * p.E;
     float l[V];
-    bool bad = false;
-    float m = -INFINITY;
-    {
-      const int64_t at = row + e0;
-      if (n > 0 && at + V <= total) {
-        if constexpr (kBf16) {
-          uint16_t raw[V];
-          __builtin_memcpy(raw, static_cast<const uint16_t*>(p.logits) + at, sizeof(raw));
+    const int64_t at = row + e0;
+    if (at + V <= total) {         // (what follows a lane's own experts is not looked at)
+      if constexpr (kBf16) {
+        uint32_t raw[V / 2];
+        __builtin_memcpy(raw, static_cast<const uint16_t*>(p.logits) + at, sizeof(raw));
 #pragma unroll
-          for (int j = 0; j < V; ++j) l[j] = bf16_bits_to_f32(raw[j]);
-        } else {
-          __builtin_memcpy(l, static_cast<const float*>(p.logits) + at, sizeof(l));
+        for (int j = 0; j < V; ++j) l[j] = __uint_as_float((j & 1) ? raw[j / 2] & 0xffff0000u : raw[j / 2] << 16);
+      } else {
+        __builtin_memcpy(l, static_cast<const float*>(p.logits) + at, sizeof(l));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) l[j] = j < n ? load_logit<kBf16>(p.logits, at + j) : -INFINITY;
+    }
+    if (p.check) {
+      bool bad = false;
+#pragma unroll
+      for (int j = 0; j < V; ++j) bad |= j < n && (l[j] != l[j] || l[j] == INFINITY);
+      raise_check(p.check, bad && active, MOE_CHECK_LOGITS);
+    }
+
+    // v: what is compared, -inf where masked or without an expert
+    float v[V];
+    float m = 0.f;
+    double sum64 = 1.0;
+    if constexpr (kBy == kBySigmoid) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l[j] * -kLog2e)) + b[j];
+        v[j] = is_live(l[j]) ? s : -INFINITY;
+      }
+    } else {
+      m = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if constexpr (kBy == kByLogit) l[j] += b[j];
+        else if (j >= n) l[j] = -INFINITY;
+        l[j] = is_live(l[j]) ? fminf(l[j], FLT_MAX) : -INFINITY;
+        m = larger(m, l[j]);
+      }
+      m = row_max(m);
+      if (m == -INFINITY) m = 0.f;   // nothing unmasked
+      if constexpr (kW == kSoftmaxAll) {   // the weights' denominator
+        sum64 = 0.0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          sum64 += exp(static_cast<double>(l[j]) - static_cast<double>(m));
+          __builtin_amdgcn_sched_barrier(0);   // one exponential's registers at a time
         }
+        sum64 = row_sum(sum64);
+      }
+      if constexpr (kBy == kBySoftmax) {
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          v[j] = __builtin_amdgcn_exp2f((l[j] - m) * kLog2e);
+          sum += v[j];
+        }
+        sum = row_sum(sum);
+        const float inv = sum > 0.f ? __builtin_amdgcn_rcpf(sum) : 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = l[j] > -INFINITY ? fmaf(v[j], inv, b[j]) : -INFINITY;
       } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) l[j] = j < n ? load_logit<kBf16>(p.logits, at + j) : -INFINITY;
+        for (int j = 0; j < V; ++j) v[j] = l[j];
       }
     }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if (j >= n) l[j] = -INFINITY;
-      bad |= l[j] != l[j] || l[j] == INFINITY;
-      l[j] = is_live(l[j]) ? fminf(l[j], FLT_MAX) : -INFINITY;
-      m = fmaxf(m, l[j]);
-    }
-    if (p.check) raise_check(p.check, bad && active, MOE_CHECK_LOGITS);
-    m = row_max(m);
-    if (m == -INFINITY) m = 0.f;   // nothing unmasked
 
-    float v[V];
-    double sum64 = 1.0;
-    if constexpr (kBy == kByLogit) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[j] = l[j];
-    } else if constexpr (kBy == kSigmoid) {
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        v[j] = l[j] > -INFINITY ? __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l[j] * -kLog2e)) + b[j] : -INFINITY;
-    } else {
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        v[j] = __builtin_amdgcn_exp2f((l[j] - m) * kLog2e);
-        sum += v[j];
-      }
-      sum = row_sum(sum);
-      const float inv = sum > 0.f ? __builtin_amdgcn_rcpf(sum) : 0.f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[j] = l[j] > -INFINITY ? fmaf(v[j], inv, b[j]) : -INFINITY;
-    }
-    if (p.softmax && !p.renorm) {   // the weights' denominator
-      sum64 = 0.0;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        if (j < n && l[j] > -INFINITY) sum64 += exp(static_cast<double>(l[j]) - static_cast<double>(m));
-        __builtin_amdgcn_sched_barrier(0);   // one exponential's registers at a time
-      }
-      sum64 = row_sum(sum64);
-    }
-
-    uint32_t key[V];   // (value + 2) << 8 | 255 - index; 1 in the value's place: masked; 0: not to be taken
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float x = kBy == kByLogit ? v[j] - m : v[j];
-      const uint32_t q = l[j] > -INFINITY ? static_cast<uint32_t>(fminf(fmaxf(fmaf(x, scale, offset), 2.f), 16777215.f)) : 1u;
-      key[j] = j < n ? (q << 8) + static_cast<uint32_t>(255 - e0 - j) : 0u;
-    }
-
-    bool doubt = false;
-    if (grouped) {
+    bool doubt = false, kept = true;
+    if (p.keep < p.n_groups) {
       float m1 = -INFINITY, m2 = -INFINITY;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        m2 = fmaxf(m2, fminf(m1, v[j]));
-        m1 = fmaxf(m1, v[j]);
+        if (kBy != kByLogit) m2 = __builtin_amdgcn_fmed3f(m1, m2, v[j]);
+        m1 = larger(m1, v[j]);
       }
-      auto join = [&](float o1, float o2) {
-        m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
-        m1 = fmaxf(m1, o1);
+      auto join = [&](int o1, int o2) {
+        if (kBy != kByLogit) m2 = larger(__builtin_amdgcn_fmed3f(m1, m2, __int_as_float(o1)), __int_as_float(o2));
+        m1 = larger(m1, __int_as_float(o1));
       };
-#define MOE_JOIN(OFF)                                                            \
-  if (lanes > OFF)                                                               \
-    join(__int_as_float(dpp_partner<OFF>(__float_as_int(m1))), __int_as_float(dpp_partner<OFF>(__float_as_int(m2))));
-      MOE_JOIN(1) MOE_JOIN(2) MOE_JOIN(4)
-#undef MOE_JOIN
-      const float score = p.top2 && m2 > -INFINITY ? m1 + m2 : m1;
-      const bool rep = l16 % lanes == 0 && group < p.n_groups;
-      int rank = 0;
-      count_ahead<1>(rep ? score : NAN, score, (2u << l16) - (2u << (l16 % lanes)), rank);
-      const bool kept = rank < p.keep;
+      if (lanes > 1) join(dpp_partner<1>(__float_as_int(m1)), dpp_partner<1>(__float_as_int(m2)));
+      if (lanes > 2) join(dpp_partner<2>(__float_as_int(m1)), dpp_partner<2>(__float_as_int(m2)));
+      if (lanes > 4) join(dpp_partner<4>(__float_as_int(m1)), dpp_partner<4>(__float_as_int(m2)));
+      const float score = kBy != kByLogit && p.top2 && m2 > -INFINITY ? m1 + m2 : m1;
+      const bool real = group < p.n_groups;
+      const float rep = real ? score : NAN;
+      const int rank = lanes == 1 ? count_ahead<1>(rep, score, l16) : lanes == 2 ? count_ahead<2>(rep, score, l16)
+                       : lanes == 4 ? count_ahead<4>(rep, score, l16) : count_ahead<8>(rep, score, l16);
+      kept = real && rank < p.keep;
       if constexpr (kBy != kByLogit) {
         // the last group kept against the first one left out
-        const float low = -row_max(rep && kept ? -score : -INFINITY);
-        const float high = row_max(rep && !kept ? score : -INFINITY);
+        const float low = -row_max(kept ? -score : -INFINITY);
+        const float high = row_max(real && !kept ? score : -INFINITY);
         doubt = high > -INFINITY && !(low - high > group_near);
       }
-      if (!kept)
+    }
+
+    uint32_t key[V];
+    const float low = kept ? 2.f : 1.f, high = kept ? 16777215.f : 1.f;
 #pragma unroll
-        for (int j = 0; j < V; ++j) key[j] = 0u;
+    for (int j = 0; j < V; ++j) {
+      const float x = kBy == kByLogit ? v[j] - m : v[j];
+      const float f = __builtin_amdgcn_fmed3f(fmaf(x, scale, offset), low, high);
+      key[j] = (static_cast<uint32_t>(f) << 8) + c[j];
     }
 
     // lane i takes the i-th key, lane k the best one left
@@ -421,42 +466,46 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs p, int lanes, int pe
         if (l16 == i) mine = best;
       }
     const int e = min(255 - static_cast<int>(mine & 255u), p.E - 1);
-    const bool some = l16 <= p.k && mine >= 512u;      // an unmasked expert
+    const bool some = l16 <= p.k && mine >= 768u;      // an unmasked expert
+    // a logit too far below the largest is cut to a masked one's value as well
+    doubt |= l16 < p.k && !some;
     float lk = some ? load_logit<kBf16>(p.logits, row + e) : -INFINITY;
     lk = fminf(lk, FLT_MAX);
     const uint32_t q = mine >> 8, q_next = static_cast<uint32_t>(next_lane(static_cast<int>(mine))) >> 8;
-    const float l_next = __int_as_float(next_lane(__float_as_int(lk)));
-    bool same = lk == l_next;
-    float bk = 0.f;
+    bool same = lk == __int_as_float(next_lane(__float_as_int(lk)));
     if constexpr (kBy != kByLogit) {
-      if (p.bias && some) bk = p.bias[e];
+      const float bk = p.bias && some ? p.bias[e] : 0.f;
       same = same && bk == __int_as_float(next_lane(__float_as_int(bk)));
     }
-    doubt |= some && l16 < p.k && q_next >= 2u && static_cast<float>(q - q_next) <= near && !same;
+    doubt |= some && l16 < p.k && q_next >= 3u && static_cast<float>(q - q_next) <= near && !same;
     const uint64_t doubts = __ballot(doubt && active);
     const bool redo = (doubts >> (lane & 48)) & 0xffffu;
 
     // weights in double, rounded once
     const bool on = some && l16 < p.k;
-    double w;
-    if (p.softmax) {
-      const double top = p.renorm ? static_cast<double>(row_max(on ? lk : -INFINITY)) : static_cast<double>(m);
-      w = on ? exp(static_cast<double>(lk) - top) : 0.0;
+    const float top = row_max(on ? lk : -INFINITY);
+    double w, sum = sum64;
+    if constexpr (kW == kSigmoids) {
+      const double x = lk, z = exp(-fabs(x));          // s = 1 / (1 + z) or z / (1 + z)
+      double up = x > 0.0 ? 1.0 : z;
+      // ratios survive where every sigmoid underflows: times exp(-top)
+      if (p.renorm && __any(top < -600.f) && top < 0.f) up = exp(x - static_cast<double>(top));
+      w = on ? quotient(up, 1.0 + z) : 0.0;
+      if (p.renorm) sum = row_sum(w);
     } else {
-      // see gate_token
-      const double top = p.renorm ? fmin(static_cast<double>(row_max(on ? lk : -INFINITY)), 0.0) : 0.0;
-      const double x = lk;
-      w = !on ? 0.0 : x > 0.0 ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / (1.0 + exp(x));
+      w = on ? exp(static_cast<double>(lk) - static_cast<double>(kW == kSoftmaxKept ? top : m)) : 0.0;
+      if (kW == kSoftmaxKept) sum = row_sum(w);
     }
-    const double sum = p.renorm ? row_sum(w) : sum64;
+    w = sum > 0.0 ? p.scale * quotient(w, sum) : 0.0;
     if (active && !redo && l16 < p.k) {
       p.idx[t * p.k + l16] = e;
-      p.w[t * p.k + l16] = static_cast<float>(sum > 0.0 ? p.scale * (w / sum) : 0.0);
+      p.w[t * p.k + l16] = static_cast<float>(w);
     }
     if (doubts)
 #pragma unroll 1
       for (int i = 0; i < 4; ++i)
-        if ((doubts >> (16 * i)) & 0xffffu) gate_token<kBf16>(p, base + i, lane, value[wave], true);
+        if ((doubts >> (16 * i)) & 0xffffu)
+          gate_token_call<kBf16>((KernelArgs*)__builtin_amdgcn_kernarg_segment_ptr(), base + i, value[wave]);
   }
 }
 
@@ -467,33 +516,38 @@ __global__ __launch_bounds__(256) void gate_wave_kernel(GateArgs p) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave;
   if (t >= p.T) return;
-  gate_token<kBf16>(p, t, lane, value[wave], true);
+  gate_token<kBf16>(p, t, lane, value[wave]);
 }
 
-template <bool kBf16, int kBy>
-void launch_slots(const GateArgs& p, hipStream_t s) {
+template <bool kBf16, By kBy, Weights kW>
+void launch_slots(GateArgs p, hipStream_t s) {
   int lanes = 16;
-  if (p.keep < p.n_groups)
-    while (16 / lanes < p.n_groups) lanes /= 2;
-  GateArgs q = p;
-  if (p.keep == p.n_groups) { q.n_groups = q.keep = 1; q.group_size = p.E; }
-  const int per = static_cast<int>(moe::ceil_div(q.group_size, lanes));
-  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(2048, moe::ceil_div(p.T, 16)));
-  if (per <= 2) gate_kernel<kBf16, 2, kBy><<<blocks, 256, 0, s>>>(q, lanes, per);
-  else if (per <= 4) gate_kernel<kBf16, 4, kBy><<<blocks, 256, 0, s>>>(q, lanes, per);
-  else if (per <= 8) gate_kernel<kBf16, 8, kBy><<<blocks, 256, 0, s>>>(q, lanes, per);
-  else if (per <= 12) gate_kernel<kBf16, 12, kBy><<<blocks, 256, 0, s>>>(q, lanes, per);
-  else if (per <= 16) gate_kernel<kBf16, 16, kBy><<<blocks, 256, 0, s>>>(q, lanes, per);
-  else gate_kernel<kBf16, 32, kBy><<<blocks, 256, 0, s>>>(q, lanes, per);
+  if (p.keep == p.n_groups) {
+    p.n_groups = p.keep = 1;
+    p.group_size = p.E;
+  }
+  while (16 / lanes < p.n_groups) lanes /= 2;
+  const int per = static_cast<int>(moe::ceil_div(p.group_size, lanes));
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(1024, moe::ceil_div(p.T, 16)));
+  if (per <= 2) gate_kernel<kBf16, 2, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes, per);
+  else if (per <= 4) gate_kernel<kBf16, 4, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes, per);
+  else if (per <= 8) gate_kernel<kBf16, 8, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes, per);
+  else if (per <= 12) gate_kernel<kBf16, 12, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes, per);
+  else if (per <= 16) gate_kernel<kBf16, 16, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes, per);
+  else gate_kernel<kBf16, 32, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes, per);
 }
 
 template <bool kBf16>
 void launch_gate(const GateArgs& p, hipStream_t s) {
+  const bool by_logit = !p.bias && !(p.top2 && p.keep < p.n_groups);
   if (p.keep < p.n_groups && p.n_groups > 16)
     gate_wave_kernel<kBf16><<<static_cast<unsigned>(moe::ceil_div(p.T, 4)), 256, 0, s>>>(p);
-  else if (!p.bias && !(p.top2 && p.keep < p.n_groups)) launch_slots<kBf16, kByLogit>(p, s);
-  else if (p.softmax) launch_slots<kBf16, kSoftmax>(p, s);
-  else launch_slots<kBf16, kSigmoid>(p, s);
+  else if (!p.softmax && by_logit) launch_slots<kBf16, kByLogit, kSigmoids>(p, s);
+  else if (!p.softmax) launch_slots<kBf16, kBySigmoid, kSigmoids>(p, s);
+  else if (p.renorm && by_logit) launch_slots<kBf16, kByLogit, kSoftmaxKept>(p, s);
+  else if (p.renorm) launch_slots<kBf16, kBySoftmax, kSoftmaxKept>(p, s);
+  else if (by_logit) launch_slots<kBf16, kByLogit, kSoftmaxAll>(p, s);
+  else launch_slots<kBf16, kBySoftmax, kSoftmaxAll>(p, s);
 }
 
 // ------------------------------------------------------------------ backward
@@ -515,26 +569,44 @@ struct GateBwdArgs {
   int32_t* check;
 };
 
-template <bool kBf16>
+// With the slot I after this lane's: its part, if it is for the same expert; and
+// whether the slot I before is for that expert already.
+template <int I>
+__device__ __forceinline__ void join_repeats(int e, float slot, int l16, int k, bool& first, float& v) {
+  if constexpr (I < moe::kMaxTopK) {
+    const int after = __float_as_int(rotated<16 - I>(__int_as_float(e)));
+    const float part = rotated<16 - I>(slot);
+    if (after == e && l16 + I < k) v += part;
+    if (__float_as_int(rotated<I>(__int_as_float(e))) == e && l16 >= I) first = false;
+    join_repeats<I + 1>(e, slot, l16, k, first, v);
+  }
+}
+
+// 16 lanes a token; a lane holds pieces of 8 consecutive experts, 128 apart.  The
+// k parts meet the zeros (or the dense term) in LDS, so the row is written once,
+// in whole pieces.  Bound by the row's bytes; float32 throughout.
+template <bool kBf16, bool kDense>
 __global__ __launch_bounds__(256) void gate_grad_kernel(GateBwdArgs p) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave;
-  if (t >= p.T) return;
-  const int64_t row = t * p.E;
-  const bool dense = p.softmax && !p.renorm;
+  constexpr int kPieces = moe::kMaxExperts / 128;
+  __shared__ float4 parts[16][moe::kMaxExperts / 4];
+  const int l16 = threadIdx.x & 15;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  const bool active = t < p.T;
+  const int64_t row = (active ? t : 0) * p.E;
+  float4* mine = parts[threadIdx.x >> 4];
 
   // lanes 0 .. k - 1: the slot's expert, gradient and logit
   int e = -1;
   float g = 0.f, lk = -INFINITY;
   bool bad = false;
-  if (lane < p.k) {
-    e = p.idx[t * p.k + lane];
+  if (active && l16 < p.k) {
+    e = p.idx[t * p.k + l16];
     bad = e < 0 || e >= p.E;
-    if (!bad) {
-      g = p.scale * p.d_w[t * p.k + lane];
-      lk = load_logit<kBf16>(p.logits, row + e);
-    } else {
+    if (bad) {
       e = -1;
+    } else {
+      g = p.scale * p.d_w[t * p.k + l16];
+      lk = load_logit<kBf16>(p.logits, row + e);
     }
   }
   if (p.check) raise_check(p.check, bad, MOE_CHECK_INDEX);
@@ -542,65 +614,83 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GateBwdArgs p) {
   lk = on ? fminf(lk, FLT_MAX) : -INFINITY;
   if (!on) g = 0.f;
 
-  float l[4];
+  float l[kPieces][8];
   float m = -INFINITY, total = 0.f;
-  if (dense) {
+  if constexpr (kDense) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = lane + 64 * j;
-      l[j] = c < p.E ? load_logit<kBf16>(p.logits, row + c) : -INFINITY;
-      l[j] = is_live(l[j]) ? fminf(l[j], FLT_MAX) : -INFINITY;
-      m = fmaxf(m, l[j]);
-    }
-    m = wave_max(m);
+    for (int c = 0; c < kPieces; ++c) {
+      const int at = c * 128 + l16 * 8, n = active ? p.E - at : 0;
+      if (n > 0) rows::unpack8<kBf16>(rows::load8_part<kBf16>(p.logits, row + at, n), l[c]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      l[j] = l[j] > -INFINITY ? expf(l[j] - m) : 0.f;
-      total += l[j];
+      for (int u = 0; u < 8; ++u) {
+        l[c][u] = u < n && is_live(l[c][u]) ? fminf(l[c][u], FLT_MAX) : -INFINITY;
+        m = larger(m, l[c][u]);
+      }
     }
-    total = wave_sum(total);
+    m = row_max(m);
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c)
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        l[c][u] = l[c][u] > -INFINITY ? expf(l[c][u] - m) : 0.f;
+        total += l[c][u];
+      }
+    total = row_sum(total);
   }
 
   float slot;   // the slot's part of d_l[e]
   float common = 0.f;
   if (p.softmax) {
-    if (p.renorm) m = wave_max(lk);
+    if (!kDense) m = row_max(lk);
     float s = on ? expf(lk - m) : 0.f;
-    if (p.renorm) total = wave_sum(s);
+    if (!kDense) total = row_sum(s);
     s = total > 0.f ? s / total : 0.f;
-    common = wave_sum(g * s);
-    slot = p.renorm ? s * (g - common) : g * s;
+    common = row_sum(g * s);
+    slot = kDense ? g * s : s * (g - common);
   } else {
     const float z = expf(-fabsf(lk));          // s = 1 / (1 + z) or z / (1 + z)
     const float other = on ? (lk > 0.f ? z : 1.f) / (1.f + z) : 0.f;   // 1 - s
     if (p.renorm) {
-      const float top = fminf(wave_max(lk), 0.f);
+      const float top = fminf(row_max(lk), 0.f);
       const float s = !on ? 0.f : (lk > 0.f ? 1.f : expf(lk - top)) / (1.f + z);
-      const float sum = wave_sum(s);
+      const float sum = row_sum(s);
       const float r = sum > 0.f ? s / sum : 0.f;
-      slot = r * (g - wave_sum(g * r)) * other;
+      slot = r * (g - row_sum(g * r)) * other;
     } else {
       slot = on ? g * ((lk > 0.f ? 1.f : z) / (1.f + z)) * other : 0.f;
     }
   }
 
-  float d[4];
+  // an expert named twice: its first slot takes the others' parts, in slot order
+  bool first = e >= 0;
+  float v = slot;
+  join_repeats<1>(e, slot, l16, p.k, first, v);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) d[j] = dense && l[j] > 0.f ? -(l[j] / total) * common : 0.f;
-  for (int i = 0; i < p.k; ++i) {
-    const int ei = __shfl(e, i);
-    const float v = __shfl(slot, i);
+  for (int c = 0; c < kPieces; ++c)
+    if (c * 128 + l16 * 8 < p.E) mine[c * 32 + l16 * 2] = mine[c * 32 + l16 * 2 + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
+  wave_lds_fence();
+  if (first) reinterpret_cast<float*>(mine)[e] = v;
+  wave_lds_fence();
+  if (!active) return;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (ei == lane + 64 * j) d[j] += v;
+  for (int c = 0; c < kPieces; ++c) {
+    const int at = c * 128 + l16 * 8, n = p.E - at;
+    if (n <= 0) continue;
+    const float4 a = mine[c * 32 + l16 * 2], b = mine[c * 32 + l16 * 2 + 1];
+    float d[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if constexpr (kDense)
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (l[c][u] > 0.f) d[u] -= l[c][u] / total * common;
+    rows::store8_part<kBf16>(p.d_logits, row + at, n, d);
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = lane + 64 * j;
-    if (c >= p.E) continue;
-    if constexpr (kBf16) static_cast<uint16_t*>(p.d_logits)[row + c] = static_cast<uint16_t>(f32_to_bf16_bits(d[j]));
-    else static_cast<float*>(p.d_logits)[row + c] = d[j];
-  }
+}
+
+template <bool kBf16>
+void launch_gate_grad(const GateBwdArgs& p, hipStream_t s) {
+  const unsigned blocks = static_cast<unsigned>(moe::ceil_div(p.T, 16));
+  if (p.softmax && !p.renorm) gate_grad_kernel<kBf16, true><<<blocks, 256, 0, s>>>(p);
+  else gate_grad_kernel<kBf16, false><<<blocks, 256, 0, s>>>(p);
 }
 
 int check_common(const char* who, moe_dtype dt, int64_t T, int E, int k, moe_score score, float scale) {
@@ -652,8 +742,7 @@ extern "C" int moe_gate_backward(const void* logits, moe_dtype dt, int64_t T, in
   if (!logits || !topk_idx || !d_topk_w || !d_logits)
     return fail(MOE_ERR_INVALID_ARG, "moe_gate_backward: null pointer");
   GateBwdArgs p{logits, topk_idx, d_topk_w, d_logits, T, E, k, score == MOE_SOFTMAX, renorm != 0, scale, check};
-  const unsigned blocks = static_cast<unsigned>(ceil_div(T, 4));
-  if (dt == MOE_BF16) gate_grad_kernel<true><<<blocks, 256, 0, as_stream(stream)>>>(p);
-  else gate_grad_kernel<false><<<blocks, 256, 0, as_stream(stream)>>>(p);
+  if (dt == MOE_BF16) launch_gate_grad<true>(p, as_stream(stream));
+  else launch_gate_grad<false>(p, as_stream(stream));
   return hip_status(hipGetLastError(), "moe_gate_backward launch");
 }
