@@ -20,6 +20,10 @@ scores or weights that are not renormalised.  In training, moe_backward (or
 moe_backward_gated and moe_gate_backward) and moe_layer_norm_backward give the
 gradients, and moe_clip_grads bounds their global norm.
 
+Those calls take microseconds on small batches, so their arguments are checked
+and their outputs allocated in a native module (csrc/binding.cpp); the others
+go through ctypes.
+
 Every hot-path call takes `check`: an int32 device tensor of one element
 (zeroed by the caller) that the kernels flag invalid input into;
 moe_check_device_error(check) reads it back.  Output tensors passed in by the
@@ -31,7 +35,7 @@ import ctypes
 
 import torch
 
-from ._native import LIB_PATH, MoEError, lib
+from ._native import LIB_PATH, MoEError, binding, lib
 
 __all__ = ["moe_route", "moe_stats_state_bytes", "moe_stats_init", "moe_stats", "moe_stats_load_state",
            "moe_plan_replicas",
@@ -120,44 +124,8 @@ def _bytes_of(t, need, name):
     return t
 
 
-def _same(t, dev, dtype, shape, name):
-    """A tensor of exactly this device, dtype and shape (None passes)."""
-    if t is None:
-        return
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch tensor")
-    if t.dtype != dtype or t.device != dev or t.shape != shape:
-        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on "
-                         f"{t.device}")
-
-
-def _call_on(dev, stream, name, *args):
-    """_call with the stream last: the device's current one, or `stream`; the
-    tensors' device is made current for the call where it is not."""
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _call(name, *args, _stream(stream))
-    _call(name, *args, _stream(stream))
-
-
-def _workspace(t, need, dev, stream, name):
-    """A given workspace, checked, or one for this call: memory that goes back to
-    the allocator when the call returns, so a call on another stream than the
-    current one tells the allocator who still uses it."""
-    if t is not None:
-        if _bytes_of(t, need, name).device != dev:
-            raise ValueError(f"{name}: on another device than the call's tensors")
-        return t
-    t = torch.empty(need, dtype=torch.uint8, device=dev)
-    if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                        torch.cuda.ExternalStream(int(stream), device=dev))
-    return t
-
-
-def _check_ptr(check, dev):
-    _same(check, dev, torch.int32, (1,), "check")
-    return _ptr(check)
+def _failed(name, status):
+    raise MoEError(name, status, lib().moe_last_error().decode(errors="replace"))
 
 
 def new_check_word(device="cuda"):
@@ -196,30 +164,17 @@ def moe_gate(logits: torch.Tensor, k: int, score="softmax", bias=None, n_groups:
     added for the selection only, the keep_groups best of n_groups groups
     (group_score "max" or "top2"; keep_groups None: all), weights renormalised over
     the k or not, times scale."""
-    dt, dev = _dtype_code(logits), logits.device
-    T, E = logits.shape
-    _same(bias, dev, torch.float32, (E,), "bias")
-    idx = _out(topk_idx, (T, k), torch.int32, dev, "topk_idx")
-    w = _out(topk_w, (T, k), torch.float32, dev, "topk_w")
-    _call_on(dev, stream, "moe_gate", _ptr(logits), dt, T, E, k, _SCORE[score], _ptr(bias), n_groups,
-             n_groups if keep_groups is None else keep_groups, _GROUP_SCORE[group_score], 1 if renorm else 0, scale,
-             _ptr(idx), _ptr(w), _check_ptr(check, dev))
-    return idx, w
+    r = binding().gate(logits, k, _SCORE[score], bias, n_groups, keep_groups, _GROUP_SCORE[group_score], renorm, scale,
+                       topk_idx, topk_w, stream, check)
+    return r if type(r) is tuple else _failed("moe_gate", r)
 
 
 def moe_gate_backward(logits: torch.Tensor, topk_idx: torch.Tensor, d_topk_w: torch.Tensor, score="softmax",
                       renorm: bool = True, scale: float = 1.0, d_logits=None, stream=None, check=None):
     """d_logits [T, E] (of the logits' dtype) from the gradient d_topk_w (float32 [T, k])
     of moe_gate's weights, for the experts topk_idx it chose."""
-    dt, dev = _dtype_code(logits), logits.device
-    T, E = logits.shape
-    k = topk_idx.shape[-1]
-    _same(topk_idx, dev, torch.int32, (T, k), "topk_idx")
-    _same(d_topk_w, dev, torch.float32, (T, k), "d_topk_w")
-    d_logits = _out(d_logits, (T, E), logits.dtype, dev, "d_logits")
-    _call_on(dev, stream, "moe_gate_backward", _ptr(logits), dt, T, E, k, _SCORE[score], 1 if renorm else 0, scale,
-             _ptr(topk_idx), _ptr(d_topk_w), _ptr(d_logits), _check_ptr(check, dev))
-    return d_logits
+    r = binding().gate_backward(logits, topk_idx, d_topk_w, _SCORE[score], renorm, scale, d_logits, stream, check)
+    return r if type(r) is not int else _failed("moe_gate_backward", r)
 
 
 # --------------------------------------------------------------- statistics
@@ -489,36 +444,13 @@ def moe_backward_gated(x_perm, y_perm, topk_idx, topk_w, inv_pos, expert_off, w_
 
 
 # --------------------------------------------------------------- layer norm
-def _norm_vectors(x, weight, bias):
-    """The dtype code of weight and bias (float32 or the rows' dtype, both alike)."""
-    if x.dim() != 2:
-        raise ValueError("layer norm takes rows [T, H]")
-    given = [t for t in (weight, bias) if t is not None]
-    w_dtype = given[0].dtype if given else x.dtype
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        _same(t, x.device, w_dtype, (x.shape[1],), name)
-    if w_dtype != x.dtype and w_dtype != torch.float32:
-        raise TypeError("weight and bias must be float32 or of the rows' dtype")
-    return MOE_F32 if w_dtype == torch.float32 else MOE_BF16
-
-
 def moe_layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, residual=None, y=None, x_sum=None,
                    stream=None):
     """(y, x_sum): the layer norm y of the rows of x [T, H], or with `residual` of
     x_sum = x + residual (None without one).  y and x_sum may be given buffers,
     x or residual among them."""
-    dt, dev = _dtype_code(x), x.device
-    w_dt = _norm_vectors(x, weight, bias)
-    T, H = x.shape
-    _same(residual, dev, x.dtype, x.shape, "residual")
-    y = _out(y, (T, H), x.dtype, dev, "y")
-    if residual is not None:
-        x_sum = _out(x_sum, (T, H), x.dtype, dev, "x_sum")
-    elif x_sum is not None:
-        raise ValueError("x_sum is written with a residual only")
-    _call_on(dev, stream, "moe_layer_norm", _ptr(x), _ptr(residual), dt, T, H, _ptr(weight), _ptr(bias), w_dt, eps,
-             _ptr(x_sum), _ptr(y))
-    return y, x_sum
+    r = binding().layer_norm(x, weight, bias, eps, residual, y, x_sum, stream)
+    return r if type(r) is tuple else _failed("moe_layer_norm", r)
 
 
 def moe_layer_norm_backward_workspace_bytes(T: int, H: int) -> int:
@@ -531,52 +463,15 @@ def moe_layer_norm_backward(d_y: torch.Tensor, x: torch.Tensor, weight=None, bia
     summed).  d_weight and d_bias are None where there is no weight or bias (the
     bias's values are not needed, only whether there is one).  d_skip: the gradient
     that reaches x past the norm, added to d_x."""
-    dt, dev = _dtype_code(x), x.device
-    w_dt = _norm_vectors(x, weight, bias)
-    T, H = x.shape
-    _same(d_y, dev, x.dtype, x.shape, "d_y")
-    _same(d_skip, dev, x.dtype, x.shape, "d_skip")
-    o = dict(out or {})
-    o["d_x"] = _out(o.get("d_x"), (T, H), x.dtype, dev, "d_x")
-    for key, t in (("d_weight", weight), ("d_bias", bias)):
-        if t is None and o.get(key) is not None:
-            raise ValueError(f"{key}: there is no such parameter")
-        o[key] = None if t is None else _out(o.get(key), (H,), t.dtype, dev, key)
-    nbytes = 0
-    if weight is not None or bias is not None:
-        nbytes = moe_layer_norm_backward_workspace_bytes(T, H)
-        workspace = _workspace(workspace, nbytes, dev, stream, "layer norm workspace")
-    _call_on(dev, stream, "moe_layer_norm_backward", _ptr(d_y), _ptr(x), dt, T, H, _ptr(weight), w_dt, eps,
-             _ptr(d_skip), _ptr(o["d_x"]), _ptr(o["d_weight"]), _ptr(o["d_bias"]), _ptr(workspace) if nbytes else None,
-             nbytes)
-    return o
+    o = {} if out is None else out
+    r = binding().layer_norm_backward(d_y, x, weight, bias, eps, d_skip, o.get("d_x"), o.get("d_weight"),
+                                      o.get("d_bias"), workspace, stream)
+    if type(r) is not tuple:
+        _failed("moe_layer_norm_backward", r)
+    return {"d_x": r[0], "d_weight": r[1], "d_bias": r[2]}
 
 
 # -------------------------------------------------------- gradient clipping
-def _grad_list(grads, dev, what):
-    """ctypes arrays (pointers, element counts, dtype codes) of a list of tensors."""
-    n = len(grads)
-    ptrs, counts, types = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int * n)()
-    for i, g in enumerate(grads):
-        if not isinstance(g, torch.Tensor):
-            raise TypeError(f"{what}: expected torch tensors")
-        if g.device != dev or not g.is_contiguous():
-            raise ValueError(f"{what}[{i}]: must be contiguous and on {dev}")
-        ptrs[i], counts[i], types[i] = g.data_ptr(), g.numel(), _dtype_code(g)
-    return ptrs, counts, types
-
-
-def _norm_buffers(grads, norm, workspace, stream):
-    if len(grads) == 0 and norm is None:
-        raise ValueError("an empty list of gradients names no device: pass norm")
-    dev = norm.device if norm is not None else grads[0].device
-    if dev.type != "cuda":
-        raise ValueError("tensors passed to the MoE library must live on the GPU")
-    norm = _out(norm, (1,), torch.float32, dev, "norm")
-    need = moe_grad_norm_workspace_bytes()
-    return dev, norm, _workspace(workspace, need, dev, stream, "gradient norm workspace"), need
-
-
 def moe_grad_norm_workspace_bytes() -> int:
     return int(lib().moe_grad_norm_workspace_bytes())
 
@@ -584,11 +479,8 @@ def moe_grad_norm_workspace_bytes() -> int:
 def moe_grad_norm(grads, norm=None, workspace=None, stream=None, check=None):
     """float32 [1] on the device: the square root of the sum of all squares of a list
     of float32 or bfloat16 tensors."""
-    dev, norm, workspace, need = _norm_buffers(grads, norm, workspace, stream)
-    ptrs, counts, types = _grad_list(grads, dev, "grads")
-    _call_on(dev, stream, "moe_grad_norm", ptrs, counts, types, len(grads), _ptr(norm), _ptr(workspace), need,
-             _check_ptr(check, dev))
-    return norm
+    r = binding().clip_grads(grads, None, None, None, norm, workspace, stream, check)
+    return r if type(r) is not int else _failed("moe_grad_norm", r)
 
 
 def moe_clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, norm=None, workspace=None, stream=None,
@@ -596,18 +488,10 @@ def moe_clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, norm=Non
     """(norm, out): the global norm of the gradients (before clipping) and the gradients
     times min(1, max_norm / (norm + eps)), in place unless `out` gives other tensors
     of the same shapes and dtypes."""
-    dev, norm, workspace, need = _norm_buffers(grads, norm, workspace, stream)
-    ptrs, counts, types = _grad_list(grads, dev, "grads")
-    outs = ptrs
-    if out is not None:
-        if len(out) != len(grads):
-            raise ValueError("out: one tensor for each gradient")
-        for i, (o, g) in enumerate(zip(out, grads)):
-            _same(o, dev, g.dtype, g.shape, f"out[{i}]")
-        outs = _grad_list(out, dev, "out")[0]
-    _call_on(dev, stream, "moe_clip_grads", ptrs, outs, counts, types, len(grads), max_norm, eps, _ptr(norm),
-             _ptr(workspace), need, _check_ptr(check, dev))
-    return norm, list(grads) if out is None else list(out)
+    r = binding().clip_grads(grads, out, max_norm, eps, norm, workspace, stream, check)
+    if type(r) is int:
+        _failed("moe_clip_grads", r)
+    return r, list(grads if out is None else out)
 
 
 # ------------------------------------------------------ one layer, composed

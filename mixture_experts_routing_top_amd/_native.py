@@ -1,11 +1,14 @@
-"""Loads libmoe_mi355x.so and declares the C signatures of include/moe.h."""
+"""Loads libmoe_mi355x.so and declares the C signatures of include/moe.h; loads the
+native binding of the calls that take microseconds (csrc/binding.cpp)."""
 from __future__ import annotations
 
 import ctypes
 import os
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_mi355x.so")
+BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
 _lib = None
+_binding = None
 
 _p, _i, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 _f = ctypes.c_float
@@ -65,3 +68,16 @@ def lib():
             fn.restype, fn.argtypes = res, args
         _lib = handle
     return _lib
+
+
+def binding():
+    """The loaded native binding.  Raises if it has not been built."""
+    global _binding
+    if _binding is None:
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
+                               "`python -m mixture_experts_routing_top_amd.build`")
+        lib()
+        from . import _binding as module
+        _binding = module
+    return _binding

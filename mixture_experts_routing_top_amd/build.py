@@ -1,4 +1,4 @@
-"""Build libmoe_mi355x.so in-tree with hipcc for gfx950.
+"""Build libmoe_mi355x.so in-tree with hipcc for gfx950, and the native binding.
 
     python -m mixture_experts_routing_top_amd.build
 
@@ -19,6 +19,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_mi355x.so")
 SOURCES = ["status.cpp", "route.hip", "stats.hip", "plan.hip", "dispatch.hip", "ffn.hip", "combine.hip", "backward.hip",
            "gate.hip", "norm.hip", "clip.hip"]
+BINDING = os.path.join(PKG, "_binding.so")
+CXX = os.environ.get("CXX", "g++")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 CFLAGS = ["-x", "hip", f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
@@ -34,18 +36,42 @@ def _compile(src: str) -> str:
     return obj
 
 
+def build_binding() -> str:
+    """The Python module of csrc/binding.cpp (host code only), against the installed
+    torch and the library beside it."""
+    import sysconfig
+
+    from torch.utils import cpp_extension
+
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           "-I", INCLUDE]
+    for path in [*cpp_extension.include_paths("cuda"), sysconfig.get_paths()["include"]]:
+        cmd += ["-isystem", path]
+    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp, LIB, "-Wl,-rpath,$ORIGIN"]
+    for path in cpp_extension.library_paths("cuda"):
+        cmd += ["-L", path]
+    cmd += ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CXX} failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     with ThreadPoolExecutor(min(8, len(SOURCES))) as ex:
         objs = list(ex.map(_compile, SOURCES))
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
+    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname,libmoe_mi355x.so", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    build_binding()
     if verbose:
-        print("built", LIB)
+        print("built", LIB, "and", BINDING)
     return LIB
 
 
