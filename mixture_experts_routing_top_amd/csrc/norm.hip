@@ -65,16 +65,19 @@ struct NormArgs {
   float eps;
 };
 
+// n of eight elements from p, the rest zero; `fill` throughout where there is no p
+template <bool kBf16>
+__device__ __forceinline__ void load_piece(const void* p, int64_t at, int n, float fill, float (&v)[8]) {
+  if (p && n > 0) unpack8<kBf16>(load8_part<kBf16>(p, at, n), v);
+  else
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = fill;
+}
+
 template <bool kWBf16, int TPR, int NV>
 __device__ __forceinline__ void load_vector(const void* p, int tid, int H, float fill, float (&v)[NV][8]) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * TPR + tid) * 8;
-    if (p && c < H) unpack8<kWBf16>(load8_part<kWBf16>(p, c, H - c), v[j]);
-    else
-#pragma unroll
-      for (int u = 0; u < 8; ++u) v[j][u] = fill;
-  }
+  for (int j = 0; j < NV; ++j) load_piece<kWBf16>(p, (j * TPR + tid) * 8, H - (j * TPR + tid) * 8, fill, v[j]);
 }
 
 template <bool kBf16, bool kWBf16, int TPR, int NV, int R>
@@ -154,36 +157,71 @@ struct NormBwdArgs {
   float eps;
 };
 
+// a row's pieces as they lie in memory
+template <bool kBf16, int NV>
+struct RawRow {
+  Raw8<kBf16> piece[NV];
+};
+
+template <bool kBf16, int TPR, int NV>
+__device__ __forceinline__ void load_row(const void* p, int64_t row, int64_t T, int H, int tid,
+                                         RawRow<kBf16, NV>& r) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * TPR + tid) * 8;
+    r.piece[j] = {};
+    if (p && row < T && c < H) r.piece[j] = load8_part<kBf16>(p, row * H + c, H - c);
+  }
+}
+
+// Blocks a CU holds of the backward kernel, by the registers it needs: 4 waves a
+// SIMD with one piece a thread, else 2.
+constexpr int bwd_blocks_per_cu(int tpr, int nv) { return tpr > 256 ? 1 : nv == 1 ? 4 : 2; }
+
 template <bool kBf16, bool kWBf16, int TPR, int NV, int R>
-__global__ __launch_bounds__(TPR* R) void norm_backward_kernel(NormBwdArgs p) {
+__global__ __launch_bounds__(TPR* R, bwd_blocks_per_cu(TPR, NV)) void norm_backward_kernel(NormBwdArgs p) {
   __shared__ float part[2][R * (TPR / 64) * 4];
   __shared__ float cols[R > 1 ? 2 * NV * 8 * TPR : 1];
   const int tid = threadIdx.x % TPR, r = threadIdx.x / TPR;
+  // the widest rows leave no registers for a row ahead; their weight is read per row
+  constexpr bool kAhead = NV <= 2;
   float w[NV][8], dw[NV][8], db[NV][8];
-  load_vector<kWBf16, TPR, NV>(p.weight, tid, p.H, 1.f, w);
+  if constexpr (kAhead) load_vector<kWBf16, TPR, NV>(p.weight, tid, p.H, 1.f, w);
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int u = 0; u < 8; ++u) dw[j][u] = db[j][u] = 0.f;
   const float inv_h = 1.f / static_cast<float>(p.H);
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * R; base < p.T; base += static_cast<int64_t>(gridDim.x) * R) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * R;
+  RawRow<kBf16, NV> xr, gr, sr, sr_now;
+  if constexpr (kAhead) {
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * R + r;
+    load_row<kBf16, TPR, NV>(p.x, row, p.T, p.H, tid, xr);
+    load_row<kBf16, TPR, NV>(p.d_y, row, p.T, p.H, tid, gr);
+    load_row<kBf16, TPR, NV>(p.d_skip, row, p.T, p.H, tid, sr);
+  }
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * R; base < p.T; base += step) {
     const int64_t row = base + r;
     const bool active = row < p.T;
-    const int64_t at = (active ? row : 0) * p.H;
+    if constexpr (!kAhead) {
+      load_row<kBf16, TPR, NV>(p.x, row, p.T, p.H, tid, xr);
+      load_row<kBf16, TPR, NV>(p.d_y, row, p.T, p.H, tid, gr);
+    }
     float v[NV][8], g[NV][8];
     float sum[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + tid) * 8;
-      const int n = active ? p.H - c : 0;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) v[j][u] = g[j][u] = 0.f;
-      if (n > 0) {
-        unpack8<kBf16>(load8_part<kBf16>(p.x, at + c, n), v[j]);
-        unpack8<kBf16>(load8_part<kBf16>(p.d_y, at + c, n), g[j]);
-      }
+      unpack8<kBf16>(xr.piece[j], v[j]);
+      unpack8<kBf16>(gr.piece[j], g[j]);
 #pragma unroll
       for (int u = 0; u < 8; ++u) sum[0] += v[j][u];
+    }
+    // the next row is on its way while this one is reduced
+    if constexpr (kAhead) {
+      sr_now = sr;
+      load_row<kBf16, TPR, NV>(p.x, row + step, p.T, p.H, tid, xr);
+      load_row<kBf16, TPR, NV>(p.d_y, row + step, p.T, p.H, tid, gr);
+      load_row<kBf16, TPR, NV>(p.d_skip, row + step, p.T, p.H, tid, sr);
     }
     row_sum<TPR, 1>(sum, part[0]);
     const float mean = sum[0] * inv_h;
@@ -192,6 +230,7 @@ __global__ __launch_bounds__(TPR* R) void norm_backward_kernel(NormBwdArgs p) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int n = p.H - (j * TPR + tid) * 8;
+      if constexpr (!kAhead) load_piece<kWBf16>(p.weight, p.H - n, n, 1.f, w[j]);
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         v[j][u] = u < n ? v[j][u] - mean : 0.f;
@@ -213,10 +252,12 @@ __global__ __launch_bounds__(TPR* R) void norm_backward_kernel(NormBwdArgs p) {
       const int n = active ? p.H - c : 0;
       if (n <= 0) continue;
       float d[8];
-      if (p.d_skip) unpack8<kBf16>(load8_part<kBf16>(p.d_skip, at + c, n), d);
-      else
-#pragma unroll
-        for (int u = 0; u < 8; ++u) d[u] = 0.f;
+      if constexpr (kAhead) {
+        unpack8<kBf16>(sr_now.piece[j], d);
+      } else {
+        load_piece<kBf16>(p.d_skip, row * p.H + c, n, 0.f, d);
+        load_piece<kWBf16>(p.weight, c, n, 1.f, w[j]);
+      }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const float hat = (v[j][u] - shift) * rstd;
@@ -224,7 +265,7 @@ __global__ __launch_bounds__(TPR* R) void norm_backward_kernel(NormBwdArgs p) {
         dw[j][u] = fmaf(g[j][u], hat, dw[j][u]);
         db[j][u] += g[j][u];
       }
-      store8_part<kBf16>(p.d_x, at + c, n, d);
+      store8_part<kBf16>(p.d_x, row * p.H + c, n, d);
     }
   }
   if (!p.partial) return;
@@ -262,55 +303,67 @@ __global__ __launch_bounds__(TPR* R) void norm_backward_kernel(NormBwdArgs p) {
   }
 }
 
-// d_weight and d_bias from the blocks' column sums: 64 columns of one of the
-// two per block, 16 threads of 4 columns by 16 groups of blocks, added in order.
+// d_weight and d_bias from the blocks' column sums: 16 columns of one of the two
+// per block, 4 threads of 4 columns by 64 groups of blocks, added in a fixed order.
 template <bool kWBf16>
 __global__ __launch_bounds__(256) void norm_columns_kernel(const float* __restrict__ partial, int blocks, int H,
                                                            int Hp, void* __restrict__ d_weight,
                                                            void* __restrict__ d_bias) {
-  __shared__ float4 part[16][16];
+  __shared__ float4 part[64][4];
   void* out = blockIdx.y ? d_bias : d_weight;
   if (!out) return;
-  const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
-  const int c = blockIdx.x * 64 + x * 4;
+  const int x = threadIdx.x & 3, y = threadIdx.x >> 2;
+  const int c = blockIdx.x * 16 + x * 4;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (c < Hp)
-    for (int b = y; b < blocks; b += 16) {
-      const float4 v = *reinterpret_cast<const float4*>(partial + (static_cast<int64_t>(b) * 2 + blockIdx.y) * Hp + c);
+  if (c < Hp) {
+    const float* col = partial + static_cast<int64_t>(blockIdx.y) * Hp + c;
+#pragma unroll 4
+    for (int b = y; b < blocks; b += 64) {
+      const float4 v = *reinterpret_cast<const float4*>(col + static_cast<int64_t>(b) * 2 * Hp);
       a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
     }
-  part[y][x] = a;
-  __syncthreads();
-  if (y != 0) return;
-  for (int k = 1; k < 16; ++k) {
-    const float4 v = part[k][x];
-    a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
   }
+  part[y][x] = a;
+#pragma unroll
+  for (int s = 32; s >= 1; s >>= 1) {
+    __syncthreads();
+    if (y < s) {
+      const float4 v = part[y + s][x];
+      a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+      part[y][x] = a;
+    }
+  }
+  if (y != 0) return;
   const float v[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
   for (int u = 0; u < 4; ++u)
     if (c + u < H) store1<kWBf16>(out, c + u, v[u]);
 }
 
-// threads per row for a width: at most 16 elements a thread
+// Threads per row and pieces a thread for a width.  In the widest rows the forward
+// pass takes 16 waves with 2 pieces (bf16 2048 x 16384: 69 us, 8 waves with 4: 90),
+// the backward pass, whose sums then spill, 8 waves with 4 (99 us against 125).
 struct Shape {
   int tpr, nv;
 };
-Shape shape_of(int H) {
+Shape shape_of(int H, bool backward) {
   if (H <= 512) return {64, 1};
   if (H <= 1024) return {64, 2};
   if (H <= 2048) return {256, 1};
   if (H <= 4096) return {256, 2};
   if (H <= 8192) return {512, 2};
-  return {1024, 2};
+  return backward ? Shape{512, 4} : Shape{1024, 2};
 }
 
-constexpr int kFwdThreads = 256, kBwdThreads = 512;
-constexpr int kFwdBlocks = 2048, kBwdBlocks = 512;
+constexpr int kFwdThreads = 256, kBwdThreads = 256;
+constexpr int kFwdBlocks = 2048, kCUs = 256;
 
+// As many blocks as the card holds at once, so that none waits for another, and
+// not more than the rows fill.
 int bwd_blocks(int64_t T, int H) {
-  const int rows = std::max(1, kBwdThreads / shape_of(H).tpr);
-  return static_cast<int>(std::min<int64_t>(kBwdBlocks, moe::ceil_div(T, rows)));
+  const Shape sh = shape_of(H, true);
+  const int rows = std::max(1, kBwdThreads / sh.tpr);
+  return static_cast<int>(std::min<int64_t>(kCUs * bwd_blocks_per_cu(sh.tpr, sh.nv), moe::ceil_div(T, rows)));
 }
 int padded(int H) { return static_cast<int>(moe::ceil_div(H, 8) * 8); }
 
@@ -327,14 +380,14 @@ void launch_norm_backward(const NormBwdArgs& p, hipStream_t s) {
   norm_backward_kernel<kBf16, kWBf16, TPR, NV, R><<<bwd_blocks(p.T, p.H), TPR * R, 0, s>>>(p);
 }
 
-#define MOE_NORM_BY_SHAPE(fn, a, b)                        \
-  switch (shape_of(p.H).tpr * 4 + shape_of(p.H).nv) {      \
-    case 64 * 4 + 1: fn<a, b, 64, 1>(p, s); break;         \
-    case 64 * 4 + 2: fn<a, b, 64, 2>(p, s); break;         \
-    case 256 * 4 + 1: fn<a, b, 256, 1>(p, s); break;       \
-    case 256 * 4 + 2: fn<a, b, 256, 2>(p, s); break;       \
-    case 512 * 4 + 2: fn<a, b, 512, 2>(p, s); break;       \
-    default: fn<a, b, 1024, 2>(p, s); break;               \
+#define MOE_NORM_BY_SHAPE(fn, backward, a, b)                                  \
+  switch (const Shape sh = shape_of(p.H, backward); sh.tpr * 8 + sh.nv) {      \
+    case 64 * 8 + 1: fn<a, b, 64, 1>(p, s); break;                             \
+    case 64 * 8 + 2: fn<a, b, 64, 2>(p, s); break;                             \
+    case 256 * 8 + 1: fn<a, b, 256, 1>(p, s); break;                           \
+    case 256 * 8 + 2: fn<a, b, 256, 2>(p, s); break;                           \
+    case 512 * 8 + 2: fn<a, b, 512, 2>(p, s); break;                           \
+    default: fn<a, b, backward ? 512 : 1024, backward ? 4 : 2>(p, s); break;   \
   }
 
 int check_norm(const char* who, moe_dtype dt, moe_dtype w_dt, int64_t T, int H, float eps) {
@@ -368,9 +421,9 @@ extern "C" int moe_layer_norm(const void* x, const void* residual, moe_dtype dt,
     return fail(MOE_ERR_INVALID_ARG, "moe_layer_norm: misaligned weight or bias");
   const NormArgs p{x, residual, weight, bias, x_sum, y, T, H, eps};
   const hipStream_t s = as_stream(stream);
-  if (dt == MOE_F32) { MOE_NORM_BY_SHAPE(launch_norm, false, false) }
-  else if (w_dt == MOE_F32) { MOE_NORM_BY_SHAPE(launch_norm, true, false) }
-  else { MOE_NORM_BY_SHAPE(launch_norm, true, true) }
+  if (dt == MOE_F32) { MOE_NORM_BY_SHAPE(launch_norm, false, false, false) }
+  else if (w_dt == MOE_F32) { MOE_NORM_BY_SHAPE(launch_norm, false, true, false) }
+  else { MOE_NORM_BY_SHAPE(launch_norm, false, true, true) }
   return hip_status(hipGetLastError(), "moe_layer_norm launch");
 }
 
@@ -405,13 +458,13 @@ extern "C" int moe_layer_norm_backward(const void* d_y, const void* x, moe_dtype
   if (T > 0) {
     const NormBwdArgs p{d_y, x, weight, d_skip, d_x, columns ? static_cast<float*>(workspace) : nullptr,
                         T, H, padded(H), eps};
-    if (dt == MOE_F32) { MOE_NORM_BY_SHAPE(launch_norm_backward, false, false) }
-    else if (w_dt == MOE_F32) { MOE_NORM_BY_SHAPE(launch_norm_backward, true, false) }
-    else { MOE_NORM_BY_SHAPE(launch_norm_backward, true, true) }
+    if (dt == MOE_F32) { MOE_NORM_BY_SHAPE(launch_norm_backward, true, false, false) }
+    else if (w_dt == MOE_F32) { MOE_NORM_BY_SHAPE(launch_norm_backward, true, true, false) }
+    else { MOE_NORM_BY_SHAPE(launch_norm_backward, true, true, true) }
     if (int rc = hip_status(hipGetLastError(), "moe_layer_norm_backward launch")) return rc;
   }
   if (columns) {
-    const dim3 grid(static_cast<unsigned>(ceil_div(H, 64)), 2);
+    const dim3 grid(static_cast<unsigned>(ceil_div(H, 16)), 2);
     const float* part = static_cast<const float*>(workspace);
     if (w_dt == MOE_BF16) norm_columns_kernel<true><<<grid, 256, 0, s>>>(part, blocks, H, padded(H), d_weight, d_bias);
     else norm_columns_kernel<false><<<grid, 256, 0, s>>>(part, blocks, H, padded(H), d_weight, d_bias);

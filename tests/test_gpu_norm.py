@@ -1,7 +1,8 @@
 """moe_layer_norm and moe_layer_norm_backward against the float64 oracle.
 
 Tolerances, with u = 2^-24.  A row's sum in float32 goes over at most 16 values
-a thread, 6 steps of a wave and 16 waves: n = 38 roundings.  The mean's error is
+a thread, 6 steps of a wave and 16 waves, or 32 values, 6 steps and 8 waves: n = 46
+roundings at most (38 in the forward pass).  The mean's error is
 made good by the sum of the deviations, which itself errs by n u mean|d|.  So
 n^ = (x - mean) rstd errs by at most (n/2 + 8) u |n^| + 2 n u: y = n^ w + b by
 64 u ((|n^| + 1) |w| + |b|), plus half a step of the type.  The deviations are
