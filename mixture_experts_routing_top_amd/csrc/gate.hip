@@ -287,6 +287,27 @@ __device__ __forceinline__ double quotient(double a, double b) {
   return fma(fma(-b, q, a), r, q);
 }
 
+// exp(x) for x <= 0 (0 below -745) to about 1e-11: far closer than the float a
+// weight is rounded to, in half the instructions of the full function.  With
+// x = (n + f) ln 2, |f| <= 1/2, it is 2^n times the exponential series in f ln 2,
+// whose terms end at (ln 2 / 2)^9 / 9!.
+__device__ __forceinline__ double exp_of(double x) {
+  const double t = fmax(x, -800.0) * 1.4426950408889634;
+  const double n = rint(t);
+  const double r = (t - n) * 0.6931471805599453;
+  double e = 1.0 / 362880.0;
+  e = fma(e, r, 1.0 / 40320.0);
+  e = fma(e, r, 1.0 / 5040.0);
+  e = fma(e, r, 1.0 / 720.0);
+  e = fma(e, r, 1.0 / 120.0);
+  e = fma(e, r, 1.0 / 24.0);
+  e = fma(e, r, 1.0 / 6.0);
+  e = fma(e, r, 0.5);
+  e = fma(e, r, 1.0);
+  e = fma(e, r, 1.0);
+  return ldexp(e, static_cast<int>(n));
+}
+
 enum By { kByLogit, kBySigmoid, kBySoftmax };          // what the selection compares
 enum Weights { kSoftmaxKept, kSoftmaxAll, kSigmoids };  // softmax over the kept logits, over all; sigmoids
 
@@ -397,7 +418,7 @@ __global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, i
         sum64 = 0.0;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          sum64 += exp(static_cast<double>(l[j]) - static_cast<double>(m));
+          sum64 += exp_of(static_cast<double>(l[j]) - static_cast<double>(m));
           __builtin_amdgcn_sched_barrier(0);   // one exponential's registers at a time
         }
         sum64 = row_sum(sum64);
@@ -459,12 +480,11 @@ __global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, i
 
     // lane i takes the i-th key, lane k the best one left
     uint32_t best = 0, mine = 0;
-#pragma unroll
-    for (int i = 0; i <= moe::kMaxTopK; ++i)
-      if (i <= p.k) {
-        best = next_key<V>(key, best);
-        if (l16 == i) mine = best;
-      }
+#pragma unroll 1   // (a small call is bound by fetching its code)
+    for (int i = 0; i <= p.k; ++i) {
+      best = next_key<V>(key, best);
+      if (l16 == i) mine = best;
+    }
     const int e = min(255 - static_cast<int>(mine & 255u), p.E - 1);
     const bool some = l16 <= p.k && mine >= 768u;      // an unmasked expert
     // a logit too far below the largest is cut to a masked one's value as well
@@ -486,14 +506,14 @@ __global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, i
     const float top = row_max(on ? lk : -INFINITY);
     double w, sum = sum64;
     if constexpr (kW == kSigmoids) {
-      const double x = lk, z = exp(-fabs(x));          // s = 1 / (1 + z) or z / (1 + z)
+      const double x = lk, z = exp_of(-fabs(x));          // s = 1 / (1 + z) or z / (1 + z)
       double up = x > 0.0 ? 1.0 : z;
       // ratios survive where every sigmoid underflows: times exp(-top)
-      if (p.renorm && __any(top < -600.f) && top < 0.f) up = exp(x - static_cast<double>(top));
+      if (p.renorm && __any(top < -600.f) && top < 0.f) up = exp_of(x - static_cast<double>(top));
       w = on ? quotient(up, 1.0 + z) : 0.0;
       if (p.renorm) sum = row_sum(w);
     } else {
-      w = on ? exp(static_cast<double>(lk) - static_cast<double>(kW == kSoftmaxKept ? top : m)) : 0.0;
+      w = on ? exp_of(static_cast<double>(lk) - static_cast<double>(kW == kSoftmaxKept ? top : m)) : 0.0;
       if (kW == kSoftmaxKept) sum = row_sum(w);
     }
     w = sum > 0.0 ? p.scale * quotient(w, sum) : 0.0;
