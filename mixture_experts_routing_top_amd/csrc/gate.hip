@@ -103,10 +103,71 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// (no NaN reaches it: the middle of two values and infinity is the larger one,
+// without fmaxf's instruction more that quiets a signalling NaN)
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
+__device__ __forceinline__ float row_max(float v) {
+  v = larger(v, __int_as_float(dpp_partner<1>(__float_as_int(v))));
+  v = larger(v, __int_as_float(dpp_partner<2>(__float_as_int(v))));
+  v = larger(v, __int_as_float(dpp_partner<4>(__float_as_int(v))));
+  return larger(v, __int_as_float(dpp_partner<8>(__float_as_int(v))));
+}
+// exp(x) for x <= 0 (0 below -745) to about 1e-11: far closer than the float a
+// weight is rounded to, in half the instructions of the full function.  With
+// x = (n + f) ln 2, |f| <= 1/2, it is 2^n times the exponential series in f ln 2,
+// whose terms end at (ln 2 / 2)^9 / 9!.
+__device__ __forceinline__ double exp_of(double x) {
+  const double t = fmax(x, -800.0) * 1.4426950408889634;
+  const double n = rint(t);
+  const double r = (t - n) * 0.6931471805599453;
+  double e = 1.0 / 362880.0;
+  e = fma(e, r, 1.0 / 40320.0);
+  e = fma(e, r, 1.0 / 5040.0);
+  e = fma(e, r, 1.0 / 720.0);
+  e = fma(e, r, 1.0 / 120.0);
+  e = fma(e, r, 1.0 / 24.0);
+  e = fma(e, r, 1.0 / 6.0);
+  e = fma(e, r, 0.5);
+  e = fma(e, r, 1.0);
+  e = fma(e, r, 1.0);
+  return ldexp(e, static_cast<int>(n));
+}
+
+// a / b in double for b in the normal range, to about an ulp
+__device__ __forceinline__ double quotient(double a, double b) {
+  double r = __builtin_amdgcn_rcp(b);
+  r = fma(fma(-b, r, 1.0), r, r);
+  r = fma(fma(-b, r, 1.0), r, r);
+  const double q = a * r;
+  return fma(fma(-b, q, a), r, q);
+}
+
+// The weight of this lane's chosen expert (lanes 0 .. k - 1 of 16; `on` in those
+// whose expert is unmasked), from its logit lk; m and total: the largest logit of
+// the row and the sum of exp(l - m), for a softmax over all.
+__device__ __forceinline__ double chosen_weight(bool softmax, bool renorm, float scale, float lk, bool on, float m,
+                                                double total) {
+  const float top = row_max(on ? lk : -INFINITY);
+  double w;
+  if (softmax) {
+    w = on ? exp_of(static_cast<double>(lk) - static_cast<double>(renorm ? top : m)) : 0.0;
+  } else {
+    const double x = lk, z = exp_of(-fabs(x));          // s = 1 / (1 + z) or z / (1 + z)
+    double up = x > 0.0 ? 1.0 : z;
+    // ratios survive where every sigmoid underflows: times exp(-top)
+    if (renorm && __any(top < -600.f) && top < 0.f) up = exp_of(x - static_cast<double>(top));
+    w = on ? quotient(up, 1.0 + z) : 0.0;
+  }
+  const double sum = renorm ? row_sum(w) : softmax ? total : 1.0;
+  return sum > 0.0 ? scale * quotient(w, sum) : 0.0;
+}
+
+using LdsDoubles = __attribute__((address_space(3))) double;
+
 // One token by one wave: lane holds experts lane, lane + 64, ...  `value` is E
 // doubles of LDS of this wave.  Every lane of the wave calls it with the same t.
 template <bool kBf16, typename Args>
-__device__ __forceinline__ void gate_token(const Args& p, int64_t t, int lane, double* value) {
+__device__ __forceinline__ void gate_token(const Args& p, int64_t t, int lane, LdsDoubles* value) {
   const int64_t row = t * p.E;
   float l[4];
   double key[4];
@@ -128,21 +189,23 @@ __device__ __forceinline__ void gate_token(const Args& p, int64_t t, int lane, d
   const bool two = p.top2 && p.keep < p.n_groups;
   double s[4] = {0.0, 0.0, 0.0, 0.0};
   double total = 1.0;
-  if (p.softmax && (!p.renorm || p.bias || two)) {
-    m = static_cast<float>(wave_max(static_cast<double>(m)));
-    total = 0.0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      s[j] = live[j] ? exp(static_cast<double>(l[j]) - m) : 0.0;
-      total += s[j];
+  if (p.bias || two || (p.softmax && !p.renorm)) {
+    if (p.softmax) {
+      m = static_cast<float>(wave_max(static_cast<double>(m)));
+      if (m == -INFINITY) m = 0.f;   // nothing unmasked
+      total = 0.0;
     }
-    total = wave_sum(total);
-  }
-  if (p.bias || two) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (p.softmax) s[j] = total > 0.0 ? s[j] / total : 0.0;
-      else s[j] = live[j] ? 1.0 / (1.0 + exp(-static_cast<double>(l[j]))) : 0.0;
+      const double x = l[j];
+      const double z = exp(p.softmax ? x - m : -fabs(x));   // 0 where masked
+      if (p.softmax) total += s[j] = z;
+      else s[j] = (x > 0.0 ? 1.0 : z) / (1.0 + z);
+    }
+    if (p.softmax) {
+      total = wave_sum(total);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] = total > 0.0 ? s[j] / total : 0.0;
     }
   }
 #pragma unroll
@@ -158,12 +221,18 @@ __device__ __forceinline__ void gate_token(const Args& p, int64_t t, int lane, d
     // lane g scores group g; a group stays if fewer than `keep` are ahead of it
     wave_lds_fence();
     double best = -INFINITY, second = -INFINITY;
-    if (lane < p.n_groups)
-      for (int i = 0; i < p.group_size; ++i) {
-        const double v = value[lane * p.group_size + i];
-        if (v > best) { second = best; best = v; }
-        else if (v > second) second = v;
-      }
+    for (int i = 0; i < p.group_size; i += 8) {
+      double v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)   // (8 reads in flight; lanes without a group read the last value)
+        v[u] = value[min(lane * p.group_size + min(i + u, p.group_size - 1), p.E - 1)];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i + u < p.group_size) {
+          second = fmax(second, fmin(best, v[u]));
+          best = fmax(best, v[u]);
+        }
+    }
     const double score = two && second > -INFINITY ? best + second : best;
     int rank = 0;
     for (int g = 0; g < p.n_groups; ++g) {
@@ -198,23 +267,16 @@ __device__ __forceinline__ void gate_token(const Args& p, int64_t t, int lane, d
   float lk = -INFINITY;
   if (lane < p.k) lk = load_logit<kBf16>(p.logits, row + mine);
   const bool on = lane < p.k && is_live(lk);
-  lk = on ? fminf(lk, FLT_MAX) : -INFINITY;
-  double v;
-  if (p.softmax) {
-    const double top = p.renorm ? wave_max(static_cast<double>(lk)) : static_cast<double>(m);
-    v = on ? exp(lk - top) : 0.0;
-  } else {
-    // with renormalisation, times exp(-top), top = min(0, the largest logit):
-    // the ratios survive where every sigmoid underflows
-    const double top = p.renorm ? fmin(wave_max(static_cast<double>(lk)), 0.0) : 0.0;
-    const double x = lk;
-    v = !on ? 0.0 : x > 0.0 ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / (1.0 + exp(x));
-  }
-  const double sum = p.renorm ? wave_sum(v) : total;
+  const double w = chosen_weight(p.softmax, p.renorm, p.scale, on ? fminf(lk, FLT_MAX) : -INFINITY, on, m, total);
   if (lane < p.k) {
     p.idx[t * p.k + lane] = mine;
-    p.w[t * p.k + lane] = static_cast<float>(sum > 0.0 ? p.scale * (v / sum) : 0.0);
+    p.w[t * p.k + lane] = static_cast<float>(w);
   }
+}
+
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  return static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32)))) << 32 | lo;
 }
 
 // gate_token called, not inlined, from a loop that few tokens leave: its double
@@ -222,20 +284,14 @@ __device__ __forceinline__ void gate_token(const Args& p, int64_t t, int lane, d
 // read from the kernel's own (its first parameter), so nothing is copied for it.
 using KernelArgs = const __attribute__((address_space(4))) GateArgs;
 template <bool kBf16>
-__device__ __noinline__ void gate_token_call(KernelArgs* p, int64_t t, double* value) {
-  gate_token<kBf16>(*p, t, threadIdx.x & 63, value);
+__device__ __noinline__ void gate_token_call(KernelArgs* p, int64_t t, LdsDoubles* value) {
+  // a function's arguments come in vector registers: they are the wave's all the same
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
+  p = reinterpret_cast<KernelArgs*>(uniform64(at));
+  gate_token<kBf16>(*p, static_cast<int64_t>(uniform64(static_cast<uint64_t>(t))), threadIdx.x & 63, value);
 }
 
 // ------------------------------------------------------------ 16 lanes a token
-// (no NaN reaches it: the middle of two values and infinity is the larger one,
-// without fmaxf's instruction more that quiets a signalling NaN)
-__device__ __forceinline__ float larger(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
-__device__ __forceinline__ float row_max(float v) {
-  v = larger(v, __int_as_float(dpp_partner<1>(__float_as_int(v))));
-  v = larger(v, __int_as_float(dpp_partner<2>(__float_as_int(v))));
-  v = larger(v, __int_as_float(dpp_partner<4>(__float_as_int(v))));
-  return larger(v, __int_as_float(dpp_partner<8>(__float_as_int(v))));
-}
 __device__ __forceinline__ uint32_t row_max(uint32_t v) {
   v = max(v, static_cast<uint32_t>(dpp_partner<1>(v)));
   v = max(v, static_cast<uint32_t>(dpp_partner<2>(v)));
@@ -278,36 +334,6 @@ __device__ __forceinline__ uint32_t next_key(const uint32_t (&key)[V], uint32_t 
   return best + row_max(d);
 }
 
-// a / b in double for b in the normal range, to about an ulp
-__device__ __forceinline__ double quotient(double a, double b) {
-  double r = __builtin_amdgcn_rcp(b);
-  r = fma(fma(-b, r, 1.0), r, r);
-  r = fma(fma(-b, r, 1.0), r, r);
-  const double q = a * r;
-  return fma(fma(-b, q, a), r, q);
-}
-
-// exp(x) for x <= 0 (0 below -745) to about 1e-11: far closer than the float a
-// weight is rounded to, in half the instructions of the full function.  With
-// x = (n + f) ln 2, |f| <= 1/2, it is 2^n times the exponential series in f ln 2,
-// whose terms end at (ln 2 / 2)^9 / 9!.
-__device__ __forceinline__ double exp_of(double x) {
-  const double t = fmax(x, -800.0) * 1.4426950408889634;
-  const double n = rint(t);
-  const double r = (t - n) * 0.6931471805599453;
-  double e = 1.0 / 362880.0;
-  e = fma(e, r, 1.0 / 40320.0);
-  e = fma(e, r, 1.0 / 5040.0);
-  e = fma(e, r, 1.0 / 720.0);
-  e = fma(e, r, 1.0 / 120.0);
-  e = fma(e, r, 1.0 / 24.0);
-  e = fma(e, r, 1.0 / 6.0);
-  e = fma(e, r, 0.5);
-  e = fma(e, r, 1.0);
-  e = fma(e, r, 1.0);
-  return ldexp(e, static_cast<int>(n));
-}
-
 enum By { kByLogit, kBySigmoid, kBySoftmax };          // what the selection compares
 enum Weights { kSoftmaxKept, kSoftmaxAll, kSigmoids };  // softmax over the kept logits, over all; sigmoids
 
@@ -317,11 +343,12 @@ constexpr float kTop = 16777200.f;     // the largest fixed-point value, below 2
 // Lane i of a token's 16 holds `per` consecutive experts (at most V) of one group:
 // groups begin at multiples of `lanes` lanes.  A wave takes 4 tokens at a time.
 template <bool kBf16, int V, By kBy, Weights kW>
-__global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, int lanes, int per) {
+__global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, int lanes_log2, int per) {
   __shared__ double value[4][moe::kMaxExperts];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l16 = lane & 15;
-  const int group = l16 / lanes;                      // == p.n_groups or more: an idle lane
-  const int inside = (l16 % lanes) * per;
+  const int lanes = 1 << lanes_log2;
+  const int group = l16 >> lanes_log2;                // == p.n_groups or more: an idle lane
+  const int inside = (l16 & (lanes - 1)) * per;
   const int e0 = group * p.group_size + inside;
   const int n = group < p.n_groups ? max(0, min(per, p.group_size - inside)) : 0;   // this lane's experts
   const int64_t total = p.T * p.E;
@@ -340,17 +367,21 @@ __global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, i
   float offset = 3.f + kTop;    // only equal keys of unequal logits are in doubt
   float near = 0.f, group_near = 0.f;
 #pragma unroll
-  for (int j = 0; j < V; ++j) b[j] = j >= n ? -INFINITY : kBy != kByLogit && p.bias ? p.bias[e0 + j] : 0.f;
+  for (int j = 0; j < V; ++j) b[j] = 0.f;
+  if (kBy != kByLogit && p.bias)
+#pragma unroll
+    for (int j = 0; j < V; ++j) b[j] = p.bias[min(e0 + j, p.E - 1)];
+#pragma unroll
+  for (int j = 0; j < V; ++j) b[j] = j < n ? b[j] : -INFINITY;
   if constexpr (kBy != kByLogit) {
     float lo = INFINITY, hi = -INFINITY;
     bool odd = false;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (j < n) {
-        odd |= !(fabsf(b[j]) <= 1e30f);
-        lo = fminf(lo, b[j]);
-        hi = fmaxf(hi, b[j]);
-      }
+    for (int j = 0; j < V; ++j) {
+      odd |= (j < n) & !(fabsf(b[j]) <= 1e30f);
+      lo = fminf(lo, j < n ? b[j] : INFINITY);
+      hi = fmaxf(hi, b[j]);
+    }
     if (odd) lo = hi = INFINITY;     // left to the doubles
     lo = -row_max(-lo);
     hi = row_max(hi);
@@ -384,12 +415,12 @@ __global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, i
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < V; ++j) l[j] = j < n ? load_logit<kBf16>(p.logits, at + j) : -INFINITY;
+      for (int j = 0; j < V; ++j) l[j] = load_logit<kBf16>(p.logits, min(at + j, total - 1));
     }
     if (p.check) {
       bool bad = false;
 #pragma unroll
-      for (int j = 0; j < V; ++j) bad |= j < n && (l[j] != l[j] || l[j] == INFINITY);
+      for (int j = 0; j < V; ++j) bad |= (j < n) & ((l[j] != l[j]) | (l[j] == INFINITY));
       raise_check(p.check, bad && active, MOE_CHECK_LOGITS);
     }
 
@@ -502,21 +533,8 @@ __global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, i
     const bool redo = (doubts >> (lane & 48)) & 0xffffu;
 
     // weights in double, rounded once
-    const bool on = some && l16 < p.k;
-    const float top = row_max(on ? lk : -INFINITY);
-    double w, sum = sum64;
-    if constexpr (kW == kSigmoids) {
-      const double x = lk, z = exp_of(-fabs(x));          // s = 1 / (1 + z) or z / (1 + z)
-      double up = x > 0.0 ? 1.0 : z;
-      // ratios survive where every sigmoid underflows: times exp(-top)
-      if (p.renorm && __any(top < -600.f) && top < 0.f) up = exp_of(x - static_cast<double>(top));
-      w = on ? quotient(up, 1.0 + z) : 0.0;
-      if (p.renorm) sum = row_sum(w);
-    } else {
-      w = on ? exp_of(static_cast<double>(lk) - static_cast<double>(kW == kSoftmaxKept ? top : m)) : 0.0;
-      if (kW == kSoftmaxKept) sum = row_sum(w);
-    }
-    w = sum > 0.0 ? p.scale * quotient(w, sum) : 0.0;
+    const double w = chosen_weight(kW != kSigmoids, kW == kSigmoids ? p.renorm : kW == kSoftmaxKept, p.scale, lk,
+                                   some && l16 < p.k, m, sum64);
     if (active && !redo && l16 < p.k) {
       p.idx[t * p.k + l16] = e;
       p.w[t * p.k + l16] = static_cast<float>(w);
@@ -525,7 +543,7 @@ __global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, i
 #pragma unroll 1
       for (int i = 0; i < 4; ++i)
         if ((doubts >> (16 * i)) & 0xffffu)
-          gate_token_call<kBf16>((KernelArgs*)__builtin_amdgcn_kernarg_segment_ptr(), base + i, value[wave]);
+          gate_token_call<kBf16>((KernelArgs*)__builtin_amdgcn_kernarg_segment_ptr(), base + i, (LdsDoubles*)value[wave]);
   }
 }
 
@@ -536,25 +554,25 @@ __global__ __launch_bounds__(256) void gate_wave_kernel(GateArgs p) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave;
   if (t >= p.T) return;
-  gate_token<kBf16>(p, t, lane, value[wave]);
+  gate_token<kBf16>(p, t, lane, (LdsDoubles*)value[wave]);
 }
 
 template <bool kBf16, By kBy, Weights kW>
 void launch_slots(GateArgs p, hipStream_t s) {
-  int lanes = 16;
+  int lanes_log2 = 4;
   if (p.keep == p.n_groups) {
     p.n_groups = p.keep = 1;
     p.group_size = p.E;
   }
-  while (16 / lanes < p.n_groups) lanes /= 2;
-  const int per = static_cast<int>(moe::ceil_div(p.group_size, lanes));
+  while ((16 >> lanes_log2) < p.n_groups) --lanes_log2;
+  const int per = static_cast<int>(moe::ceil_div(p.group_size, 1 << lanes_log2));
   const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(1024, moe::ceil_div(p.T, 16)));
-  if (per <= 2) gate_kernel<kBf16, 2, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes, per);
-  else if (per <= 4) gate_kernel<kBf16, 4, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes, per);
-  else if (per <= 8) gate_kernel<kBf16, 8, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes, per);
-  else if (per <= 12) gate_kernel<kBf16, 12, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes, per);
-  else if (per <= 16) gate_kernel<kBf16, 16, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes, per);
-  else gate_kernel<kBf16, 32, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes, per);
+  if (per <= 2) gate_kernel<kBf16, 2, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes_log2, per);
+  else if (per <= 4) gate_kernel<kBf16, 4, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes_log2, per);
+  else if (per <= 8) gate_kernel<kBf16, 8, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes_log2, per);
+  else if (per <= 12) gate_kernel<kBf16, 12, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes_log2, per);
+  else if (per <= 16) gate_kernel<kBf16, 16, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes_log2, per);
+  else gate_kernel<kBf16, 32, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes_log2, per);
 }
 
 template <bool kBf16>
