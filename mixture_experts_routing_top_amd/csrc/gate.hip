@@ -633,6 +633,15 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GateBwdArgs p) {
   const int64_t row = (active ? t : 0) * p.E;
   float4* mine = parts[threadIdx.x >> 4];
 
+  rows::Raw8<kBf16> raw[kPieces];
+  if constexpr (kDense)
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) {
+      const int at = c * 128 + l16 * 8;
+      raw[c] = {};
+      if (active && at < p.E) raw[c] = rows::load8_part<kBf16>(p.logits, row + at, p.E - at);
+    }
+
   // lanes 0 .. k - 1: the slot's expert, gradient and logit
   int e = -1;
   float g = 0.f, lk = -INFINITY;
@@ -657,8 +666,8 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GateBwdArgs p) {
   if constexpr (kDense) {
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
-      const int at = c * 128 + l16 * 8, n = active ? p.E - at : 0;
-      if (n > 0) rows::unpack8<kBf16>(rows::load8_part<kBf16>(p.logits, row + at, n), l[c]);
+      const int n = active ? p.E - (c * 128 + l16 * 8) : 0;
+      rows::unpack8<kBf16>(raw[c], l[c]);
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         l[c][u] = u < n && is_live(l[c][u]) ? fminf(l[c][u], FLT_MAX) : -INFINITY;
