@@ -64,6 +64,9 @@ def parse():
                     help="time moe_stats with co-occurrence (a chained layer) on the workloads' shapes")
     ap.add_argument("--backward", action="store_true",
                     help="time the layer's backward pass (moe_backward) on the Mixtral layer")
+    ap.add_argument("--train", action="store_true",
+                    help="time a training step of the DeepSeek-V2-shaped layer (grouped gate, residual norm, "
+                         "backward, clipping) and each of its operators")
     ap.add_argument("--pipeline", action="store_true",
                     help="horizontal-split pipeline and memory kernels on CU-masked streams (Mixtral layer)")
     ap.add_argument("--predict", action="store_true",
@@ -766,6 +769,61 @@ def backward_bench(moe, synth, torch, np, steps=5, warmup=2):
                          "workspace_gb": round(ws.numel() / 1e9, 2)}}
 
 
+def train_bench(moe, synth, torch, np, steps=5, warmup=2):
+    """A training step of the DeepSeek-V2-shaped layer: the 160 experts in 8 groups of
+    which a token reaches 3, unnormalised softmax weights, the residual sum and its
+    layer norm, every gradient, and the weights' gradients clipped to norm 1.  Random
+    weights and gradients; each operator is also timed alone."""
+    cfg = synth.CONFIGS["dsv2"]
+    T, H, I, E, k = cfg.T, cfg.H, cfg.I, cfg.E, cfg.k
+    dev = torch.device("cuda:0")
+    gen = torch.Generator(device=dev).manual_seed(0)
+
+    def rnd(*shape, scale=1.0, dtype=torch.bfloat16):
+        return torch.randn(shape, generator=gen, device=dev, dtype=dtype).mul_(scale)
+
+    wts = [rnd(E, I, H, scale=H ** -0.5), rnd(E, I, H, scale=H ** -0.5), rnd(E, H, I, scale=I ** -0.5)]
+    x, d_out, d_sum = rnd(T, H), rnd(T, H, scale=0.1), rnd(T, H, scale=0.1)
+    logits = torch.from_numpy(synth.logits(cfg, 0, 0)).to(dev)
+    gate = dict(score="softmax", n_groups=8, keep_groups=3, renorm=False, scale=16.0)
+    norm = dict(weight=1 + rnd(H, scale=0.1, dtype=torch.float32), bias=rnd(H, scale=0.1, dtype=torch.float32))
+    bufs = {}
+    ws = torch.empty(moe.moe_backward_workspace_bytes(torch.bfloat16, T, k, H, I, E), dtype=torch.uint8, device=dev)
+    state = {}
+
+    def step():
+        state["f"] = f = moe.moe_layer_forward(x, logits, k, *wts, cfg.act, copy_rows=True, bufs=bufs, gate=gate,
+                                               norm=norm, residual=x)
+        state["b"] = moe.moe_layer_backward(f, logits, *wts, d_out, cfg.act, gate=gate, norm=norm, d_x_sum=d_sum,
+                                            max_norm=1.0, workspace=ws)
+
+    def timed(fn):
+        for _ in range(warmup):
+            fn()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(steps):
+            fn()
+        b.record()
+        torch.cuda.synchronize()
+        return round(a.elapsed_time(b) / steps, 4)
+
+    ms = timed(step)
+    f, b = state["f"], state["b"]
+    grads = [b[key] for key in ("d_w_gate", "d_w_up", "d_w_down", "d_weight", "d_bias")]
+    norms = (0.5 ** i for i in range(1, 100))
+    parts = {"gate": lambda: moe.moe_gate(logits, k, **gate),
+             "gate_backward": lambda: moe.moe_gate_backward(logits, f["idx"], b["d_topk_w"], renorm=False, scale=16.0),
+             "layer_norm": lambda: moe.moe_layer_norm(f["out"], **norm, residual=x),
+             "layer_norm_backward": lambda: moe.moe_layer_norm_backward(d_out, f["x_sum"], **norm, d_skip=d_sum),
+             # (to half the last norm each time: what is at its norm already is only read)
+             "clip_grads": lambda: moe.moe_clip_grads(grads, next(norms))}
+    return {"train": {"workload": f"DeepSeek-V2-shaped layer T={T} H={H} I={I} E={E} k={k} bf16", "ms": ms,
+                      "tokens_per_s": round(T / (ms * 1e-3), 1),
+                      "clipped_gb": round(sum(g.numel() * g.element_size() for g in grads) / 1e9, 2),
+                      "operators_ms": {name: timed(fn) for name, fn in parts.items()}}}
+
+
 def vs_hipblaslt(moe, torch, np, reps=10):
     """The library's GEMMs next to the vendor library on the same dense shapes
     (one expert holding all M = 16384 rows, so no partial tiles): the gate/up GEMM
@@ -856,6 +914,9 @@ def main():
         return
     if a.backward:
         print(json.dumps(backward_bench(moe, synth, torch, np)), flush=True)
+        return
+    if a.train:
+        print(json.dumps(train_bench(moe, synth, torch, np)), flush=True)
         return
     if a.stats:
         print(json.dumps(stats_bench(moe, synth, torch, np)), flush=True)
