@@ -505,8 +505,8 @@ int moe_backward_gated(const void* x_perm, const void* y_perm, moe_dtype dt, int
  *   d_weight = sum over rows of d_y n, d_bias = sum over rows of d_y, in
  *         `w_dt`, summed in fp32 in an order that only T and H decide; either
  *         may be NULL.
- * The row's mean and rstd are formed again from x.  d_x may be d_y or d_skip
- * itself, not x.  Workspace (only where d_weight or d_bias is asked for and T > 0):
+ * The row's mean and rstd are formed again from x.  d_x may be d_y, d_skip
+ * or x itself.  Workspace (only where d_weight or d_bias is asked for and T > 0):
  * moe_layer_norm_backward_workspace_bytes(T, H) bytes, 16-byte aligned.
  */
 int moe_layer_norm(const void* x, const void* residual, moe_dtype dt, int64_t T, int H, const void* weight,

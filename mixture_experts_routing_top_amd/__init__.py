@@ -416,7 +416,11 @@ def _backward(name, gate_grad, x_perm, y_perm, topk_idx, topk_w, inv_pos, expert
         o["d_w_up"] = _out(o.get("d_w_up"), tuple(w_up.shape), w_up.dtype, dev, "d_w_up")
     o["d_w_down"] = _out(o.get("d_w_down"), tuple(w_down.shape), w_down.dtype, dev, "d_w_down")
     need = moe_backward_workspace_bytes(x_perm.dtype, T, k, H, I, E, act)
-    workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else \
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        if isinstance(stream, torch.cuda.Stream):   # it is freed on return, while that stream still uses it
+            workspace.record_stream(stream)
+    else:
         _bytes_of(workspace, need, "backward workspace")
     _call(name, _ptr(x_perm), _ptr(y_perm), _dtype_code(x_perm), ctypes.c_int64(T), k, H, I, E,
           _ptr(topk_idx), _ptr(topk_w), _ptr(inv_pos), _ptr(expert_off), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
@@ -601,8 +605,8 @@ def moe_layer_backward(fwd, logits, w_gate, w_up, w_down, d_out, act="swiglu", g
     same `norm` and `gate` dicts), else of fwd["out"]; d_x_sum the gradient that
     reaches fwd["x_sum"] otherwise (e.g. the next layer's residual).  Returns
     dict(d_x, d_logits, d_w_gate, d_w_up, d_w_down), with a norm also d_weight,
-    d_bias and, if the forward pass summed a residual, d_residual (d_x does not
-    hold it).  max_norm: the weights' gradients (experts and norm) are clipped in
+    d_bias, d_out (the gradient of fwd["out"]) and, if the forward pass summed a
+    residual, d_residual (the same tensor; d_x does not hold it).  max_norm: the weights' gradients (experts and norm) are clipped in
     place to that global norm, and the result holds grad_norm."""
     if fwd.get("x_perm") is None:
         raise ValueError("the forward pass must keep its rows: moe_layer_forward(copy_rows=True)")
@@ -611,7 +615,7 @@ def moe_layer_backward(fwd, logits, w_gate, w_up, w_down, d_out, act="swiglu", g
         summed = fwd.get("x_sum")
         n = moe_layer_norm_backward(d_out, fwd["out"] if summed is None else summed, norm.get("weight"),
                                     norm.get("bias"), norm.get("eps", 1e-5), d_skip=d_x_sum, stream=stream)
-        d_out = n["d_x"]
+        d_out = res["d_out"] = n["d_x"]
         res.update({key: n[key] for key in ("d_weight", "d_bias") if n[key] is not None})
         if summed is not None:
             res["d_residual"] = d_out

@@ -387,9 +387,10 @@ __global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, i
     hi = row_max(hi);
     const float range = 1.f + (hi - lo), big = fmaxf(fabsf(lo), fabsf(hi));
     // s: exp2's argument, exp2, the sum and the reciprocal, 6 u in all (u = 2^-24);
-    // a softmax's sum of up to 32 values in sequence and 4 steps: 36 u more.
-    // s + b rounds once more.  In the key: half a unit of fma, one of the cut.
-    const float err = (kBy == kBySigmoid ? 7.f : 43.f) + big;
+    // a softmax's sum of up to 32 values in sequence and 4 steps, 36 u more, and the
+    // terms' own errors in it, at most 10 u.  s + b rounds once more.  In the key: half
+    // a unit of fma, one of the cut.
+    const float err = (kBy == kBySigmoid ? 7.f : 53.f) + big;
     scale = kTop / range;
     offset = 4.f - lo * scale;
     near = 2.f * (err / range + 2.f);

@@ -48,7 +48,8 @@ def _check_gate(lg, k, bias=None, **kw):
 # E, n_groups, keep, k: one expert to 256, group sizes that divide nothing evenly
 SHAPES = [(1, 1, 1, 1), (2, 1, 1, 2), (8, 1, 1, 2), (9, 3, 2, 4), (16, 1, 1, 4), (31, 1, 1, 8), (64, 64, 8, 8),
           (64, 8, 3, 6), (65, 5, 2, 8), (96, 3, 1, 5), (128, 2, 1, 8), (160, 8, 3, 6), (160, 1, 1, 6), (203, 7, 4, 3),
-          (255, 5, 5, 7), (256, 8, 4, 8), (256, 1, 1, 1), (256, 32, 2, 8)]
+          (255, 5, 5, 7), (256, 8, 4, 8), (256, 1, 1, 1), (256, 32, 2, 8), (8, 1, 1, 8), (16, 16, 8, 8), (144, 9, 4, 8),
+          (208, 13, 5, 8), (256, 16, 3, 8), (256, 2, 1, 8), (252, 3, 2, 7), (240, 6, 1, 5)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -110,6 +111,29 @@ def test_gate_bias_extremes_keep_the_order_defined():
     lg[:, [i for i in range(16) if i not in (1, 2, 3, 7)]] = -math.inf
     idx, _ = moe.moe_gate(lg, 5, score="sigmoid", bias=bias)
     assert torch.all(idx[:, 2:] == torch.tensor([3, 7, 0], device="cuda"))
+
+
+@pytest.mark.parametrize("scale", [1e3, 1e8, 1e25, 1e34])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_wide_biases_and_logits(score, scale):
+    """Biases and logits whose spread leaves no float between close scores."""
+    T, E = 41, 72
+    rng = np.random.default_rng(int(math.log10(scale)))
+    small = (0.01 * rng.standard_normal(E)).astype(np.float32)
+    for bias in (small + np.float32(scale), np.where(np.arange(E) % 5 == 0, np.float32(scale), small),
+                 np.where(np.arange(E) % 7 == 0, np.float32(-scale), small)):
+        b = torch.from_numpy(bias.astype(np.float32)).cuda()
+        for G, keep, gs in ((1, 1, "max"), (8, 3, "max"), (8, 3, "top2")):
+            _check_gate(_logits(T, E, torch.float32, 3), 6, bias=b, score=score, n_groups=G, keep_groups=keep,
+                        group_score=gs, renorm=False)
+    wide = _logits(T, E, torch.float32, 4)
+    wide[:, ::3] *= -scale
+    wide[:, 1] += scale
+    for G, keep, gs in ((1, 1, "max"), (6, 2, "max"), (6, 2, "top2")):
+        for bias in (None, torch.from_numpy(small).cuda()):
+            for renorm in (False, True):
+                _check_gate(wide, 8, bias=bias, score=score, n_groups=G, keep_groups=keep, group_score=gs,
+                            renorm=renorm)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])

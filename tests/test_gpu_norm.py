@@ -203,8 +203,10 @@ def test_norm_in_place(T, H, dtype):
     dy2, skip2 = dy.clone(), skip.clone()
     d2 = moe.moe_layer_norm_backward(dy2, s, w, b, d_skip=skip, out={"d_x": dy2})
     d3 = moe.moe_layer_norm_backward(dy, s, w, b, d_skip=skip2, out={"d_x": skip2})
+    s4 = s.clone()
+    d4 = moe.moe_layer_norm_backward(dy, s4, w, b, d_skip=skip, out={"d_x": s4})
     for key in d:
-        assert torch.equal(d[key], d2[key]) and torch.equal(d[key], d3[key]), key
+        assert all(torch.equal(d[key], other[key]) for other in (d2, d3, d4)), key
 
 
 def test_norm_backward_against_differences():
