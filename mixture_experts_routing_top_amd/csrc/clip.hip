@@ -55,15 +55,9 @@ __device__ __forceinline__ int tensor_near(const GradList& l, int chunk, int at)
   return chunk >= l.first[at] && chunk < l.first[at + 1] ? at : tensor_of(l, chunk);
 }
 
-__device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
-  return v;
-}
-
 __device__ __forceinline__ double block_sum64(double v) {
   __shared__ double part[kThreads / 64];
-  v = wave_sum64(v);
+  v = wave_sum(v);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
   __syncthreads();
   double s = 0.0;

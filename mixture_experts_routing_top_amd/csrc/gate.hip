@@ -58,34 +58,12 @@ __device__ __forceinline__ bool ahead(double v1, int i1, double v2, int i2) {
   return v1 > v2 || (v1 == v2 && i1 < i2);
 }
 
-template <int OFF>
-__device__ __forceinline__ double partner64(double v) {
-  return __hiloint2double(dpp_partner<OFF>(__double2hiint(v)), dpp_partner<OFF>(__double2loint(v)));
-}
-__device__ __forceinline__ double lane64(double v, int lane) {
-  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), lane),
-                          __builtin_amdgcn_readlane(__double2loint(v), lane));
-}
-__device__ __forceinline__ double row_max(double v) {
-  v = fmax(v, partner64<1>(v));
-  v = fmax(v, partner64<2>(v));
-  v = fmax(v, partner64<4>(v));
-  return fmax(v, partner64<8>(v));
-}
-__device__ __forceinline__ double row_sum(double v) {
-  v += partner64<1>(v);
-  v += partner64<2>(v);
-  v += partner64<4>(v);
-  return v + partner64<8>(v);
-}
-__device__ __forceinline__ double wave_max(double v) {
-  v = row_max(v);
-  return fmax(fmax(lane64(v, 0), lane64(v, 16)), fmax(lane64(v, 32), lane64(v, 48)));
-}
-__device__ __forceinline__ double wave_sum(double v) {
-  v = row_sum(v);
-  return (lane64(v, 0) + lane64(v, 16)) + (lane64(v, 32) + lane64(v, 48));
-}
+using rows::lane64;
+using rows::row_max;
+using rows::row_sum;
+using rows::wave_max;
+using rows::wave_sum;
+
 // the smallest of some lanes' values
 __device__ __forceinline__ int least_of(uint64_t lanes, int v) {
   int least = INT32_MAX;

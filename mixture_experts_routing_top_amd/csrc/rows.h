@@ -95,4 +95,34 @@ __device__ __forceinline__ float wave_sum(float v) {
          (__int_as_float(__builtin_amdgcn_readlane(x, 32)) + __int_as_float(__builtin_amdgcn_readlane(x, 48)));
 }
 
+// Doubles: over the 16 lanes of a row, and over the wave.
+template <int OFF>
+__device__ __forceinline__ double partner64(double v) {
+  return __hiloint2double(dpp_partner<OFF>(__double2hiint(v)), dpp_partner<OFF>(__double2loint(v)));
+}
+__device__ __forceinline__ double lane64(double v, int lane) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), lane),
+                          __builtin_amdgcn_readlane(__double2loint(v), lane));
+}
+__device__ __forceinline__ double row_max(double v) {
+  v = fmax(v, partner64<1>(v));
+  v = fmax(v, partner64<2>(v));
+  v = fmax(v, partner64<4>(v));
+  return fmax(v, partner64<8>(v));
+}
+__device__ __forceinline__ double row_sum(double v) {
+  v += partner64<1>(v);
+  v += partner64<2>(v);
+  v += partner64<4>(v);
+  return v + partner64<8>(v);
+}
+__device__ __forceinline__ double wave_max(double v) {
+  v = row_max(v);
+  return fmax(fmax(lane64(v, 0), lane64(v, 16)), fmax(lane64(v, 32), lane64(v, 48)));
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v = row_sum(v);
+  return (lane64(v, 0) + lane64(v, 16)) + (lane64(v, 32) + lane64(v, 48));
+}
+
 }  // namespace rows
