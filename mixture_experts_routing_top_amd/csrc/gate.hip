@@ -13,12 +13,20 @@
 // A masked expert (logit NaN or <= kMaskBelow) has score 0 and comes after
 // every other expert of the kept groups, in index order.
 //
-// Two steps.  gate_kernel gives a token to 16 lanes and selects in float32 on
-// 32-bit keys, 24 bits of the value in fixed point and 8 of the index, knowing
-// a bound on its own error: a token whose order two candidates closer than the
-// bound could turn (not if they are equal in logit and bias: then the index
-// decides, in double as well) is done again by the whole wave in double
-// (gate_token).  Doing every token in double costs ten times the time.
+// gate_kernel gives a token to 16 lanes and selects in float32 on 32-bit keys, 23
+// bits of the value in fixed point and 8 of the index, knowing a bound on its own
+// error.  Where two candidates lie closer than the bound (and are not equal in
+// logit and bias: then the index decides, in double as well), the token's 16 best
+// are put in the order of their values in double, which is the answer if the 16th
+// lies clearly below the k-th.  A token for which that does not do, or whose last
+// kept group is as close to the first one left out, is done again by the whole wave
+// in double (gate_token).  About one token in a thousand needs the first, one in
+// tens of thousands the second; every token in double costs four times the time.
+//
+// Bound by the vector instructions, some 840 for four tokens of 256 experts and
+// k = 8: 35 % in the k + 1 rounds of selection, 20 % in the scores, 12 % in the
+// weights.  65536 tokens, biased sigmoids in 8 groups, bf16: 39 us (168 us with a
+// wave a token, in double); 16384 x 160, softmax, float32: 9.4 us (34).
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -111,6 +119,15 @@ __device__ __forceinline__ double exp_of(double x) {
   return ldexp(e, static_cast<int>(n));
 }
 
+// In double: a sigmoid, and a bias held within the keys of unmasked experts (NaN: lowest).
+__device__ __forceinline__ double sigmoid_of(double x) {
+  const double z = exp(-fabs(x));
+  return (x > 0.0 ? 1.0 : z) / (1.0 + z);
+}
+__device__ __forceinline__ double bias_of(float b) {
+  return fmin(fmax(static_cast<double>(b), -kBiasLimit), kBiasLimit);
+}
+
 // a / b in double for b in the normal range, to about an ulp
 __device__ __forceinline__ double quotient(double a, double b) {
   double r = __builtin_amdgcn_rcp(b);
@@ -176,9 +193,8 @@ __device__ __forceinline__ void gate_token(const Args& p, int64_t t, int lane, L
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const double x = l[j];
-      const double z = exp(p.softmax ? x - m : -fabs(x));   // 0 where masked
-      if (p.softmax) total += s[j] = z;
-      else s[j] = (x > 0.0 ? 1.0 : z) / (1.0 + z);
+      if (p.softmax) total += s[j] = exp(x - m);   // 0 where masked
+      else s[j] = sigmoid_of(x);
     }
     if (p.softmax) {
       total = wave_sum(total);
@@ -190,7 +206,7 @@ __device__ __forceinline__ void gate_token(const Args& p, int64_t t, int lane, L
   for (int j = 0; j < 4; ++j) {
     const int e = lane + 64 * j;
     double b = 0.0;
-    if (p.bias && e < p.E) b = fmin(fmax(static_cast<double>(p.bias[e]), -kBiasLimit), kBiasLimit);  // NaN: lowest
+    if (p.bias && e < p.E) b = bias_of(p.bias[e]);
     key[j] = e >= p.E ? -INFINITY : !live[j] ? kMaskedKey : p.bias ? s[j] + b : static_cast<double>(l[j]);
     if (p.keep < p.n_groups && e < p.E) value[e] = !two ? key[j] : live[j] ? s[j] + b : -INFINITY;
   }
@@ -270,11 +286,13 @@ __device__ __noinline__ void gate_token_call(KernelArgs* p, int64_t t, LdsDouble
 }
 
 // ------------------------------------------------------------ 16 lanes a token
+// (bound control on, which no lane of these pairings needs, lets the move be part of
+// the maximum's own instruction)
 __device__ __forceinline__ uint32_t row_max(uint32_t v) {
-  v = max(v, static_cast<uint32_t>(dpp_partner<1>(v)));
-  v = max(v, static_cast<uint32_t>(dpp_partner<2>(v)));
-  v = max(v, static_cast<uint32_t>(dpp_partner<4>(v)));
-  return max(v, static_cast<uint32_t>(dpp_partner<8>(v)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0xB1, 0xf, 0xf, true)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0x4E, 0xf, 0xf, true)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0x141, 0xf, 0xf, true)));
+  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0x140, 0xf, 0xf, true)));
 }
 __device__ __forceinline__ float row_sum(float v) {
   v += __int_as_float(dpp_partner<1>(__float_as_int(v)));
@@ -286,8 +304,12 @@ __device__ __forceinline__ float row_sum(float v) {
 __device__ __forceinline__ int next_lane(int v) { return __builtin_amdgcn_update_dpp(v, v, 0x101, 0xf, 0xf, false); }
 // the value of the lane N down, around the 16
 template <int N>
+__device__ __forceinline__ int rotated_bits(int v) {
+  return __builtin_amdgcn_mov_dpp(v, 0x120 + N, 0xf, 0xf, false);
+}
+template <int N>
 __device__ __forceinline__ float rotated(float v) {
-  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x120 + N, 0xf, 0xf, false));
+  return __int_as_float(rotated_bits<N>(__float_as_int(v)));
 }
 
 // Groups ahead of this lane's, the groups being kLanes lanes each: `rep` is the
@@ -298,6 +320,16 @@ __device__ __forceinline__ int count_ahead(float rep, float score, int l16) {
   else {
     const float o = rotated<N>(rep);   // of the group N / kLanes before, around the 16
     return (o > score || (o == score && l16 >= N)) + count_ahead<kLanes, N + kLanes>(rep, score, l16);
+  }
+}
+
+// How many of the token's other 15 lanes come before this one, by value and then index.
+template <int N>
+__device__ __forceinline__ int rank16(double v, int e) {
+  if constexpr (N >= 16) return 0;
+  else {
+    const double o = __hiloint2double(rotated_bits<N>(__double2hiint(v)), rotated_bits<N>(__double2loint(v)));
+    return ahead(o, rotated_bits<N>(e), v, e) + rank16<N + 1>(v, e);
   }
 }
 
@@ -316,12 +348,17 @@ enum By { kByLogit, kBySigmoid, kBySoftmax };          // what the selection com
 enum Weights { kSoftmaxKept, kSoftmaxAll, kSigmoids };  // softmax over the kept logits, over all; sigmoids
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kTop = 16777200.f;     // the largest fixed-point value, below 2^24
+// Keys are cut from floats between 2^23 and 2^24, whose low 23 bits count units:
+// 8 bits further up they leave room for the index.
+constexpr float kZero = 8388608.f;     // 2^23: a key's value of 0
 
 // Lane i of a token's 16 holds `per` consecutive experts (at most V) of one group:
 // groups begin at multiples of `lanes` lanes.  A wave takes 4 tokens at a time.
+// Blocks a CU holds, by the registers the slots take; a launch has just as many.
+constexpr int gate_blocks_per_cu(int V) { return V > 16 ? 2 : V > 8 ? 3 : 4; }
+
 template <bool kBf16, int V, By kBy, Weights kW>
-__global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, int lanes_log2, int per) {
+__global__ __launch_bounds__(256, gate_blocks_per_cu(V)) void gate_kernel(GateArgs p, int lanes_log2, int per) {
   __shared__ double value[4][moe::kMaxExperts];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l16 = lane & 15;
   const int lanes = 1 << lanes_log2;
@@ -331,50 +368,50 @@ __global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, i
   const int n = group < p.n_groups ? max(0, min(per, p.group_size - inside)) : 0;   // this lane's experts
   const int64_t total = p.T * p.E;
 
-  // A key is (fixed-point value << 8) + c: the value at least 3, 2 for a masked
-  // expert (-inf is cut to it), 1 where the group is not kept; c = 255 - index, or
-  // what takes a slot without an expert below the masked ones.
+  // A key is (value << 8) + c: the value at least 3, 2 for a masked expert (-inf is
+  // cut to it), 1 where the group is not kept; c = 255 - index, or what takes a slot
+  // without an expert below the masked ones.
   uint32_t c[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) c[j] = j < n ? static_cast<uint32_t>(255 - e0 - j) : static_cast<uint32_t>(-256);
 
-  // the bias, -inf in a slot without an expert; the fixed-point scale, and the
-  // bound on the error of two values' difference
+  // b: 0, or the bias in units, and -inf in a slot without an expert; the units of a
+  // score and the bound on the error of two values' difference
   float b[V];
-  float scale = kTop / 32.f;    // logits down to 32 below the largest: the cut is monotone, so
-  float offset = 3.f + kTop;    // only equal keys of unequal logits are in doubt
+  float scale = 0x1p19f;         // units of a logit, down to 16 below the largest.  The cut is
+  float offset = 0.f;            // monotone: only equal keys of unequal logits are in doubt
   float near = 0.f, group_near = 0.f;
 #pragma unroll
   for (int j = 0; j < V; ++j) b[j] = 0.f;
-  if (kBy != kByLogit && p.bias)
-#pragma unroll
-    for (int j = 0; j < V; ++j) b[j] = p.bias[min(e0 + j, p.E - 1)];
-#pragma unroll
-  for (int j = 0; j < V; ++j) b[j] = j < n ? b[j] : -INFINITY;
   if constexpr (kBy != kByLogit) {
+    if (p.bias)
+#pragma unroll
+      for (int j = 0; j < V; ++j) b[j] = p.bias[min(e0 + j, p.E - 1)];
     float lo = INFINITY, hi = -INFINITY;
     bool odd = false;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       odd |= (j < n) & !(fabsf(b[j]) <= 1e30f);
       lo = fminf(lo, j < n ? b[j] : INFINITY);
-      hi = fmaxf(hi, b[j]);
+      hi = fmaxf(hi, j < n ? b[j] : -INFINITY);
     }
-    if (odd) lo = hi = INFINITY;     // left to the doubles
+    if (odd) lo = hi = INFINITY;     // left to the doubles: no key is finite
     lo = -row_max(-lo);
     hi = row_max(hi);
-    const float range = 1.f + (hi - lo), big = fmaxf(fabsf(lo), fabsf(hi));
-    // s: exp2's argument, exp2, the sum and the reciprocal, 6 u in all (u = 2^-24);
-    // a softmax's sum of up to 32 values in sequence and 4 steps, 36 u more, and the
-    // terms' own errors in it, at most 10 u.  s + b rounds once more.  In the key: half
-    // a unit of fma, one of the cut.
-    const float err = (kBy == kBySigmoid ? 7.f : 53.f) + big;
-    scale = kTop / range;
-    offset = 4.f - lo * scale;
-    near = 2.f * (err / range + 2.f);
-    group_near = (4.f * err + 4.f * (1.f + big)) * 0x1p-24f;
-    if (!(hi < INFINITY)) near = group_near = INFINITY;
+    scale = (kZero - 1024.f) / (1.f + (hi - lo));
+    offset = kZero + 16.f - lo * scale;
+#pragma unroll
+    for (int j = 0; j < V; ++j) b[j] = fmaf(b[j], scale, offset);
+    // s: exp2's argument 0.4 u (u = 2^-24), exp2 0.5, the sum 1 and the reciprocal 2; a softmax's
+    // sum of up to 32 values in sequence and 4 steps 36 u more, the terms' own errors in it
+    // at most 10 u, and the scaled reciprocal.  b and the sum in units: half a unit each.
+    const float err = (kBy == kBySigmoid ? 5.f : 53.f) * 0x1p-24f * scale + 1.f;
+    near = 2.f * err + 0.5f;
+    // a sum of two: twice that, the sum's rounding and, beyond 2^24, the offset's
+    group_near = !p.top2 ? near : 4.f * err + 3.f + (fabsf(offset) > 2.f * kZero ? fabsf(offset) * 0x1p-21f : 0.f);
   }
+#pragma unroll
+  for (int j = 0; j < V; ++j) b[j] = j < n ? b[j] : -INFINITY;
 
   for (int64_t base = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * 4; base < p.T;
        base += static_cast<int64_t>(gridDim.x) * 16) {
@@ -403,15 +440,15 @@ __global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, i
       raise_check(p.check, bad && active, MOE_CHECK_LOGITS);
     }
 
-    // v: what is compared, -inf where masked or without an expert
+    // v: what is compared, in units (a logit as it is), -inf where masked or without an expert
     float v[V];
     float m = 0.f;
     double sum64 = 1.0;
     if constexpr (kBy == kBySigmoid) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l[j] * -kLog2e)) + b[j];
-        v[j] = is_live(l[j]) ? s : -INFINITY;
+        const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l[j] * -kLog2e));
+        v[j] = is_live(l[j]) ? fmaf(s, scale, b[j]) : -INFINITY;
       }
     } else {
       m = -INFINITY;
@@ -441,7 +478,7 @@ __global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, i
           sum += v[j];
         }
         sum = row_sum(sum);
-        const float inv = sum > 0.f ? __builtin_amdgcn_rcpf(sum) : 0.f;
+        const float inv = sum > 0.f ? scale * __builtin_amdgcn_rcpf(sum) : 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] = l[j] > -INFINITY ? fmaf(v[j], inv, b[j]) : -INFINITY;
       } else {
@@ -465,7 +502,8 @@ __global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, i
       if (lanes > 1) join(dpp_partner<1>(__float_as_int(m1)), dpp_partner<1>(__float_as_int(m2)));
       if (lanes > 2) join(dpp_partner<2>(__float_as_int(m1)), dpp_partner<2>(__float_as_int(m2)));
       if (lanes > 4) join(dpp_partner<4>(__float_as_int(m1)), dpp_partner<4>(__float_as_int(m2)));
-      const float score = kBy != kByLogit && p.top2 && m2 > -INFINITY ? m1 + m2 : m1;
+      // (a score of 0 has `offset` units: counted once in a sum of two)
+      const float score = kBy != kByLogit && p.top2 && m2 > -INFINITY ? m1 + (m2 - offset) : m1;
       const bool real = group < p.n_groups;
       const float rep = real ? score : NAN;
       const int rank = lanes == 1 ? count_ahead<1>(rep, score, l16) : lanes == 2 ? count_ahead<2>(rep, score, l16)
@@ -480,12 +518,12 @@ __global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, i
     }
 
     uint32_t key[V];
-    const float low = kept ? 2.f : 1.f, high = kept ? 16777215.f : 1.f;
+    const float low = kZero + (kept ? 2.f : 1.f), high = kept ? 2.f * kZero - 1.f : low;
+    const float down = 2.f * kZero - 64.f - m * scale;   // (by logit: the largest near the top)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const float x = kBy == kByLogit ? v[j] - m : v[j];
-      const float f = __builtin_amdgcn_fmed3f(fmaf(x, scale, offset), low, high);
-      key[j] = (static_cast<uint32_t>(f) << 8) + c[j];
+      const float f = __builtin_amdgcn_fmed3f(kBy == kByLogit ? fmaf(v[j], scale, down) : v[j], low, high);
+      key[j] = (__float_as_uint(f) << 8) + c[j];
     }
 
     // lane i takes the i-th key, lane k the best one left
@@ -495,8 +533,9 @@ __global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, i
       best = next_key<V>(key, best);
       if (l16 == i) mine = best;
     }
-    const int e = min(255 - static_cast<int>(mine & 255u), p.E - 1);
-    const bool some = l16 <= p.k && mine >= 768u;      // an unmasked expert
+    int e = min(255 - static_cast<int>(mine & 255u), p.E - 1);
+    bool some = l16 <= p.k && mine >= 768u;      // an unmasked expert
+    const bool group_doubt = doubt;
     // a logit too far below the largest is cut to a masked one's value as well
     doubt |= l16 < p.k && !some;
     float lk = some ? load_logit<kBf16>(p.logits, row + e) : -INFINITY;
@@ -507,9 +546,43 @@ __global__ __launch_bounds__(256, V > 16 ? 2 : 4) void gate_kernel(GateArgs p, i
       const float bk = p.bias && some ? p.bias[e] : 0.f;
       same = same && bk == __int_as_float(next_lane(__float_as_int(bk)));
     }
-    doubt |= some && l16 < p.k && q_next >= 3u && static_cast<float>(q - q_next) <= near && !same;
-    const uint64_t doubts = __ballot(doubt && active);
-    const bool redo = (doubts >> (lane & 48)) & 0xffffu;
+    const bool close = some && l16 < p.k && q_next >= 3u && static_cast<float>(q - q_next) <= near;
+    doubt |= close && !same;
+    // the last one taken and the first one left are equal: the one after them may belong before both
+    const bool tie = close && same && l16 == p.k - 1;
+    if (__any(tie)) {
+      const uint32_t next = next_key<V>(key, best);
+      doubt |= tie && next < best && (next >> 8) >= 3u && static_cast<float>(q - (next >> 8)) <= near;
+    }
+    uint64_t doubts = __ballot(doubt && active);
+    bool redo = (doubts >> (lane & 48)) & 0xffffu;
+    if (kBy != kBySoftmax && doubts) {
+      // The 16 best by key in the order of their exact values.  That is the answer where
+      // the 16th lies clearly below the k-th, so that none of the others can pass it.
+      const uint32_t last = static_cast<uint32_t>(__shfl(static_cast<int>(mine), (lane & 48) | (p.k - 1)));
+      best = last;
+#pragma unroll 1
+      for (int i = p.k; i < 16; ++i) {
+        const uint32_t next = next_key<V>(key, best);
+        best = best != 0u && next < best ? next : 0u;   // (past the last key the largest comes again)
+        if (l16 == i) mine = best;
+      }
+      e = min(255 - static_cast<int>(mine & 255u), p.E - 1);
+      const bool there = mine >= 512u;
+      const float raw = there ? load_logit<kBf16>(p.logits, row + e) : -INFINITY;
+      const double x = fminf(raw, FLT_MAX);
+      double exact = x;
+      if constexpr (kBy == kBySigmoid) exact = sigmoid_of(x) + (p.bias ? bias_of(p.bias[e]) : 0.0);
+      exact = !there ? -INFINITY : is_live(raw) ? exact : kMaskedKey;
+      const uint32_t last_q = static_cast<uint32_t>(__shfl(static_cast<int>(mine), (lane & 48) | 15)) >> 8;
+      redo = redo && (group_doubt || !(last_q < 2u || static_cast<float>((last >> 8) - last_q) > near));
+      const int to = ((lane & 48) + rank16<1>(exact, e)) * 4;
+      e = __builtin_amdgcn_ds_permute(to, e);
+      lk = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(raw)));
+      some = l16 < p.k && is_live(lk);
+      lk = some ? fminf(lk, FLT_MAX) : -INFINITY;
+      doubts = __ballot(redo && active);
+    }
 
     // weights in double, rounded once
     const double w = chosen_weight(kW != kSigmoids, kW == kSigmoids ? p.renorm : kW == kSoftmaxKept, p.scale, lk,
@@ -536,6 +609,13 @@ __global__ __launch_bounds__(256) void gate_wave_kernel(GateArgs p) {
   gate_token<kBf16>(p, t, lane, (LdsDoubles*)value[wave]);
 }
 
+template <int V, bool kBf16, By kBy, Weights kW>
+void launch_by(const GateArgs& p, int lanes_log2, int per, hipStream_t s) {
+  constexpr int64_t kBlocks = 256 * gate_blocks_per_cu(V);
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(kBlocks, moe::ceil_div(p.T, 16)));
+  gate_kernel<kBf16, V, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes_log2, per);
+}
+
 template <bool kBf16, By kBy, Weights kW>
 void launch_slots(GateArgs p, hipStream_t s) {
   int lanes_log2 = 4;
@@ -545,13 +625,12 @@ void launch_slots(GateArgs p, hipStream_t s) {
   }
   while ((16 >> lanes_log2) < p.n_groups) --lanes_log2;
   const int per = static_cast<int>(moe::ceil_div(p.group_size, 1 << lanes_log2));
-  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(1024, moe::ceil_div(p.T, 16)));
-  if (per <= 2) gate_kernel<kBf16, 2, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes_log2, per);
-  else if (per <= 4) gate_kernel<kBf16, 4, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes_log2, per);
-  else if (per <= 8) gate_kernel<kBf16, 8, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes_log2, per);
-  else if (per <= 12) gate_kernel<kBf16, 12, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes_log2, per);
-  else if (per <= 16) gate_kernel<kBf16, 16, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes_log2, per);
-  else gate_kernel<kBf16, 32, kBy, kW><<<blocks, 256, 0, s>>>(p, lanes_log2, per);
+  if (per <= 2) launch_by<2, kBf16, kBy, kW>(p, lanes_log2, per, s);
+  else if (per <= 4) launch_by<4, kBf16, kBy, kW>(p, lanes_log2, per, s);
+  else if (per <= 8) launch_by<8, kBf16, kBy, kW>(p, lanes_log2, per, s);
+  else if (per <= 12) launch_by<12, kBf16, kBy, kW>(p, lanes_log2, per, s);
+  else if (per <= 16) launch_by<16, kBf16, kBy, kW>(p, lanes_log2, per, s);
+  else launch_by<32, kBf16, kBy, kW>(p, lanes_log2, per, s);
 }
 
 template <bool kBf16>
@@ -654,11 +733,12 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GateBwdArgs p) {
       }
     }
     m = row_max(m);
+    const float top = m > -INFINITY ? m : 0.f;
 #pragma unroll
     for (int c = 0; c < kPieces; ++c)
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        l[c][u] = l[c][u] > -INFINITY ? expf(l[c][u] - m) : 0.f;
+        l[c][u] = __builtin_amdgcn_exp2f((l[c][u] - top) * kLog2e);   // (0 where masked)
         total += l[c][u];
       }
     total = row_sum(total);
@@ -698,6 +778,7 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GateBwdArgs p) {
   if (first) reinterpret_cast<float*>(mine)[e] = v;
   wave_lds_fence();
   if (!active) return;
+  const float share = kDense && total > 0.f ? common / total : 0.f;
 #pragma unroll
   for (int c = 0; c < kPieces; ++c) {
     const int at = c * 128 + l16 * 8, n = p.E - at;
@@ -707,7 +788,7 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GateBwdArgs p) {
     if constexpr (kDense)
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        if (l[c][u] > 0.f) d[u] -= l[c][u] / total * common;
+        if (l[c][u] > 0.f) d[u] = fmaf(-l[c][u], share, d[u]);
     rows::store8_part<kBf16>(p.d_logits, row + at, n, d);
   }
 }

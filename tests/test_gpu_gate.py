@@ -163,6 +163,45 @@ def test_gate_orders_scores_closer_than_a_float(score, dtype):
                         group_score=gs)
 
 
+@pytest.mark.parametrize("E,G,keep,k", [(64, 1, 1, 6), (160, 8, 3, 6), (256, 8, 4, 8), (24, 1, 1, 8), (20, 4, 2, 8)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_pairs_closer_than_a_float(score, E, G, keep, k):
+    """In every row some pairs (or triples) of experts whose values differ by about a
+    float's step or less, among otherwise spread ones: logits a few steps apart without a
+    bias, and with one logits that make up for the bias as well as a float can."""
+    T = 700
+    rng = np.random.default_rng(E)
+    lg = (2.0 * rng.standard_normal((T, E)) + 1.0).astype(np.float32)
+    plain = lg.copy()
+    for t in range(T):
+        order = np.argsort(-plain[t])
+        for at in rng.integers(0, k + 2, 3):     # the partner of a high one: anywhere in the row
+            other = rng.integers(0, E)
+            steps = int(rng.integers(-3, 4))
+            v = plain[t, order[min(at, E - 1)]]
+            plain[t, other] = v + steps * np.spacing(v)
+    opts = dict(score=score, n_groups=G, keep_groups=keep)
+    for gs in ("max", "top2"):
+        _check_gate(torch.from_numpy(plain).cuda(), k, group_score=gs, **opts)
+    if score == "softmax":
+        bias = np.zeros(E, np.float32)       # (the scores hang on the whole row: equal logits, ties by index)
+        _check_gate(torch.from_numpy(plain).cuda(), k, bias=torch.from_numpy(bias).cuda(), group_score="top2", **opts)
+        return
+    bias = (0.2 * rng.standard_normal(E)).astype(np.float32)
+    for t in range(T):
+        value = 1.0 / (1.0 + np.exp(-lg[t].astype(np.float64))) + bias
+        order = np.argsort(-value)
+        for at in rng.integers(0, k + 2, 3):
+            other = int(rng.integers(0, E))
+            s = value[order[min(at, E - 1)]] - bias[other]
+            if 1e-3 < s < 1 - 1e-3:
+                lg[t, other] = np.float32(np.log(s / (1.0 - s)))
+                value[other] = 1.0 / (1.0 + np.exp(-np.float64(lg[t, other]))) + bias[other]
+    b = torch.from_numpy(bias).cuda()
+    for gs in ("max", "top2"):
+        _check_gate(torch.from_numpy(lg).cuda(), k, bias=b, group_score=gs, **opts)
+
+
 def test_gate_equals_moe_route_where_they_mean_the_same():
     lg = _logits(1000, 160, torch.float32, 8)
     idx, w = moe.moe_gate(lg, 6)
