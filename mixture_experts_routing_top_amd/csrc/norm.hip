@@ -80,11 +80,29 @@ __device__ __forceinline__ void load_vector(const void* p, int tid, int H, float
   for (int j = 0; j < NV; ++j) load_piece<kWBf16>(p, (j * TPR + tid) * 8, H - (j * TPR + tid) * 8, fill, v[j]);
 }
 
-// Blocks a CU holds of the forward kernel, by the registers it needs: 8 waves a SIMD
-// with one piece a thread, 5 with two (4 in blocks of 8 or 16 waves).  The launch has
-// just as many: 8192 x 4096 bf16 with residual takes 49 us on 5 blocks a CU, 56 on 4,
-// 57 on 8 and 62 on a block for each row.
-constexpr int fwd_blocks_per_cu(int tpr, int nv) { return tpr == 1024 ? 1 : tpr == 512 ? 2 : nv == 1 ? 8 : 5; }
+// a row's pieces as they lie in memory
+template <bool kBf16, int NV>
+struct RawRow {
+  Raw8<kBf16> piece[NV];
+};
+
+template <bool kBf16, int TPR, int NV>
+__device__ __forceinline__ void load_row(const void* p, int64_t row, int64_t T, int H, int tid,
+                                         RawRow<kBf16, NV>& r) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * TPR + tid) * 8;
+    r.piece[j] = {};
+    if (p && row < T && c < H) r.piece[j] = load8_part<kBf16>(p, row * H + c, H - c);
+  }
+}
+
+// Blocks a CU holds of the forward kernel, by the registers it needs with a row
+// ahead: 6 waves a SIMD with one piece a thread, 4 with two.  The launch has just as
+// many, and the next row is loaded while one is reduced: 8192 x 4096 bf16 with
+// residual takes 47 us (5.7 TB/s), without the row ahead 50 on 5 blocks a CU, 56 on
+// 4, 57 on 8 and 62 on a block for each row; 4096 x 8192 takes 46 against 55.
+constexpr int fwd_blocks_per_cu(int tpr, int nv) { return tpr == 1024 ? 1 : tpr == 512 ? 2 : nv == 1 ? 6 : 4; }
 
 template <bool kBf16, bool kWBf16, int TPR, int NV, int R>
 __global__ __launch_bounds__(TPR* R, fwd_blocks_per_cu(TPR, NV)) void norm_kernel(NormArgs p) {
@@ -94,7 +112,11 @@ __global__ __launch_bounds__(TPR* R, fwd_blocks_per_cu(TPR, NV)) void norm_kerne
   load_vector<kWBf16, TPR, NV>(p.weight, tid, p.H, 1.f, w);
   load_vector<kWBf16, TPR, NV>(p.bias, tid, p.H, 0.f, b);
   const float inv_h = 1.f / static_cast<float>(p.H);
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * R; base < p.T; base += static_cast<int64_t>(gridDim.x) * R) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * R;
+  RawRow<kBf16, NV> xr, rr;
+  load_row<kBf16, TPR, NV>(p.x, static_cast<int64_t>(blockIdx.x) * R + r, p.T, p.H, tid, xr);
+  load_row<kBf16, TPR, NV>(p.residual, static_cast<int64_t>(blockIdx.x) * R + r, p.T, p.H, tid, rr);
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * R; base < p.T; base += step) {
     const int64_t row = base + r;
     const bool active = row < p.T;
     const int64_t at = (active ? row : 0) * p.H;
@@ -104,13 +126,11 @@ __global__ __launch_bounds__(TPR* R, fwd_blocks_per_cu(TPR, NV)) void norm_kerne
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TPR + tid) * 8;
       const int n = active ? p.H - c : 0;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) v[j][u] = 0.f;
+      unpack8<kBf16>(xr.piece[j], v[j]);
       if (n > 0) {
-        unpack8<kBf16>(load8_part<kBf16>(p.x, at + c, n), v[j]);
         if (p.residual) {
           float q[8];
-          unpack8<kBf16>(load8_part<kBf16>(p.residual, at + c, n), q);
+          unpack8<kBf16>(rr.piece[j], q);
 #pragma unroll
           for (int u = 0; u < 8; ++u) v[j][u] += q[u];
           const Raw8<kBf16> s = pack8<kBf16>(v[j]);  // the sum as it is kept
@@ -121,6 +141,9 @@ __global__ __launch_bounds__(TPR* R, fwd_blocks_per_cu(TPR, NV)) void norm_kerne
 #pragma unroll
       for (int u = 0; u < 8; ++u) sum[0] += v[j][u];
     }
+    // the next row is on its way while this one is reduced
+    load_row<kBf16, TPR, NV>(p.x, row + step, p.T, p.H, tid, xr);
+    load_row<kBf16, TPR, NV>(p.residual, row + step, p.T, p.H, tid, rr);
     row_sum<TPR, 1>(sum, part[0]);
     const float mean = sum[0] * inv_h;
     float dev[2] = {0.f, 0.f};
@@ -162,23 +185,6 @@ struct NormBwdArgs {
   int H, Hp;
   float eps;
 };
-
-// a row's pieces as they lie in memory
-template <bool kBf16, int NV>
-struct RawRow {
-  Raw8<kBf16> piece[NV];
-};
-
-template <bool kBf16, int TPR, int NV>
-__device__ __forceinline__ void load_row(const void* p, int64_t row, int64_t T, int H, int tid,
-                                         RawRow<kBf16, NV>& r) {
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * TPR + tid) * 8;
-    r.piece[j] = {};
-    if (p && row < T && c < H) r.piece[j] = load8_part<kBf16>(p, row * H + c, H - c);
-  }
-}
 
 // Blocks a CU holds of the backward kernel, by the registers it needs: 4 waves a
 // SIMD with one piece a thread, else 2.
@@ -347,8 +353,9 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(const float* __restri
 }
 
 // Threads per row and pieces a thread for a width.  In the widest rows the forward
-// pass takes 16 waves with 2 pieces (bf16 2048 x 16384: 69 us, 8 waves with 4: 90),
-// the backward pass, whose sums then spill, 8 waves with 4 (99 us against 125).
+// pass takes 16 waves with 2 pieces (bf16 2048 x 16384, before the row ahead: 69 us,
+// 8 waves with 4: 90), the backward pass, whose sums then spill, 8 waves with 4 (99 us
+// against 125).
 struct Shape {
   int tpr, nv;
 };
