@@ -8,7 +8,9 @@ rounding, two ulps of exp and one of the sum's term), a sum's over E <= 256
 terms 8 u more, a ratio's 2 (R + 13) u; s (g - sum g s) then errs by at most
 2 G (4 (R + 13) + k + 4) u with G the largest |scale d_w| (every s is at most 1,
 the inner sum at most G in size and k terms long), plus half a step of the
-output's type.  Renormalised sigmoids have ratios of the same form.
+output's type.  Renormalised sigmoids have ratios of the same form.  The dense
+row's exponentials are 2^x of a product rounded once, (1.5 R + 2) u each: their
+2 G (4.5 R + 19.5 + k/2) u in all is less than the above up to R = 73.
 """
 import math
 
