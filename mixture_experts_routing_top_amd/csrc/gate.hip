@@ -382,6 +382,7 @@ __global__ __launch_bounds__(256, gate_blocks_per_cu(V)) void gate_kernel(GateAr
   float scale = 0x1p19f;         // units of a logit, down to 16 below the largest.  The cut is
   float offset = 0.f;            // monotone: only equal keys of unequal logits are in doubt
   float near = 0.f, group_near = 0.f;
+  bool wild = false;             // biases that no units measure: every token goes to the doubles
 #pragma unroll
   for (int j = 0; j < V; ++j) b[j] = 0.f;
   if constexpr (kBy != kByLogit) {
@@ -396,9 +397,10 @@ __global__ __launch_bounds__(256, gate_blocks_per_cu(V)) void gate_kernel(GateAr
       lo = fminf(lo, j < n ? b[j] : INFINITY);
       hi = fmaxf(hi, j < n ? b[j] : -INFINITY);
     }
-    if (odd) lo = hi = INFINITY;     // left to the doubles: no key is finite
+    if (odd) lo = hi = INFINITY;
     lo = -row_max(-lo);
     hi = row_max(hi);
+    wild = !(hi < INFINITY);
     scale = (kZero - 1024.f) / (1.f + (hi - lo));
     offset = kZero + 16.f - lo * scale;
 #pragma unroll
@@ -488,7 +490,7 @@ __global__ __launch_bounds__(256, gate_blocks_per_cu(V)) void gate_kernel(GateAr
       }
     }
 
-    bool doubt = false, kept = true;
+    bool doubt = wild, kept = true;
     if (p.keep < p.n_groups) {
       float m1 = -INFINITY, m2 = -INFINITY;
 #pragma unroll
@@ -514,7 +516,7 @@ __global__ __launch_bounds__(256, gate_blocks_per_cu(V)) void gate_kernel(GateAr
         // the last group kept against the first one left out
         const float low = -row_max(kept ? -score : -INFINITY);
         const float high = row_max(real && !kept ? score : -INFINITY);
-        doubt = high > -INFINITY && !(low - high > group_near);
+        doubt |= high > -INFINITY && !(low - high > group_near);
       }
     }
 

@@ -165,6 +165,36 @@ def test_gate_orders_scores_closer_than_a_float(score, dtype):
                         group_score=gs)
 
 
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,keep,k", [(8, 4, 2, 3), (40, 2, 1, 4), (64, 8, 1, 2), (64, 8, 2, 5), (24, 3, 2, 8),
+                                        (33, 1, 1, 2), (256, 32, 2, 8)])
+def test_gate_biases_without_a_spread(E, G, keep, k, score, renorm):
+    """Infinite and NaN biases and ones beyond 1e30, in whole groups, in all but a few
+    experts and throughout: they rank as +-1e299 (NaN lowest), ties by index."""
+    rng = np.random.default_rng(E + k)
+    size = E // G
+    small = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    cases = []
+    for odd in (math.inf, -math.inf, math.nan, 2e30, -3e38):
+        last, few, all_ = small.copy(), np.full(E, odd, np.float32), np.full(E, odd, np.float32)
+        last[-size:] = odd
+        few[[0, E // 2, E - 1]] = small[[0, E // 2, E - 1]]
+        mixed = small.copy()
+        mixed[::3] = odd
+        cases += [last, few, all_, mixed]
+    for b in cases:
+        exact = b.astype(np.float64)
+        exact = np.clip(np.where(np.isnan(exact), -math.inf, exact), -1e299, 1e299)
+        lg = _logits(19, E, torch.float32, 8)
+        for gs in ("max", "top2"):
+            kw = dict(score=score, n_groups=G, keep_groups=keep, group_score=gs, renorm=renorm)
+            idx, w = moe.moe_gate(lg, k, bias=torch.from_numpy(b).cuda(), **kw)
+            ref_idx, ref_w = oo.gate(_f64(lg), k, bias=exact, **kw)
+            assert np.array_equal(idx.cpu().numpy(), ref_idx), (b, gs)
+            assert np.all(np.abs(_f64(w) - ref_w) <= 1.01 * U * np.abs(ref_w) + 2.0 ** -149)
+
+
 @pytest.mark.parametrize("E,G,keep,k", [(64, 1, 1, 6), (160, 8, 3, 6), (256, 8, 4, 8), (24, 1, 1, 8), (20, 4, 2, 8)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_gate_pairs_closer_than_a_float(score, E, G, keep, k):
