@@ -575,7 +575,9 @@ __global__ __launch_bounds__(256, gate_blocks_per_cu(V)) void gate_kernel(GateAr
       const float raw = there ? load_logit<kBf16>(p.logits, row + e) : -INFINITY;
       const double x = fminf(raw, FLT_MAX);
       double exact = x;
-      if constexpr (kBy == kBySigmoid) exact = sigmoid_of(x) + (p.bias ? bias_of(p.bias[e]) : 0.0);
+      // (without a bias by the logit: large ones' sigmoids are 1 in double too)
+      if constexpr (kBy == kBySigmoid)
+        if (p.bias) exact = sigmoid_of(x) + bias_of(p.bias[e]);
       exact = !there ? -INFINITY : is_live(raw) ? exact : kMaskedKey;
       const uint32_t last_q = static_cast<uint32_t>(__shfl(static_cast<int>(mine), (lane & 48) | 15)) >> 8;
       redo = redo && (group_doubt || !(last_q < 2u || static_cast<float>((last >> 8) - last_q) > near));

@@ -195,6 +195,19 @@ def test_gate_biases_without_a_spread(E, G, keep, k, score, renorm):
             assert np.all(np.abs(_f64(w) - ref_w) <= 1.01 * U * np.abs(ref_w) + 2.0 ** -149)
 
 
+@pytest.mark.parametrize("E,G,keep,k", [(16, 4, 2, 4), (16, 4, 1, 3), (64, 8, 2, 8), (24, 3, 2, 8)])
+def test_gate_without_a_bias_saturated_sigmoids_go_by_logit(E, G, keep, k):
+    """From 37 on a sigmoid is 1 in double too, and the experts' order still the logits'."""
+    rng = np.random.default_rng(E)
+    size = E // G
+    lg = rng.standard_normal((21, E)) - 5.0
+    for row in lg:
+        for g in rng.permutation(G)[:keep]:
+            row[g * size:(g + 1) * size] = 40.0 + rng.permutation(size)
+    _check_gate(torch.from_numpy(lg.astype(np.float32)).cuda(), k, score="sigmoid", n_groups=G, keep_groups=keep,
+                group_score="top2")
+
+
 @pytest.mark.parametrize("E,G,keep,k", [(64, 1, 1, 6), (160, 8, 3, 6), (256, 8, 4, 8), (24, 1, 1, 8), (20, 4, 2, 8)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_gate_pairs_closer_than_a_float(score, E, G, keep, k):
