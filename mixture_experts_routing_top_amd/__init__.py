@@ -582,6 +582,8 @@ def moe_layer_forward(x, logits, k, w_gate, w_up, w_down, act="swiglu", replica_
     else:
         y = moe_expert_ffn_profiled(ffn_in, d["slot_off"], d["slot_expert"], d["n_slots"], w_gate, w_up, w_down,
                                     ffn_events, act, path, b["y_perm"], b["ws_f"], stream, check, row_src=row_src)
+    if residual is not None and "out" in b and residual.data_ptr() == b["out"].data_ptr():
+        del b["out"]   # the last layer's output is still to be read: the combine writes another
     out = moe_combine(y, d["inv_pos"], w, b.get("out"), stream, check)
     b["out"] = out
     res.update(d)

@@ -196,3 +196,20 @@ def test_a_stream_argument_other_than_the_current_one():
         assert torch.equal(d["d_weight"], ref["d_weight"]) and torch.equal(d["d_bias"], ref["d_bias"])
         assert torch.equal(norm, ref_norm)
         del junk
+
+
+def test_layers_that_share_buffers_may_sum_the_last_output():
+    """The residual may be what the last layer left in the buffers."""
+    c = _case("softmax", torch.float32)
+    run = lambda x, bufs, r: moe.moe_layer_forward(x, c["logits"], c["k"], *c["wts"], gate=c["gate"],  # noqa: E731
+                                                   norm=c["norm"], residual=r, bufs=bufs)
+    for name in ("out", "normed", "x_sum"):
+        own = run(c["x"], {}, c["x"])[name]
+        want = run(own, {}, own)
+        bufs = {}
+        last = run(c["x"], bufs, c["x"])[name]
+        kept = last.clone()
+        got = run(last, bufs, last)
+        assert torch.equal(kept, own)
+        for key in ("out", "x_sum", "normed"):
+            assert torch.equal(got[key], want[key]), (name, key)
