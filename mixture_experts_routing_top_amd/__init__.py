@@ -608,10 +608,13 @@ def moe_layer_backward(fwd, logits, w_gate, w_up, w_down, d_out, act="swiglu", g
     reaches fwd["x_sum"] otherwise (e.g. the next layer's residual).  Returns
     dict(d_x, d_logits, d_w_gate, d_w_up, d_w_down), with a norm also d_weight,
     d_bias, d_out (the gradient of fwd["out"]) and, if the forward pass summed a
-    residual, d_residual (the same tensor; d_x does not hold it).  max_norm: the weights' gradients (experts and norm) are clipped in
-    place to that global norm, and the result holds grad_norm."""
+    residual, d_residual (the same tensor; d_x does not hold it).  max_norm: the
+    weights' gradients (experts and norm) are clipped in place to that global norm,
+    and the result holds grad_norm."""
     if fwd.get("x_perm") is None:
         raise ValueError("the forward pass must keep its rows: moe_layer_forward(copy_rows=True)")
+    if norm is not None and "normed" not in fwd:
+        raise ValueError("norm: the forward pass ran without a norm")
     res = {}
     if norm is not None:
         summed = fwd.get("x_sum")

@@ -213,3 +213,10 @@ def test_layers_that_share_buffers_may_sum_the_last_output():
         assert torch.equal(kept, own)
         for key in ("out", "x_sum", "normed"):
             assert torch.equal(got[key], want[key]), (name, key)
+
+
+def test_layer_backward_refuses_a_norm_that_did_not_run():
+    c = _case("softmax", torch.float32)
+    f = moe.moe_layer_forward(c["x"], c["logits"], c["k"], *c["wts"], gate=c["gate"], copy_rows=True)
+    with pytest.raises(ValueError, match="norm"):
+        moe.moe_layer_backward(f, c["logits"], *c["wts"], c["d_normed"], gate=c["gate"], norm=c["norm"])
