@@ -492,10 +492,12 @@ def moe_clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, norm=Non
     """(norm, out): the global norm of the gradients (before clipping) and the gradients
     times min(1, max_norm / (norm + eps)), in place unless `out` gives other tensors
     of the same shapes and dtypes."""
-    r = binding().clip_grads(grads, out, max_norm, eps, norm, workspace, stream, check)
+    grads = list(grads)   # (an iterator is read once)
+    out = grads if out is None else list(out)
+    r = binding().clip_grads(grads, None if out is grads else out, max_norm, eps, norm, workspace, stream, check)
     if type(r) is int:
         _failed("moe_clip_grads", r)
-    return r, list(grads if out is None else out)
+    return r, out
 
 
 # ------------------------------------------------------ one layer, composed

@@ -171,3 +171,16 @@ def test_clip_empty_lists_and_refusals():
         moe.moe_clip_grads(g, math.nan)
     with pytest.raises(ValueError):
         moe.moe_grad_norm(g, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+def test_lists_may_be_any_iterable():
+    a, b = _grads([300, 5000], 3)[:2], _grads([300, 5000], 3)[:2]
+    norm, out = moe.moe_clip_grads(a, 0.01)
+    norm2, out2 = moe.moe_clip_grads((g for g in b), 0.01)
+    assert [o.data_ptr() for o in out2] == [g.data_ptr() for g in b]
+    assert torch.equal(norm, norm2) and all(torch.equal(x, y) for x, y in zip(out, out2))
+    other = [torch.empty_like(g) for g in b]
+    _, out3 = moe.moe_clip_grads(iter(b), 1e9, out=iter(other))
+    assert [o.data_ptr() for o in out3] == [o.data_ptr() for o in other]
+    assert all(torch.equal(x, y) for x, y in zip(out3, b))
+    assert torch.equal(moe.moe_grad_norm(g for g in b), moe.moe_grad_norm(b))
