@@ -113,7 +113,7 @@ int moe_route(const float* logits, int64_t T, int E, int k, int32_t* topk_idx, f
  *   score      s[e]: softmax of the row over the unmasked experts, or
  *              1 / (1 + exp(-logit)); 0 for a masked expert.
  *   bias       fp32 [E] or NULL: added to the scores for the selection only.
- *              NaN counts as the lowest value.
+ *              Infinite ones count as +-1e299, NaN as the lowest value.
  *   n_groups, keep_groups, group_score   the experts in n_groups contiguous
  *              groups of E / n_groups; a group's score is the largest s + b of
  *              its unmasked experts (GROUP_MAX) or the sum of its two largest
@@ -521,7 +521,9 @@ int moe_layer_norm_backward(const void* d_y, const void* x, moe_dtype dt, int64_
  *   norm  fp32 [1] out: sqrt of the sum of all squares of all tensors, summed
  *         in double in an order that only the sizes decide.
  * moe_clip_grads -- the norm, and each gradient scaled to it:
- *   out[i] = grads[i] * min(1, max_norm / (norm + eps)), rounded once.
+ *   out[i] = grads[i] * min(1, max_norm / (norm + eps)): the factor formed in
+ *         double and rounded to 24 bits, the product rounded to fp32 and then to
+ *         the gradient's type.
  * The lists are [host] arrays, read before the call returns: grads (and out)
  * hold device pointers, numel element counts (0 is fine), dt dtypes; types may
  * be mixed and tensors need only the alignment of their elements.  out[i] may
