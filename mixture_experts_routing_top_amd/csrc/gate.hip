@@ -402,16 +402,25 @@ __global__ __launch_bounds__(256, gate_blocks_per_cu(V)) void gate_kernel(GateAr
     hi = row_max(hi);
     wild = !(hi < INFINITY);
     scale = (kZero - 1024.f) / (1.f + (hi - lo));
-    offset = kZero + 16.f - lo * scale;
+    // from the lowest bias on, so that every key lies in 16 .. 2^23 whatever the biases have in common
 #pragma unroll
-    for (int j = 0; j < V; ++j) b[j] = fmaf(b[j], scale, offset);
+    for (int j = 0; j < V; ++j) b[j] = fmaf(b[j] - lo, scale, kZero + 16.f);
+    // what a score of 0 without a bias has in these units; whole, as all values are
+    offset = rintf(fmaf(-lo, scale, kZero + 16.f));
+    // the largest |s + b|, in units.  In double, where the order is defined, it is rounded too
+    const float most = (1.f + fmaxf(fabsf(lo), fabsf(hi))) * scale, defined = most * 0x1p-50f;
     // s: exp2's argument 0.4 u (u = 2^-24), exp2 0.5, the sum 1 and the reciprocal 2; a softmax's
     // sum of up to 32 values in sequence and 4 steps 36 u more, the terms' own errors in it
-    // at most 10 u, and the scaled reciprocal.  b and the sum in units: half a unit each.
-    const float err = (kBy == kBySigmoid ? 5.f : 53.f) * 0x1p-24f * scale + 1.f;
-    near = 2.f * err + 0.5f;
-    // a sum of two: twice that, the sum's rounding and, beyond 2^24, the offset's
-    group_near = !p.top2 ? near : 4.f * err + 3.f + (fabsf(offset) > 2.f * kZero ? fabsf(offset) * 0x1p-21f : 0.f);
+    // at most 10 u, and the scaled reciprocal.  b and the sum are below 2^24 units: half a unit
+    // each, and b - lo u of itself.
+    const float err = (kBy == kBySigmoid ? 5.f : 53.f) * 0x1p-24f * scale + 1.f + (hi - lo) * scale * 0x1p-24f;
+    near = 2.f * err + 0.5f + defined;
+    // a sum of two: twice that; below 2^24 units the offset half a unit (of a group with one
+    // expert it is not taken off) and the sum 1 + most u, each once on both sides; beyond,
+    // steps of at most u of the offset once and of `most` twice
+    const float big = fmaxf(most, fabsf(offset));
+    group_near = !p.top2 ? near
+                         : 4.f * err + 3.f + most * 0x1p-23f + (big > 2.f * kZero ? big * 0x1p-21f : 0.f) + defined;
   }
 #pragma unroll
   for (int j = 0; j < V; ++j) b[j] = j < n ? b[j] : -INFINITY;
