@@ -150,8 +150,9 @@ __device__ __forceinline__ double chosen_weight(bool softmax, bool renorm, float
   } else {
     const double x = lk, z = exp_of(-fabs(x));          // s = 1 / (1 + z) or z / (1 + z)
     double up = x > 0.0 ? 1.0 : z;
-    // ratios survive where every sigmoid underflows: times exp(-top)
-    if (renorm && __any(top < -600.f) && top < 0.f) up = exp_of(x - static_cast<double>(top));
+    // ratios survive where every sigmoid underflows: times exp(-top).  (By the token's own
+    // logits alone: the two forms differ by some 1e-11, which can turn a rounding.)
+    if (renorm && top < -600.f) up = exp_of(x - static_cast<double>(top));
     w = on ? quotient(up, 1.0 + z) : 0.0;
   }
   const double sum = renorm ? row_sum(w) : softmax ? total : 1.0;
