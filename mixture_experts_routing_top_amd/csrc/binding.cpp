@@ -69,23 +69,24 @@ struct Stream {
   std::optional<c10::Stream> other;  // a stream given by the caller
 };
 
+// None (the current stream), a torch stream, its handle as an integer, or any
+// object with the handle as `cuda_stream`
 Stream stream_of(PyObject* o, const at::Device& dev) {
   if (o == Py_None) return {c10::hip::getCurrentHIPStream(dev.index()).stream(), std::nullopt};
+  THPObjectPtr handle(PyIndex_Check(o) ? PyNumber_Index(o) : PyObject_GetAttrString(o, "cuda_stream"));
+  TORCH_CHECK_TYPE(handle, "stream: expected a torch stream, its handle or an object with a cuda_stream");
+  void* raw = PyLong_AsVoidPtr(handle.get());
+  if (PyErr_Occurred()) throw python_error();
   if (PyObject_IsInstance(o, reinterpret_cast<PyObject*>(THPStreamClass)) == 1) {
     const auto* s = reinterpret_cast<THPStream*>(o);
     const c10::Stream st = c10::Stream::unpack3(s->stream_id, static_cast<c10::DeviceIndex>(s->device_index),
                                                 static_cast<c10::DeviceType>(s->device_type));
     TORCH_CHECK_VALUE(st.device_index() == dev.index(), "the stream belongs to another device than the tensors");
-    PyObject* v = PyObject_GetAttrString(o, "cuda_stream");
-    if (!v) throw python_error();
-    void* raw = PyLong_AsVoidPtr(v);
-    Py_DECREF(v);
-    if (PyErr_Occurred()) throw python_error();
     return {raw, st};
   }
-  void* raw = PyLong_AsVoidPtr(o);
-  if (PyErr_Occurred()) throw python_error();
-  return {raw, c10::hip::getStreamFromExternal(static_cast<hipStream_t>(raw), dev.index()).unwrap()};
+  // torch's streams carry the device type of its tensors, which an external HIP stream's does not
+  const auto id = c10::hip::getStreamFromExternal(static_cast<hipStream_t>(raw), dev.index()).id();
+  return {raw, c10::Stream(c10::Stream::UNSAFE, dev, id)};
 }
 
 // A given workspace, checked, or one for this call: memory that goes back to the
