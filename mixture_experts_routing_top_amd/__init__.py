@@ -24,6 +24,10 @@ Those calls take microseconds on small batches, so their arguments are checked
 and their outputs allocated in a native module (csrc/binding.cpp); the others
 go through ctypes.
 
+`stream` is None (the current stream), a torch stream or its handle.  What a call
+allocates belongs to that stream, outputs among them: as with any tensor made on
+one stream and used on another, the caller orders the streams.
+
 Every hot-path call takes `check`: an int32 device tensor of one element
 (zeroed by the caller) that the kernels flag invalid input into;
 moe_check_device_error(check) reads it back.  Output tensors passed in by the
@@ -31,6 +35,7 @@ caller are checked for shape, dtype and device before anything is launched.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -81,6 +86,20 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _on(stream, dev, *given):
+    """The context a call allocates in (nothing to enter where it allocates nothing: every
+    tensor of `given` is there).  What it allocates belongs to the stream it runs on, so
+    torch's allocator hands the memory of a workspace dropped on return, or of an output
+    dropped early, only to later work of the same stream, and takes none that another
+    stream still uses."""
+    if stream is None or (given and all(t is not None for t in given)):
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = _stream(stream).value   # (None for 0)
+        stream = torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -149,8 +168,9 @@ def moe_route(logits: torch.Tensor, k: int, topk_idx=None, topk_w=None, stream=N
     if logits.dtype != torch.float32:
         raise TypeError("router logits must be float32")
     dev = logits.device
-    topk_idx = _out(topk_idx, (T, k), torch.int32, dev, "topk_idx")
-    topk_w = _out(topk_w, (T, k), torch.float32, dev, "topk_w")
+    with _on(stream, dev, topk_idx, topk_w):
+        topk_idx = _out(topk_idx, (T, k), torch.int32, dev, "topk_idx")
+        topk_w = _out(topk_w, (T, k), torch.float32, dev, "topk_w")
     _call("moe_route", _ptr(logits), ctypes.c_int64(T), E, k, _ptr(topk_idx), _ptr(topk_w), _ptr(check),
           _stream(stream))
     return topk_idx, topk_w
@@ -214,9 +234,10 @@ def moe_stats_load_state(state: torch.Tensor, L: int, E: int, window: int, layer
     """Decayed-window popularity, per-expert anomaly flags and [n_flagged, transient]
     of `layer` after iteration `it` was recorded."""
     dev = state.device
-    p_decay = torch.empty(E, dtype=torch.float32, device=dev) if p_decay is None else p_decay
-    anomalous = _i32(E, dev) if anomalous is None else anomalous
-    summary = _i32(2, dev) if summary is None else summary
+    with _on(stream, dev, p_decay, anomalous, summary):
+        p_decay = torch.empty(E, dtype=torch.float32, device=dev) if p_decay is None else p_decay
+        anomalous = _i32(E, dev) if anomalous is None else anomalous
+        summary = _i32(2, dev) if summary is None else summary
     _call("moe_stats_load_state", _ptr(state), ctypes.c_size_t(state.numel() * state.element_size()), L, E, window,
           layer, ctypes.c_int64(it), ctypes.c_double(decay), _ptr(p_decay), _ptr(anomalous), _ptr(summary),
           _stream(stream))
@@ -230,8 +251,9 @@ def moe_plan_replicas(pred: torch.Tensor, total: int, replica_budget: int, pred_
     E = pred.numel()
     if pred.dtype != torch.float32:
         raise TypeError("the prediction must be float32")
-    pred_counts = _i32(E, pred.device) if pred_counts is None else pred_counts
-    replicas = _i32(E, pred.device) if replicas is None else replicas
+    with _on(stream, pred.device, pred_counts, replicas):
+        pred_counts = _i32(E, pred.device) if pred_counts is None else pred_counts
+        replicas = _i32(E, pred.device) if replicas is None else replicas
     _call("moe_plan_replicas", _ptr(pred), E, ctypes.c_int64(total), replica_budget, _ptr(pred_counts),
           _ptr(replicas), _stream(stream))
     return pred_counts, replicas
@@ -244,7 +266,8 @@ def moe_prediction_quality(pred: torch.Tensor, counts: torch.Tensor, replicas=No
     E = pred.numel()
     if pred.dtype != torch.float32 or counts.dtype != torch.int32:
         raise TypeError("pred must be float32 and counts int32")
-    out = torch.empty(4, dtype=torch.float32, device=pred.device) if out is None else out
+    with _on(stream, pred.device, out):
+        out = torch.empty(4, dtype=torch.float32, device=pred.device) if out is None else out
     _call("moe_prediction_quality", _ptr(pred), _ptr(counts), E, _ptr(replicas), top_n, _ptr(out), _stream(stream))
     return out
 
@@ -252,6 +275,9 @@ def moe_prediction_quality(pred: torch.Tensor, counts: torch.Tensor, replicas=No
 # ----------------------------------------------------------------- dispatch
 def moe_dispatch_workspace_bytes(T: int, k: int, E: int) -> int:
     return int(lib().moe_dispatch_workspace_bytes(ctypes.c_int64(T), k, E))
+
+
+_DISPATCH_OUTPUTS = ("x_perm", "perm_src", "inv_pos", "expert_off", "slot_off", "slot_expert", "n_slots")
 
 
 def _dispatch_outputs(out, T, k, H, E, max_slots, dtype, dev, copy=True):
@@ -283,10 +309,11 @@ def moe_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, E: int, replicas=None,
     for t, name in ((replicas, "replicas"), (counts, "counts")):
         if t is not None and (t.numel() != E or t.dtype != torch.int32):
             raise ValueError(f"{name} must be int32 [E]")
-    o = _dispatch_outputs(out, T, k, H, E, max_slots, x.dtype, dev, copy)
     need = moe_dispatch_workspace_bytes(T, k, E)
-    workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else \
-        _bytes_of(workspace, need, "dispatch workspace")
+    with _on(stream, dev, workspace, *((out or {}).get(key) for key in _DISPATCH_OUTPUTS if copy or key != "x_perm")):
+        o = _dispatch_outputs(out, T, k, H, E, max_slots, x.dtype, dev, copy)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else \
+            _bytes_of(workspace, need, "dispatch workspace")
     _call("moe_dispatch", _ptr(x), _dtype_code(x), ctypes.c_int64(T), H, _ptr(topk_idx), k, E, _ptr(counts),
           _ptr(replicas), replica_budget, max_slots, _ptr(o["x_perm"]), _ptr(o["perm_src"]), _ptr(o["inv_pos"]),
           _ptr(o["expert_off"]), _ptr(o["slot_off"]), _ptr(o["slot_expert"]), _ptr(o["n_slots"]), _ptr(workspace),
@@ -304,9 +331,8 @@ def moe_dispatch_noalloc(x: torch.Tensor, topk_idx: torch.Tensor, E: int, replic
         raise ValueError("topk_idx must be int32 [T, k] for the T rows of x")
     k = topk_idx.shape[1]
     max_slots = E + replica_budget if max_slots is None else max_slots
-    need = ("x_perm", "perm_src", "inv_pos", "expert_off", "slot_off", "slot_expert", "n_slots")
-    if out is None or any(key not in out for key in need):
-        raise ValueError(f"moe_dispatch_noalloc allocates nothing: out must hold {need}")
+    if out is None or any(key not in out for key in _DISPATCH_OUTPUTS):
+        raise ValueError(f"moe_dispatch_noalloc allocates nothing: out must hold {_DISPATCH_OUTPUTS}")
     for t, name in ((replicas, "replicas"), (counts, "counts")):
         if t is not None and (t.numel() != E or t.dtype != torch.int32):
             raise ValueError(f"{name} must be int32 [E]")
@@ -324,7 +350,7 @@ def moe_expert_ffn_workspace_bytes(dtype, M: int, H: int, I: int, max_slots: int
     return int(lib().moe_expert_ffn_workspace_bytes(code, ctypes.c_int64(M), H, I, max_slots))
 
 
-def _ffn_args(x_perm, slot_off, slot_expert, n_slots, w_gate, w_up, w_down, y_perm, workspace, row_src=None):
+def _ffn_args(x_perm, slot_off, slot_expert, n_slots, w_gate, w_up, w_down, y_perm, workspace, row_src, stream):
     """row_src (int32 [M], e.g. moe_dispatch's perm_src): x_perm is then the token
     matrix x [T, H] and the FFN gathers row r from x_perm[row_src[r]]."""
     if row_src is not None:
@@ -342,10 +368,11 @@ def _ffn_args(x_perm, slot_off, slot_expert, n_slots, w_gate, w_up, w_down, y_pe
     max_slots = slot_expert.numel()
     if slot_off.numel() != max_slots + 1 or n_slots.numel() != 1:
         raise ValueError("slot_off must hold max_slots + 1 entries and n_slots one")
-    y_perm = _out(y_perm, (M, H), x_perm.dtype, x_perm.device, "y_perm")
     need = moe_expert_ffn_workspace_bytes(x_perm.dtype, M, H, I, max_slots)
-    workspace = torch.empty(need, dtype=torch.uint8, device=x_perm.device) if workspace is None else \
-        _bytes_of(workspace, need, "FFN workspace")
+    with _on(stream, x_perm.device, y_perm, workspace):
+        y_perm = _out(y_perm, (M, H), x_perm.dtype, x_perm.device, "y_perm")
+        workspace = torch.empty(need, dtype=torch.uint8, device=x_perm.device) if workspace is None else \
+            _bytes_of(workspace, need, "FFN workspace")
     return M, H, I, E, max_slots, y_perm, workspace
 
 
@@ -353,7 +380,7 @@ def moe_expert_ffn(x_perm: torch.Tensor, slot_off, slot_expert, n_slots, w_gate,
                    path="grouped", y_perm=None, workspace=None, stream=None, check=None, row_src=None):
     """row_src: see _ffn_args (gathering the rows from x instead of x_perm)."""
     M, H, I, E, max_slots, y_perm, workspace = _ffn_args(x_perm, slot_off, slot_expert, n_slots, w_gate, w_up,
-                                                         w_down, y_perm, workspace, row_src)
+                                                         w_down, y_perm, workspace, row_src, stream)
     _call("moe_expert_ffn", _ptr(x_perm), _ptr(row_src), ctypes.c_int64(x_perm.shape[0]), _dtype_code(x_perm),
           ctypes.c_int64(M), H, I, E, _ptr(slot_off),
           _ptr(slot_expert), _ptr(n_slots), max_slots, _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ACT[act],
@@ -368,7 +395,7 @@ def moe_expert_ffn_profiled(x_perm: torch.Tensor, slot_off, slot_expert, n_slots
     """moe_expert_ffn recording three torch.cuda.Event objects on the stream: before
     the gate/up GEMM, after it, after the down GEMM."""
     M, H, I, E, max_slots, y_perm, workspace = _ffn_args(x_perm, slot_off, slot_expert, n_slots, w_gate, w_up,
-                                                         w_down, y_perm, workspace, row_src)
+                                                         w_down, y_perm, workspace, row_src, stream)
     for e in events:          # torch creates an event's handle on its first record
         if not e.cuda_event:
             e.record(stream if stream is not None else torch.cuda.current_stream())
@@ -388,7 +415,8 @@ def moe_combine(y_perm: torch.Tensor, inv_pos: torch.Tensor, topk_w: torch.Tenso
     T, k = topk_w.shape
     if inv_pos.numel() != T * k or inv_pos.dtype != torch.int32 or topk_w.dtype != torch.float32:
         raise ValueError("inv_pos must be int32 [T, k] and topk_w float32 [T, k]")
-    out = _out(out, (T, H), y_perm.dtype, y_perm.device, "out")
+    with _on(stream, y_perm.device, out):
+        out = _out(out, (T, H), y_perm.dtype, y_perm.device, "out")
     _call("moe_combine", _ptr(y_perm), _dtype_code(y_perm), ctypes.c_int64(M), _ptr(inv_pos), _ptr(topk_w),
           ctypes.c_int64(T), k, H, _ptr(out), _ptr(check), _stream(stream))
     return out
@@ -409,19 +437,17 @@ def _backward(name, gate_grad, x_perm, y_perm, topk_idx, topk_w, inv_pos, expert
     if M != T * k or tuple(y_perm.shape) != (M, H) or tuple(d_out.shape) != (T, H) or d_out.dtype != x_perm.dtype:
         raise ValueError("x_perm and y_perm must be [T*k, H] and d_out [T, H] of the activation dtype")
     o = dict(out or {})
-    o["d_x"] = _out(o.get("d_x"), (T, H), x_perm.dtype, dev, "d_x")
-    o[gate_grad] = _out(o.get(gate_grad), (T, E) if gate_grad == "d_logits" else (T, k), torch.float32, dev, gate_grad)
-    o["d_w_gate"] = _out(o.get("d_w_gate"), tuple(w_gate.shape), w_gate.dtype, dev, "d_w_gate")
-    if w_up is not None:
-        o["d_w_up"] = _out(o.get("d_w_up"), tuple(w_up.shape), w_up.dtype, dev, "d_w_up")
-    o["d_w_down"] = _out(o.get("d_w_down"), tuple(w_down.shape), w_down.dtype, dev, "d_w_down")
     need = moe_backward_workspace_bytes(x_perm.dtype, T, k, H, I, E, act)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        if isinstance(stream, torch.cuda.Stream):   # it is freed on return, while that stream still uses it
-            workspace.record_stream(stream)
-    else:
-        _bytes_of(workspace, need, "backward workspace")
+    with _on(stream, dev):
+        o["d_x"] = _out(o.get("d_x"), (T, H), x_perm.dtype, dev, "d_x")
+        o[gate_grad] = _out(o.get(gate_grad), (T, E) if gate_grad == "d_logits" else (T, k), torch.float32, dev,
+                            gate_grad)
+        o["d_w_gate"] = _out(o.get("d_w_gate"), tuple(w_gate.shape), w_gate.dtype, dev, "d_w_gate")
+        if w_up is not None:
+            o["d_w_up"] = _out(o.get("d_w_up"), tuple(w_up.shape), w_up.dtype, dev, "d_w_up")
+        o["d_w_down"] = _out(o.get("d_w_down"), tuple(w_down.shape), w_down.dtype, dev, "d_w_down")
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else \
+            _bytes_of(workspace, need, "backward workspace")
     _call(name, _ptr(x_perm), _ptr(y_perm), _dtype_code(x_perm), ctypes.c_int64(T), k, H, I, E,
           _ptr(topk_idx), _ptr(topk_w), _ptr(inv_pos), _ptr(expert_off), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
           _ACT[act], _ptr(d_out), _ptr(o["d_x"]), _ptr(o[gate_grad]), _ptr(o["d_w_gate"]), _ptr(o.get("d_w_up")),
@@ -542,6 +568,18 @@ def moe_layer_forward(x, logits, k, w_gate, w_up, w_down, act="swiglu", replica_
     if b.get("_key") != key:
         b.clear()
         b["_key"] = key
+    names = ["ws_d", "y_perm", "ws_f"]
+    if stats_state is not None:
+        names += ["counts", "p_seq", "replicas"] + (["cond", "pred_next"] if layer + 1 < stats_dims[0] else [])
+    if any(name not in b for name in names):
+        sizes = {"ws_d": (moe_dispatch_workspace_bytes(T, k, E), torch.uint8), "y_perm": ((T * k, H), x.dtype),
+                 "ws_f": (moe_expert_ffn_workspace_bytes(x.dtype, T * k, H, I, max_slots), torch.uint8),
+                 "counts": (E, torch.int32), "p_seq": (E, torch.float32), "replicas": (E, torch.int32),
+                 "cond": ((E, E), torch.float32), "pred_next": (E, torch.float32)}
+        with _on(stream, dev):
+            for name in names:
+                if name not in b:
+                    b[name] = torch.empty(sizes[name][0], dtype=sizes[name][1], device=dev)
     if gate is None:
         idx, w = moe_route(logits, k, b.get("idx"), b.get("w"), stream, check)
     else:
@@ -551,12 +589,6 @@ def moe_layer_forward(x, logits, k, w_gate, w_up, w_down, act="swiglu", replica_
     replicas, counts = None, None
     if stats_state is not None:
         L_, E_, win = stats_dims
-        for name, n, dt in (("counts", E, torch.int32), ("p_seq", E, torch.float32), ("replicas", E, torch.int32)):
-            if name not in b:
-                b[name] = torch.empty(n, dtype=dt, device=dev)
-        if layer + 1 < L_:
-            b.setdefault("cond", torch.empty((E, E), dtype=torch.float32, device=dev))
-            b.setdefault("pred_next", torch.empty(E, dtype=torch.float32, device=dev))
         st = moe_stats(stats_state, L_, E_, win, layer, it, idx, prev_topk_idx, k, b["counts"], b["p_seq"],
                        b.get("cond") if layer + 1 < L_ else None, b.get("pred_next") if layer + 1 < L_ else None,
                        replica_budget, b["replicas"] if replica_budget > 0 and planned_replicas is None else None,
@@ -567,17 +599,10 @@ def moe_layer_forward(x, logits, k, w_gate, w_up, w_down, act="swiglu", replica_
     if planned_replicas is not None:
         replicas = planned_replicas
         res["replicas"] = planned_replicas
-    if "ws_d" not in b:
-        b["ws_d"] = torch.empty(moe_dispatch_workspace_bytes(T, k, E), dtype=torch.uint8, device=dev)
     d = moe_dispatch(x, idx, E, replicas, max_slots, b.get("disp"), b["ws_d"], stream, counts, check,
                      replica_budget=replica_budget if replicas is None else 0, copy=copy_rows)
     b["disp"] = d
-    if "y_perm" not in b:
-        b["y_perm"] = torch.empty((T * k, H), dtype=x.dtype, device=dev)
     ffn_in, row_src = (d["x_perm"], None) if copy_rows else (x, d["perm_src"])
-    if "ws_f" not in b:
-        b["ws_f"] = torch.empty(moe_expert_ffn_workspace_bytes(x.dtype, T * k, H, I, max_slots), dtype=torch.uint8,
-                                device=dev)
     if ffn_events is None:
         y = moe_expert_ffn(ffn_in, d["slot_off"], d["slot_expert"], d["n_slots"], w_gate, w_up, w_down, act,
                            path, b["y_perm"], b["ws_f"], stream, check, row_src=row_src)
@@ -667,18 +692,23 @@ def moe_layer_forward_pipelined(x, logits, k, w_gate, w_up, w_down, act="swiglu"
     start = torch.cuda.Event()
     start.record(cs)
     ms.wait_event(start)
-    idx, w = moe_route(logits, k, b.get("idx"), b.get("w"), ms)
+    # what both streams use belongs to the compute stream, which waits for the whole layer
+    with _on(compute_stream, dev):
+        idx = _out(b.get("idx"), (T, k), torch.int32, dev, "topk_idx")
+        w = _out(b.get("w"), (T, k), torch.float32, dev, "topk_w")
+        out = b.get("out")
+        if out is None or out.shape != (T, H) or out.dtype != x.dtype:
+            out = b["out"] = torch.empty((T, H), dtype=x.dtype, device=dev)
+    moe_route(logits, k, idx, w, ms)
     b["idx"], b["w"] = idx, w
-    out = b.get("out")
-    if out is None or out.shape != (T, H) or out.dtype != x.dtype:
-        out = b["out"] = torch.empty((T, H), dtype=x.dtype, device=dev)
     bounds = [T * c // n_chunks for c in range(n_chunks + 1)]
     chunks = [(c, bounds[c], bounds[c + 1]) for c in range(n_chunks) if bounds[c + 1] > bounds[c]]
     t_max = max(t1 - t0 for _, t0, t1 in chunks) if chunks else 0
     if b.get("_ws_key") != (t_max, k, E, H, I, x.dtype):
-        b["ws_d"] = torch.empty(moe_dispatch_workspace_bytes(t_max, k, E), dtype=torch.uint8, device=dev)
-        b["ws_f"] = torch.empty(moe_expert_ffn_workspace_bytes(x.dtype, t_max * k, H, I, E), dtype=torch.uint8,
-                                device=dev)
+        with _on(compute_stream, dev):
+            b["ws_d"] = torch.empty(moe_dispatch_workspace_bytes(t_max, k, E), dtype=torch.uint8, device=dev)
+            b["ws_f"] = torch.empty(moe_expert_ffn_workspace_bytes(x.dtype, t_max * k, H, I, E), dtype=torch.uint8,
+                                    device=dev)
         b["_ws_key"] = (t_max, k, E, H, I, x.dtype)
     disp, done_d = {}, {}
     for c, t0, t1 in chunks:
@@ -695,7 +725,8 @@ def moe_layer_forward_pipelined(x, logits, k, w_gate, w_up, w_down, act="swiglu"
         cb = b[("chunk", c)]
         d = disp[c]
         if "y_perm" not in cb or cb["y_perm"].shape != d["x_perm"].shape:
-            cb["y_perm"] = torch.empty_like(d["x_perm"])
+            with _on(compute_stream, dev):
+                cb["y_perm"] = torch.empty_like(d["x_perm"])
         cs.wait_event(done_d[c])
         moe_expert_ffn(d["x_perm"], d["slot_off"], d["slot_expert"], d["n_slots"], w_gate, w_up, w_down, act,
                        "grouped", cb["y_perm"], b["ws_f"], cs)

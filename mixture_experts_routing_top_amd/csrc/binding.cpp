@@ -10,6 +10,7 @@
 
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/StreamGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/Stream.h>
@@ -64,15 +65,19 @@ at::Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const
   return t;
 }
 
+// A call's stream.  One that the caller gave is the current one while the call
+// allocates: what is allocated then belongs to it in torch's allocator, which hands the
+// memory of a workspace dropped on return, or of an output dropped early, only to later
+// work of the same stream, and takes none that another stream still uses.
 struct Stream {
   void* raw;
-  std::optional<c10::Stream> other;  // a stream given by the caller
+  c10::OptionalStreamGuard current;
 };
 
 // None (the current stream), a torch stream, its handle as an integer, or any
 // object with the handle as `cuda_stream`
 Stream stream_of(PyObject* o, const at::Device& dev) {
-  if (o == Py_None) return {c10::hip::getCurrentHIPStream(dev.index()).stream(), std::nullopt};
+  if (o == Py_None) return {c10::hip::getCurrentHIPStream(dev.index()).stream(), c10::OptionalStreamGuard()};
   THPObjectPtr handle(PyIndex_Check(o) ? PyNumber_Index(o) : PyObject_GetAttrString(o, "cuda_stream"));
   TORCH_CHECK_TYPE(handle, "stream: expected a torch stream, its handle or an object with a cuda_stream");
   void* raw = PyLong_AsVoidPtr(handle.get());
@@ -82,17 +87,15 @@ Stream stream_of(PyObject* o, const at::Device& dev) {
     const c10::Stream st = c10::Stream::unpack3(s->stream_id, static_cast<c10::DeviceIndex>(s->device_index),
                                                 static_cast<c10::DeviceType>(s->device_type));
     TORCH_CHECK_VALUE(st.device_index() == dev.index(), "the stream belongs to another device than the tensors");
-    return {raw, st};
+    return {raw, c10::OptionalStreamGuard(st)};
   }
   // torch's streams carry the device type of its tensors, which an external HIP stream's does not
   const auto id = c10::hip::getStreamFromExternal(static_cast<hipStream_t>(raw), dev.index()).id();
-  return {raw, c10::Stream(c10::Stream::UNSAFE, dev, id)};
+  return {raw, c10::OptionalStreamGuard(c10::Stream(c10::Stream::UNSAFE, dev, id))};
 }
 
-// A given workspace, checked, or one for this call: memory that goes back to the
-// allocator when the call returns, so the allocator hears of a stream other than
-// the current one that still uses it.
-at::Tensor workspace_of(PyObject* o, size_t need, const at::Device& dev, const Stream& s, const char* name) {
+// A given workspace, checked, or one for this call.
+at::Tensor workspace_of(PyObject* o, size_t need, const at::Device& dev, const char* name) {
   if (o != Py_None) {
     const at::Tensor& t = tensor(o);
     on_gpu(t);
@@ -100,9 +103,7 @@ at::Tensor workspace_of(PyObject* o, size_t need, const at::Device& dev, const S
     TORCH_CHECK_VALUE(t.nbytes() >= need, name, ": needs ", need, " bytes, got ", t.nbytes());
     return t;
   }
-  at::Tensor t = at::empty({static_cast<int64_t>(need)}, at::TensorOptions().dtype(at::kByte).device(dev));
-  if (s.other) t.record_stream(*s.other);
-  return t;
+  return at::empty({static_cast<int64_t>(need)}, at::TensorOptions().dtype(at::kByte).device(dev));
 }
 
 int32_t* check_word(PyObject* o, const at::Device& dev) {
@@ -161,9 +162,9 @@ PyObject* gate(PyObject*, Args a, Py_ssize_t n) {
   const int64_t T = lg.size(0), E = lg.size(1), k = small(a[1]);
   TORCH_CHECK_VALUE(E <= INT32_MAX && k >= 0, "k or E out of range");
   auto* bias = static_cast<const float*>(given(a[3], {E}, at::kFloat, dev, "bias"));
+  const Stream s = stream_of(a[11], dev);
   const at::Tensor idx = output(a[9], {T, k}, at::kInt, dev, "topk_idx");
   const at::Tensor w = output(a[10], {T, k}, at::kFloat, dev, "topk_w");
-  const Stream s = stream_of(a[11], dev);
   int32_t* check = check_word(a[12], dev);
   const int groups = small(a[4]), keep = a[5] == Py_None ? groups : small(a[5]), score = small(a[2]), gs = small(a[6]);
   const int renorm = PyObject_IsTrue(a[7]);
@@ -194,8 +195,8 @@ PyObject* gate_backward(PyObject*, Args a, Py_ssize_t n) {
   expect(idx, {T, k}, at::kInt, dev, "topk_idx");
   const at::Tensor& g = tensor(a[2]);
   expect(g, {T, k}, at::kFloat, dev, "d_topk_w");
-  const at::Tensor d = output(a[6], {T, E}, lg.scalar_type(), dev, "d_logits");
   const Stream s = stream_of(a[7], dev);
+  const at::Tensor d = output(a[6], {T, E}, lg.scalar_type(), dev, "d_logits");
   int32_t* check = check_word(a[8], dev);
   const int score = small(a[3]), renorm = PyObject_IsTrue(a[4]);
   const float scale = real(a[5]);
@@ -240,9 +241,9 @@ PyObject* layer_norm(PyObject*, Args a, Py_ssize_t n) {
   const void* residual = given(a[4], x.sizes(), x.scalar_type(), dev, "residual");
   const bool sums = a[4] != Py_None;
   TORCH_CHECK_VALUE(sums || a[6] == Py_None, "x_sum is written with a residual only");
+  const Stream s = stream_of(a[7], dev);
   const at::Tensor y = output(a[5], {T, H}, x.scalar_type(), dev, "y");
   const at::Tensor x_sum = sums ? output(a[6], {T, H}, x.scalar_type(), dev, "x_sum") : at::Tensor();
-  const Stream s = stream_of(a[7], dev);
   const float eps = real(a[3]);
   const int rc = without_gil(dev, [&] {
     return moe_layer_norm(x.data_ptr(), residual, dt, T, static_cast<int>(H), v.weight, v.bias, v.code, eps,
@@ -269,13 +270,13 @@ PyObject* layer_norm_backward(PyObject*, Args a, Py_ssize_t n) {
   const void* skip = given(a[5], x.sizes(), x.scalar_type(), dev, "d_skip");
   TORCH_CHECK_VALUE(a[2] != Py_None || a[7] == Py_None, "d_weight: there is no such parameter");
   TORCH_CHECK_VALUE(a[3] != Py_None || a[8] == Py_None, "d_bias: there is no such parameter");
+  const Stream s = stream_of(a[10], dev);
   const at::Tensor dx = output(a[6], {T, H}, x.scalar_type(), dev, "d_x");
   const at::Tensor dw = a[2] == Py_None ? at::Tensor() : output(a[7], {H}, v.type, dev, "d_weight");
   const at::Tensor db = a[3] == Py_None ? at::Tensor() : output(a[8], {H}, v.type, dev, "d_bias");
-  const Stream s = stream_of(a[10], dev);
   const size_t need = dw.defined() || db.defined()
                           ? moe_layer_norm_backward_workspace_bytes(T, static_cast<int>(H)) : 0;
-  const at::Tensor ws = need ? workspace_of(a[9], need, dev, s, "layer norm workspace") : at::Tensor();
+  const at::Tensor ws = need ? workspace_of(a[9], need, dev, "layer norm workspace") : at::Tensor();
   const float eps = real(a[4]);
   const int rc = without_gil(dev, [&] {
     return moe_layer_norm_backward(dy.data_ptr(), x.data_ptr(), dt, T, static_cast<int>(H), v.weight, v.code, eps, skip,
@@ -341,11 +342,11 @@ PyObject* clip_grads(PyObject*, Args a, Py_ssize_t n) {
       l.out.push_back(g.data_ptr());
     }
   }
-  const at::Tensor norm = output(a[4], {1}, at::kFloat, dev, "norm");
   const Stream s = stream_of(a[6], dev);
+  const at::Tensor norm = output(a[4], {1}, at::kFloat, dev, "norm");
   int32_t* check = check_word(a[7], dev);
   const size_t need = moe_grad_norm_workspace_bytes();
-  const at::Tensor ws = workspace_of(a[5], need, dev, s, "gradient norm workspace");
+  const at::Tensor ws = workspace_of(a[5], need, dev, "gradient norm workspace");
   const bool clips = a[2] != Py_None;
   const float max_norm = clips ? real(a[2]) : 0.f, eps = clips ? real(a[3]) : 0.f;
   const int rc = without_gil(dev, [&] {
