@@ -527,6 +527,17 @@ def moe_clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, norm=Non
 
 
 # ------------------------------------------------------ one layer, composed
+def _gate_formula(gate):
+    """What the gradient of a gate's weights hangs on, from its options (None: moe_route)."""
+    g = gate or {}
+    return _SCORE[g.get("score", "softmax")], bool(g.get("renorm", True)), float(g.get("scale", 1.0))
+
+
+def _norm_formula(norm):
+    """The same of a norm: its eps and whether it has a weight (None: no norm)."""
+    return None if norm is None else (float(norm.get("eps", 1e-5)), norm.get("weight") is not None)
+
+
 def moe_layer_forward(x, logits, k, w_gate, w_up, w_down, act="swiglu", replica_budget=0, stats_state=None,
                       stats_dims=None, layer=0, it=0, prev_topk_idx=None, path="grouped", bufs=None, stream=None,
                       planned_replicas=None, check=None, ffn_events=None, copy_rows=False, gate=None, residual=None,
@@ -555,7 +566,10 @@ def moe_layer_forward(x, logits, k, w_gate, w_up, w_down, act="swiglu", replica_
     routes in moe_route's place.  norm: a dict of moe_layer_norm's weight, bias
     and eps (may be empty): the layer's output is normed, after the sum with
     `residual` (e.g. x) where that is given; the result then holds `normed` and
-    `x_sum`."""
+    `x_sum`.  With shared `bufs` the next call writes over this one's result: a
+    layer whose backward pass is to follow needs bufs of its own until then.
+    The result also records the gate's and the norm's formulas, which
+    moe_layer_backward compares."""
     T, E = logits.shape
     H = x.shape[1]
     I = w_gate.shape[1]
@@ -585,7 +599,7 @@ def moe_layer_forward(x, logits, k, w_gate, w_up, w_down, act="swiglu", replica_
     else:
         idx, w = moe_gate(logits, k, topk_idx=b.get("idx"), topk_w=b.get("w"), stream=stream, check=check, **gate)
     b["idx"], b["w"] = idx, w
-    res = {"idx": idx, "w": w}
+    res = {"idx": idx, "w": w, "gate_formula": _gate_formula(gate), "norm_formula": _norm_formula(norm)}
     replicas, counts = None, None
     if stats_state is not None:
         L_, E_, win = stats_dims
@@ -631,8 +645,10 @@ def moe_layer_backward(fwd, logits, w_gate, w_up, w_down, d_out, act="swiglu", g
     norm -> combine, experts and dispatch -> gate.
 
     d_out is the gradient of fwd["normed"] where the layer had a norm (pass the
-    same `norm` and `gate` dicts), else of fwd["out"]; d_x_sum the gradient that
-    reaches fwd["x_sum"] otherwise (e.g. the next layer's residual).  Returns
+    same `norm` and `gate` dicts: another score, renorm, scale, eps or a missing
+    weight is refused; a bias left out only leaves out d_bias), else of
+    fwd["out"]; d_x_sum the gradient that reaches fwd["x_sum"] otherwise (e.g. the
+    next layer's residual).  Returns
     dict(d_x, d_logits, d_w_gate, d_w_up, d_w_down), with a norm also d_weight,
     d_bias, d_out (the gradient of fwd["out"]) and, if the forward pass summed a
     residual, d_residual (the same tensor; d_x does not hold it).  max_norm: the
@@ -642,6 +658,10 @@ def moe_layer_backward(fwd, logits, w_gate, w_up, w_down, d_out, act="swiglu", g
         raise ValueError("the forward pass must keep its rows: moe_layer_forward(copy_rows=True)")
     if norm is not None and "normed" not in fwd:
         raise ValueError("norm: the forward pass ran without a norm")
+    for name, given, formula in (("gate", gate, _gate_formula), ("norm", norm, _norm_formula)):
+        ran = fwd.get(name + "_formula", formula(given))
+        if formula(given) != ran:
+            raise ValueError(f"{name}: not the forward pass's ({formula(given)}, which ran {ran})")
     res = {}
     if norm is not None:
         summed = fwd.get("x_sum")
