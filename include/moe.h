@@ -490,8 +490,10 @@ int moe_backward_gated(const void* x_perm, const void* y_perm, moe_dtype dt, int
  *   both NULL: s = x);  y = (s - mean) / sqrt(var + eps) * weight + bias
  * over the H elements of each of the T rows; mean, var and the products in
  * fp32, y rounded once.  weight and bias [H] in `w_dt` (fp32, or `dt`); either
- * may be NULL (1 and 0).  A row with a NaN or infinity gives NaN in that row
- * alone; squares of |s - mean| beyond 1e18 overflow.  y or x_sum may be x or
+ * may be NULL (1 and 0).  A row with a NaN or an infinity, or whose magnitudes
+ * add up to more than 3.4e38 (fp32's range: at H = 4096 values of 8e34), gives
+ * NaN in that row alone; squares of |s - mean| beyond 1e18 overflow; from a mean
+ * of some 1e5 sqrt(var + eps) on y loses precision.  y or x_sum may be x or
  * residual itself (the same buffer), not each other.
  * Limits: 1 <= H <= 16384, 0 <= T < 2^40, eps > 0; rows need only the
  * alignment of their elements.
