@@ -398,7 +398,8 @@ def moe_expert_ffn_profiled(x_perm: torch.Tensor, slot_off, slot_expert, n_slots
                                                          w_down, y_perm, workspace, row_src, stream)
     for e in events:          # torch creates an event's handle on its first record
         if not e.cuda_event:
-            e.record(stream if stream is not None else torch.cuda.current_stream())
+            with _on(stream, x_perm.device):
+                e.record()
     evs = (ctypes.c_void_p * 3)(*(e.cuda_event for e in events))
     _call("moe_expert_ffn_profiled", _ptr(x_perm), _ptr(row_src), ctypes.c_int64(x_perm.shape[0]),
           _dtype_code(x_perm), ctypes.c_int64(M), H, I, E, _ptr(slot_off),

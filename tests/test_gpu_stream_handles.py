@@ -46,3 +46,19 @@ def test_a_stream_that_is_none_is_refused():
     for bad in ("stream", 1.5, object()):
         with pytest.raises(TypeError):
             moe.moe_layer_norm(x, stream=bad)
+
+
+@pytest.mark.parametrize("form", ["stream", "integer", "object", "external", "default"])
+def test_the_profiled_ffn_takes_every_form_of_a_stream(form):
+    """Its events, whose handles do not exist before the call, are of that stream too."""
+    gen = torch.Generator().manual_seed(6)
+    rnd = lambda *s: torch.randn(s, generator=gen).cuda()  # noqa: E731
+    x, lg = rnd(60, 128), rnd(60, 8)
+    wts = [rnd(8, 192, 128), rnd(8, 192, 128), rnd(8, 128, 192)]
+    want = moe.moe_layer_forward(x, lg, 2, *wts)["out"]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    events = [torch.cuda.Event(enable_timing=True) for _ in range(3)]
+    got = moe.moe_layer_forward(x, lg, 2, *wts, ffn_events=events, stream=_forms(s)[form])["out"]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and events[0].elapsed_time(events[2]) >= 0
