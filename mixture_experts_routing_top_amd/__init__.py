@@ -37,6 +37,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 
 import torch
 
@@ -85,7 +86,7 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else operator.index(stream))
 
 
 def _on(stream, dev, *given):

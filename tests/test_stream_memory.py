@@ -118,3 +118,11 @@ def test_pipelined_allocations_belong_to_a_stream_that_waits_for_their_use(alloc
     assert allocations and all(s in (compute, OTHER) for s, _ in allocations)
     need = moe.moe_expert_ffn_workspace_bytes(torch.float32, T // 3 * K, H, I, E)
     assert (compute, need) in allocations
+
+
+@pytest.mark.parametrize("bad", [1.5, "7", b"7", None.__class__, object()])
+def test_what_is_no_stream_is_refused(bad):
+    """A number that is not whole is no handle: cut to one, it would name memory."""
+    with pytest.raises(TypeError):
+        moe._stream(bad)
+    assert moe._stream(12).value == 12 and moe._stream(SIDE).value == 2 and moe._stream(0).value is None
