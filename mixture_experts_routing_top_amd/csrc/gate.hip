@@ -21,13 +21,15 @@
 // lies clearly below the k-th.  A token for which that does not do, or whose last
 // kept group is as close to the first one left out, is done again by the whole wave
 // in double (gate_token).  In those rows a gap among the first nine below 2^-20 of the
-// largest, about what the bound asks, was there 280 times; every token in double costs
-// four times the time.
+// largest, about what the bound asks, was there 280 times.  A batch whose tokens all
+// come to the doubles takes six times as long (65536 x 256, biased sigmoids in 8 groups:
+// 258 us with one bias -inf or -1e9, 252 with 2^20 in every bias; without a bias, in one
+// group, 22 us, 131 with one logit 30 above the rest, 548 with all logits equal).
 //
-// Bound by the vector instructions, 834 (counted) for four tokens of 256 experts and
-// k = 8: 35 % in the k + 1 rounds of selection, 20 % in the scores, 12 % in the
-// weights.  65536 tokens, biased sigmoids in 8 groups, bf16: 39 us (168 us with a
-// wave a token, in double); 16384 x 160, softmax, float32: 9.4 us (34).
+// 827 vector instructions (counted) for four tokens of 256 experts and k = 8, about a third
+// in the k + 1 rounds of selection; they take 74 % of the issue slots.  65536 tokens,
+// biased sigmoids in 8 groups, bf16: 33 - 40 us by how many tokens are in doubt (168 us
+// with a wave a token, in double); 16384 x 160, softmax, float32: 8.3 - 9 us (34).
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -129,7 +131,8 @@ __device__ __forceinline__ double bias_of(float b) {
   return fmin(fmax(static_cast<double>(b), -kBiasLimit), kBiasLimit);
 }
 
-// a / b in double for b in the normal range, to about an ulp
+// a / b in double for b in the normal range, to about an ulp: Newton's iteration for
+// 1 / b, then the quotient corrected by its own remainder
 __device__ __forceinline__ double quotient(double a, double b) {
   double r = __builtin_amdgcn_rcp(b);
   r = fma(fma(-b, r, 1.0), r, r);
@@ -356,7 +359,9 @@ constexpr float kZero = 8388608.f;     // 2^23: a key's value of 0
 
 // Lane i of a token's 16 holds `per` consecutive experts (at most V) of one group:
 // groups begin at multiples of `lanes` lanes.  A wave takes 4 tokens at a time.
-// Blocks a CU holds, by the registers the slots take; a launch has just as many.
+// Blocks a CU is given: what the variant with the most registers (biased sigmoids: 131
+// at 12 slots, 139 at 16, 174 at 32) leaves room for.  Those by the logit or a softmax
+// (105 - 118 at 12 and 16) would fit four; they were not tried with them.
 constexpr int gate_blocks_per_cu(int V) { return V > 16 ? 2 : V > 8 ? 3 : 4; }
 
 template <bool kBf16, int V, By kBy, Weights kW>

@@ -12,8 +12,10 @@
 // deviations corrects the mean's own rounding, so a row whose mean is large
 // against its spread keeps full precision.  The backward pass forms the
 // statistics again from s (the row is in registers anyway) instead of reading
-// saved ones.  8192 x 4096 bf16: with residual 46 us for 268 MB (5.8 TB/s), backward
-// with d_skip 58 us for the same and 7 for the columns' sums.
+// saved ones.  8192 x 4096 bf16 (profiler, inputs out of cache): with residual 44 us for
+// 268 MB, of which the rows written last may still lie in the last-level cache when it
+// ends (51 us a call in a run of them: 5.3 TB/s); backward with d_skip 57 us for the same
+// and 7 for the columns' sums.
 //
 // TPR threads own a row, NV pieces of 8 consecutive elements each.  A block
 // keeps its columns of weight and bias (and the backward's column sums) in
@@ -98,8 +100,9 @@ __device__ __forceinline__ void load_row(const void* p, int64_t row, int64_t T, 
   }
 }
 
-// Blocks a CU holds of the forward kernel, by the registers it needs with a row
-// ahead: 6 waves a SIMD with one piece a thread, 4 with two.  The launch has just as
+// Blocks a CU is given of the forward kernel, by the registers the float32 kernel needs
+// with a row ahead: 6 waves a SIMD with one piece a thread, 4 with two (the bf16 kernel
+// takes fewer and would leave room for more).  The launch has just as
 // many, and the next row is loaded while one is reduced: 8192 x 4096 bf16 with
 // residual takes 47 us (5.7 TB/s), without the row ahead 50 on 5 blocks a CU, 56 on
 // 4, 57 on 8 and 62 on a block for each row; 4096 x 8192 takes 46 against 55.
@@ -187,8 +190,9 @@ struct NormBwdArgs {
   float eps;
 };
 
-// Blocks a CU holds of the backward kernel, by the registers it needs: 4 waves a
-// SIMD with one piece a thread, else 2.
+// Blocks a CU is given of the backward kernel, by the registers the float32 kernel needs:
+// 4 waves a SIMD with one piece a thread, else 2 (179 - 182 registers; the bf16 kernel takes
+// 152 and would fit three).
 constexpr int bwd_blocks_per_cu(int tpr, int nv) { return tpr > 256 ? 1 : nv == 1 ? 4 : 2; }
 
 template <bool kBf16, bool kWBf16, int TPR, int NV, int R>
@@ -372,7 +376,7 @@ Shape shape_of(int H, bool backward) {
 constexpr int kFwdThreads = 256, kBwdThreads = 256;
 constexpr int kCUs = 256;
 
-// As many blocks as the card holds at once, so that none waits for another.  Where
+// As many blocks as the CUs are given at once, so that none waits for another.  Where
 // the rows do not fill them, three rows a thread group from 128 blocks on: each block
 // costs a row of column sums, written and read again (bf16 1024 x 2048: 20.7 us with
 // one row each, 15.1 with three; 300 x 5120: 19.4, 15.5; 64 x 4096: 8.6, 10.9).
