@@ -124,7 +124,8 @@ int moe_route(const float* logits, int64_t T, int E, int k, int32_t* topk_idx, f
  *              descending.  Without a bias an expert's place is its logit's.
  *              Masked experts come after all others, in index order.  Ties, of
  *              groups and of experts, go to the lower index; scores are compared
- *              in double, so two that differ only there do not tie.
+ *              in double, so two that differ only there do not tie (and sums that
+ *              differ by no more than a double's rounding may go either way).
  *   topk_w     fp32 [T, k] out: scale * s, or with `renorm` scale * s / (sum of
  *              the k chosen s).  0 for a masked expert (a row with nothing
  *              unmasked gets zeros).

@@ -562,7 +562,10 @@ __global__ __launch_bounds__(256, gate_blocks_per_cu(V)) void gate_kernel(GateAr
     bool same = lk == __int_as_float(next_lane(__float_as_int(lk)));
     if constexpr (kBy != kByLogit) {
       const float bk = p.bias && some ? p.bias[e] : 0.f;
-      same = same && bk == __int_as_float(next_lane(__float_as_int(bk)));
+      // (moved in all lanes, before the comparison: from a lane that a branch has switched
+      // off its reader would get its own value back)
+      const float next_bk = __int_as_float(next_lane(__float_as_int(bk)));
+      same &= bk == next_bk;
     }
     const bool close = some && l16 < p.k && q_next >= 3u && static_cast<float>(q - q_next) <= near;
     doubt |= close && !same;
