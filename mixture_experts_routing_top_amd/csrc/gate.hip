@@ -360,7 +360,7 @@ constexpr float kZero = 8388608.f;     // 2^23: a key's value of 0
 // Lane i of a token's 16 holds `per` consecutive experts (at most V) of one group:
 // groups begin at multiples of `lanes` lanes.  A wave takes 4 tokens at a time.
 // Blocks a CU is given: what the variant with the most registers (biased sigmoids: 131
-// at 12 slots, 139 at 16, 174 at 32) leaves room for.  Those by the logit or a softmax
+// at 12 slots, 139 at 16, 174 - 195 at 32) leaves room for.  Those by the logit or a softmax
 // (105 - 118 at 12 and 16) would fit four; they were not tried with them.
 constexpr int gate_blocks_per_cu(int V) { return V > 16 ? 2 : V > 8 ? 3 : 4; }
 
