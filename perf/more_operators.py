@@ -1,0 +1,356 @@
+"""Cases for a layer held in few bits: expert weights in microscaled 4-bit blocks, activations kept in 8 bits.
+
+    keep              rows quantised to blocks of 32 values with one power-of-two scale each, and the values
+                      they stand for back again: activations kept for the backward pass (8 bits; restored
+                      expert by expert, one row for each token and slot), weights made ready to be served (4 bits)
+    ffn               the experts' FFN on 4-bit weights; activations quantised to 8 or 4 bits by row blocks
+    combine_backward  the gradient of the weighted gather back to token order, from expert outputs kept in 8 bits
+
+A case is a dict of plain values; prepare() draws its inputs on the GPU, run() makes one pass (plain torch,
+or the library's calls where `own` is set) and exact() evaluates the definition in float64.
+
+The format: 32 consecutive values of a row share the scale 2^(b - 127), b one byte; the values are e2m1 (two a
+byte, the first in the low half) or e4m3, rounded to nearest even.  The scale is the smallest for which the
+block's largest magnitude still rounds to the format's largest value or less.
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+BLOCK = 32
+# exponent of the format's largest value; what, added to a float's bits, carries into the exponent just
+# where the mantissa would round past the largest value (1.75 and up of e2m1, above 1.8125 of e4m3)
+EMAX = {"fp4": 2, "fp8": 8}
+CARRY = {"fp4": 0x200000, "fp8": 0x17FFFF}
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+# ------------------------------------------------------------------------------------------- cases
+def listed():
+    return [
+        # the few rows of a small step: latency is all that counts
+        dict(name="keep_few", op="keep", R=16, K=1024, fmt="fp8", dtype="bf16", rows=2),
+        # a training batch of 8 experts, top 2, hidden size 4096: kept by token, restored by row
+        dict(name="keep_batch", op="keep", R=8192, K=4096, fmt="fp8", dtype="bf16", rows=2),
+        # the weights of one expert matrix after the other, made ready for serving; float32 masters of an odd width
+        dict(name="keep_weights", op="keep", R=28671, K=4095, fmt="fp4", dtype="f32", rows=0),
+        # one decoded token at 6 of 160 experts
+        dict(name="ffn_token", op="ffn", T=1, H=5120, I=1536, E=160, k=6, act="swiglu", fmt="fp8", dtype="bf16"),
+        # a batch of sequences being decoded: most experts get a few rows, some none
+        dict(name="ffn_decode", op="ffn", T=61, H=5120, I=1536, E=160, k=6, act="swiglu", fmt="fp8", dtype="bf16"),
+        # a prompt at the same experts, activations in 4 bits
+        dict(name="ffn_prompt", op="ffn", T=1021, H=5120, I=1536, E=160, k=6, act="swiglu", fmt="fp4", dtype="bf16"),
+        # GELU experts of hidden size 1024
+        dict(name="ffn_gelu", op="ffn", T=4001, H=1024, I=4096, E=32, k=2, act="gelu", fmt="fp8", dtype="bf16"),
+        # the largest batch of long prompts at 8 experts, in 8 and in 4 bits
+        dict(name="ffn_batch", op="ffn", T=8192, H=4096, I=14336, E=8, k=2, act="swiglu", fmt="fp8", dtype="bf16"),
+        dict(name="ffn_batch_fp4", op="ffn", T=8192, H=4096, I=14336, E=8, k=2, act="swiglu", fmt="fp4", dtype="bf16"),
+        # a small step's gradient, float32 rows
+        dict(name="combine_bwd_few", op="combine_backward", T=61, k=2, H=1024, dtype="f32"),
+        # training batches: top 2 and top 6
+        dict(name="combine_bwd_batch", op="combine_backward", T=8192, k=2, H=4096, dtype="bf16"),
+        dict(name="combine_bwd_top6", op="combine_backward", T=16001, k=6, H=5120, dtype="bf16"),
+    ]
+
+
+def _spread(rng, low, high):
+    """A whole number between low and high, spread evenly over its logarithm."""
+    return max(low, min(high, int(round(math.exp(rng.uniform(math.log(low), math.log(high)))))))
+
+
+def draw(rng):
+    op = rng.choice(["keep", "ffn", "ffn", "combine_backward"])
+    if op == "keep":
+        K = _spread(rng, 64, 16384)
+        return dict(op=op, R=_spread(rng, 1, max(1, 60_000_000 // K)), K=K, fmt=rng.choice(["fp8", "fp4"]),
+                    dtype=rng.choice(["bf16", "f32"]), rows=rng.choice([0, 1, 2, 4]))
+    if op == "combine_backward":
+        H, k = 8 * _spread(rng, 8, 1024), rng.randint(1, 8)
+        return dict(op=op, T=_spread(rng, 1, max(1, 240_000_000 // (H * k))), k=k, H=H, dtype=rng.choice(["bf16", "f32"]))
+    E = rng.choice([4, 8, 16, 32, 64, 160])
+    H, I, k = 128 * _spread(rng, 2, 48), 128 * _spread(rng, 2, 48), rng.randint(1, min(E, 8))
+    while E * H * I > 1_400_000_000:
+        E //= 2
+    k = min(k, E)
+    T = _spread(rng, 1, max(1, min(16384, int(2.5e11 / (H * I * k)))))
+    return dict(op=op, T=T, H=H, I=I, E=E, k=k, act=rng.choice(["swiglu", "swiglu", "gelu"]),
+                fmt=rng.choice(["fp8", "fp4"]), dtype="bf16")
+
+
+# ------------------------------------------------------------------- the format, in elementary operations
+def _scale_bytes(v, fmt):
+    """One byte a block of v [..., blocks, 32] (float32): its scale is 2^(byte - 127)."""
+    bits = v.abs().amax(-1).view(torch.int32)
+    byte = ((bits + CARRY[fmt]) >> 23) - EMAX[fmt]
+    return torch.where(bits >= 0x7F800000, torch.full_like(byte, 255), byte.clamp(0, 254))
+
+
+def _round_to(a, fmt):
+    """a (float64, at most the format's largest after rounding) to the format's nearest value, ties to even."""
+    if fmt == "fp4":
+        m = a.abs()
+        step = torch.where(m < 2, 0.5, torch.where(m < 4, 1.0, 2.0)).to(a.dtype)
+    else:
+        step = torch.exp2((torch.frexp(a).exponent - 1).clamp(min=-6).to(a.dtype) - 3)
+    return torch.round(a / step) * step
+
+
+def _quantised(x, fmt):
+    """(values in the format float64 [..., blocks, 32], scale bytes [..., blocks]) of the rows of x."""
+    K = x.shape[-1]
+    blocks = -(-K // BLOCK)
+    v = x.float()
+    if K % BLOCK:
+        v = torch.cat([v, v.new_zeros(*x.shape[:-1], blocks * BLOCK - K)], -1)
+    v = v.view(*x.shape[:-1], blocks, BLOCK)
+    byte = _scale_bytes(v, fmt)
+    return _round_to(v.double() * torch.exp2(127.0 - byte.double())[..., None], fmt), byte
+
+
+def _values(x, fmt):
+    """The float32 values that the quantised rows of x stand for."""
+    q, byte = _quantised(x, fmt)
+    v = q * torch.exp2(byte.double() - 127.0)[..., None]
+    return v.reshape(*x.shape[:-1], -1)[..., :x.shape[-1]].float()
+
+
+def _encode(x, fmt):
+    """Codes and scale bytes as they are kept: uint8 [..., K / 2 or K] and uint8 [..., K / 32]."""
+    q, byte = _quantised(x, fmt)
+    q = q.float().reshape(*x.shape[:-1], -1)
+    if fmt == "fp8":
+        return q.to(torch.float8_e4m3fn).view(torch.uint8).contiguous(), byte.to(torch.uint8)
+    code = torch.bucketize(q.abs(), torch.tensor(E2M1, device=q.device)) + 8 * (q < 0)
+    return (code[..., 0::2] + 16 * code[..., 1::2]).to(torch.uint8), byte.to(torch.uint8)
+
+
+def _decode(codes, byte, fmt, dtype=torch.float32):
+    if fmt == "fp8":
+        v = codes.view(torch.float8_e4m3fn).to(dtype)
+    else:
+        table = torch.tensor(E2M1 + tuple(-m for m in E2M1), device=codes.device, dtype=dtype)
+        v = table[torch.stack([codes & 15, codes >> 4], -1).long()].flatten(-2)
+    scale = torch.exp2(byte.to(dtype) - 127.0)
+    return (v.view(*byte.shape, BLOCK) * scale[..., None]).flatten(-2)
+
+
+# ------------------------------------------------------------------------------------------ inputs
+def _randn(gen, *shape):
+    return torch.randn(shape, generator=gen, device=gen.device, dtype=torch.float32)
+
+
+def _rows(gen, T, H, dtype):
+    """Hidden states: a shifted mean, and a few channels far larger than the others."""
+    channel = 1.0 + 29.0 * (torch.rand(H, generator=gen, device=gen.device) < 0.003).float()
+    return ((_randn(gen, T, H) + 0.25) * channel).to(dtype)
+
+
+def _routing(gen, T, E, k):
+    """The k experts of each token, a few experts hot, and a dispatch of them: the row of each (token, slot), the
+    token of each row, the rows' offsets."""
+    rank = torch.randperm(E, generator=gen, device=gen.device).float()
+    idx = torch.topk(_randn(gen, T, E) - 0.8 * torch.log(rank + 1.0), k, dim=1).indices
+    order = torch.argsort(idx.flatten(), stable=True)
+    inv = torch.empty_like(order)
+    inv[order] = torch.arange(T * k, device=order.device)
+    off = torch.zeros(E + 1, dtype=torch.int64, device=order.device)
+    off[1:] = torch.cumsum(torch.bincount(idx.flatten(), minlength=E), 0)
+    return idx, inv.view(T, k).int(), (order // k).int(), off.int()
+
+
+def _expert_weights(gen, E, N, K):
+    """E matrices [N, K], quantised one after the other."""
+    pairs = [_encode(_randn(gen, N, K) / math.sqrt(K), "fp4") for _ in range(E)]
+    return torch.stack([q for q, _ in pairs]), torch.stack([b for _, b in pairs])
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda" if torch.cuda.is_available() else "cpu").manual_seed(seed)
+    dev, op, st = gen.device, case["op"], dict(case=case)
+    dt = DTYPES[case["dtype"]]
+    if op == "keep":
+        st["x"] = _rows(gen, case["R"], case["K"], dt)
+        st["rows"] = None
+        if case["rows"]:   # a dispatch's rows: every token as often as it has experts, in the experts' order
+            order = torch.randperm(case["R"] * case["rows"], generator=gen, device=dev)
+            st["rows"] = (order // case["rows"]).int()
+    elif op == "ffn":
+        T, H, I, E, k = (case[key] for key in "T H I E k".split())
+        st["x"] = _rows(gen, T, H, dt)
+        _, _, st["perm_src"], st["slot_off"] = _routing(gen, T, E, k)
+        st["slot_expert"] = torch.arange(E, dtype=torch.int32, device=dev)
+        st["n_slots"] = torch.full((1,), E, dtype=torch.int32, device=dev)
+        st["w_gate"] = _expert_weights(gen, E, I, H)
+        st["w_up"] = _expert_weights(gen, E, I, H) if case["act"] == "swiglu" else None
+        st["w_down"] = _expert_weights(gen, E, H, I)
+    else:
+        T, k, H = case["T"], case["k"], case["H"]
+        _, st["inv_pos"], _, _ = _routing(gen, T, 8 if k <= 2 else 32, k)
+        st["topk_w"] = torch.softmax(_randn(gen, T, k), 1)
+        codes = [_encode(part, "fp8") for part in _randn(gen, T * k, -(-H // BLOCK) * BLOCK).split(16384)]
+        st["y_kept"] = (torch.cat([q for q, _ in codes])[:, :H].contiguous(), torch.cat([b for _, b in codes]))
+        st["d_out"] = (0.01 * _randn(gen, T, H)).to(dt)
+    if dev.type == "cuda":
+        torch.cuda.synchronize()
+    return st
+
+
+# ------------------------------------------------------------------------------------ plain forms
+def _keep_plain(st):
+    v = _values(st["x"], st["case"]["fmt"]).to(st["x"].dtype)
+    return v if st["rows"] is None else v[st["rows"].long()]
+
+
+def _act(g, u):
+    if u is None:
+        return 0.5 * g * (1.0 + torch.erf(g * math.sqrt(0.5)))
+    return g / (1.0 + torch.exp(-g)) * u
+
+
+def _ffn_plain(st):
+    """The experts that have rows, each padded to the most rows that one of them has."""
+    fmt = st["case"]["fmt"]
+    x = _values(st["x"], fmt)[st["perm_src"].long()]
+    off = st["slot_off"].long()
+    count = off[1:] - off[:-1]
+    live = torch.nonzero(count).flatten()
+    most = int(count.max())
+    place = torch.arange(most, device=x.device)
+    there = place[None, :] < count[live][:, None]                  # [experts, most]
+    row = (off[live][:, None] + place[None, :]).clamp(max=x.shape[0] - 1)
+    xe = torch.where(there[..., None], x[row], torch.zeros((), device=x.device))
+
+    def product(a, w):
+        return torch.matmul(a, _decode(w[0][live], w[1][live], "fp4").transpose(1, 2))
+
+    h = _act(product(xe, st["w_gate"]), None if st["w_up"] is None else product(xe, st["w_up"]))
+    ye = product(_values(h, fmt), st["w_down"])
+    y = torch.empty_like(x)
+    y[row[there]] = ye[there]
+    return y.to(st["x"].dtype)
+
+
+def _combine_backward_plain(st):
+    H = st["d_out"].shape[1]
+    codes, byte = st["y_kept"]
+    pad = byte.shape[1] * BLOCK - H
+    y = _decode(torch.nn.functional.pad(codes, (0, pad)), byte, "fp8")[:, :H]
+    inv, w, d_out = st["inv_pos"].long(), st["topk_w"], st["d_out"].float()
+    d_w = (d_out[:, None, :] * y[inv]).sum(2)
+    d_y = torch.empty((inv.numel(), H), dtype=st["d_out"].dtype, device=y.device)
+    d_y[inv.flatten()] = (w[:, :, None] * d_out[:, None, :]).to(d_y.dtype).flatten(0, 1)
+    return {"d_y": d_y, "d_topk_w": d_w}
+
+
+# ------------------------------------------------------------------------------------------- a pass
+def _library(st):
+    import mixture_experts_routing_top_amd as moe
+    c = st["case"]
+    if c["op"] == "keep":
+        kept, scale = moe.moe_mx_quantize(st["x"], c["fmt"])
+        return moe.moe_mx_dequantize(kept, scale, c["fmt"], st["x"].dtype, cols=c["K"], rows=st["rows"])
+    if c["op"] == "ffn":
+        return moe.moe_mx_expert_ffn(st["x"], st["slot_off"], st["slot_expert"], st["n_slots"], st["w_gate"],
+                                     st["w_up"], st["w_down"], act=c["act"], x_format=c["fmt"],
+                                     row_src=st["perm_src"])
+    d_y, d_w = moe.moe_combine_backward(st["d_out"], st["y_kept"], st["inv_pos"], st["topk_w"])
+    return {"d_y": d_y, "d_topk_w": d_w}
+
+
+def run(state):
+    if own:
+        return _library(state)
+    plain = {"keep": _keep_plain, "ffn": _ffn_plain, "combine_backward": _combine_backward_plain}
+    return plain[state["case"]["op"]](state)
+
+
+def work(case):
+    """Every input read once, every output written once (kept values written and read); the formulas' operations."""
+    op, s = case["op"], {"f32": 4, "bf16": 2}[case["dtype"]]
+    if op == "keep":
+        n, bits = case["R"] * case["K"], {"fp4": 4.25, "fp8": 8.25}[case["fmt"]]
+        back = max(1, case["rows"])
+        return {"bytes": n * s * (1 + back) + 2 * n * bits / 8, "flops": n * (2 + back)}
+    if op == "ffn":
+        T, H, I, E, k = (case[key] for key in "T H I E k".split())
+        mats = 3 if case["act"] == "swiglu" else 2
+        return {"bytes": min(E, T * k) * mats * H * I * 4.25 / 8 + T * H * s + T * k * H * s,
+                "flops": 2 * T * k * H * I * mats}
+    T, k, H = case["T"], case["k"], case["H"]
+    return {"bytes": T * H * s + T * k * H * (s + 8.25 / 8) + T * k * 12, "flops": 3 * T * k * H}
+
+
+# ----------------------------------------------------------------------- the definitions in float64
+def _grid(fmt, dev):
+    """Every value of the format that is not negative, ascending."""
+    if fmt == "fp4":
+        return torch.tensor(E2M1, dtype=torch.float64, device=dev)
+    return torch.arange(127, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn).double()
+
+
+def _nearest(x, fmt):
+    """What the rows of x (float64) stand for once quantised: the smallest scale with which the largest magnitude
+    of a block is at most, or rounds to, the format's largest value; then the nearest value, the even code of two."""
+    K = x.shape[-1]
+    v = torch.nn.functional.pad(x, (0, -K % BLOCK)).unflatten(-1, (-1, BLOCK))
+    grid = _grid(fmt, x.device)
+    past = {"fp4": 7.0, "fp8": 464.0}[fmt]   # half-way past the largest value: to it only from 464 (an even code)
+    top = v.abs().amax(-1, keepdim=True)
+    scale = torch.exp2(torch.ceil(torch.log2(top.clamp(min=2.0 ** -140) / past)))
+    over = top / scale >= past if fmt == "fp4" else top / scale > past
+    scale = torch.where(over, 2 * scale, scale)
+    below = top / (scale / 2) < past if fmt == "fp4" else top / (scale / 2) <= past
+    scale = torch.where(below, scale / 2, scale).clamp(2.0 ** -127, 2.0 ** 127)
+    a = (v / scale).abs().clamp(max=float(grid[-1]))
+    high = torch.searchsorted(grid, a.contiguous()).clamp(max=len(grid) - 1)
+    low = (high - 1).clamp(min=0)
+    up, down = grid[high] - a, a - grid[low]
+    code = torch.where((up < down) | ((up == down) & (high % 2 == 0)), high, low)
+    return (torch.sign(v) * grid[code] * scale).flatten(-2)[..., :K]
+
+
+def _exact_keep(st):
+    out = torch.cat([_nearest(part.double(), st["case"]["fmt"]) for part in st["x"].split(4096)])
+    return out if st["rows"] is None else out[st["rows"].long()]
+
+
+def _exact_ffn(st):
+    """One expert after the other."""
+    fmt, off = st["case"]["fmt"], st["slot_off"].tolist()
+    y = torch.empty((st["perm_src"].numel(), st["x"].shape[1]), dtype=torch.float64, device=st["x"].device)
+    for e, (lo, hi) in enumerate(zip(off, off[1:])):
+        if lo == hi:
+            continue
+        wide = {key: None if st[key] is None else _decode(st[key][0][e], st[key][1][e], "fp4", torch.float64)
+                for key in ("w_gate", "w_up", "w_down")}
+        for a in range(lo, hi, 1024):
+            b = min(hi, a + 1024)
+            x = _nearest(st["x"][st["perm_src"][a:b].long()].double(), fmt)
+            g = x @ wide["w_gate"].T
+            h = g * torch.special.ndtr(g) if wide["w_up"] is None else g * torch.sigmoid(g) * (x @ wide["w_up"].T)
+            y[a:b] = _nearest(h, fmt) @ wide["w_down"].T
+    return y
+
+
+def _exact_combine_backward(st):
+    """Token slot by token slot."""
+    (codes, byte), H = st["y_kept"], st["d_out"].shape[1]
+    T, k = st["inv_pos"].shape
+    d_out, step = st["d_out"].double(), torch.exp2(byte.double() - 127.0)
+    d_w = torch.empty((T, k), dtype=torch.float64, device=d_out.device)
+    d_y = torch.empty((T * k, H), dtype=torch.float64, device=d_out.device)
+    for i in range(k):
+        row = st["inv_pos"][:, i].long()
+        scale = step[row].repeat_interleave(BLOCK, 1)[:, :H]
+        d_w[:, i] = (codes[row].view(torch.float8_e4m3fn).double() * scale * d_out).sum(1)
+        d_y[row] = d_out * st["topk_w"][:, i:i + 1].double()
+    return {"d_y": d_y, "d_topk_w": d_w}
+
+
+def exact(case, seed):
+    st = prepare(case, seed)
+    forms = {"keep": _exact_keep, "ffn": _exact_ffn, "combine_backward": _exact_combine_backward}
+    return forms[case["op"]](st)
