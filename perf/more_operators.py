@@ -3,14 +3,14 @@
     keep              rows quantised to blocks of 32 values with one power-of-two scale each, and the values
                       they stand for back again: activations kept for the backward pass (8 bits; restored
                       expert by expert, one row for each token and slot), weights made ready to be served (4 bits)
-    ffn               the experts' FFN on 4-bit weights; activations quantised to 8 or 4 bits by row blocks
+    ffn               the experts' FFN on 4-bit weights; activations quantised to 6 or 4 bits by row blocks
     combine_backward  the gradient of the weighted gather back to token order, from expert outputs kept in 8 bits
 
 A case is a dict of plain values; prepare() draws its inputs on the GPU, run() makes one pass (plain torch,
 or the library's calls where `own` is set) and exact() evaluates the definition in float64.
 
-The format: 32 consecutive values of a row share the scale 2^(b - 127), b one byte; the values are e2m1 (two a
-byte, the first in the low half) or e4m3, rounded to nearest even.  The scale is the smallest for which the
+The format: 32 consecutive values of a row share the scale 2^(b - 127), b one byte; the values are e2m1 (4 bits, two
+a byte, the first in the low half), e2m3 (6 bits) or e4m3 (8 bits), rounded to nearest even.  The scale is the smallest for which the
 block's largest magnitude still rounds to the format's largest value or less.
 """
 import math
@@ -22,9 +22,12 @@ own = False
 DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
 BLOCK = 32
 # exponent of the format's largest value; what, added to a float's bits, carries into the exponent just
-# where the mantissa would round past the largest value (1.75 and up of e2m1, above 1.8125 of e4m3)
-EMAX = {"fp4": 2, "fp8": 8}
-CARRY = {"fp4": 0x200000, "fp8": 0x17FFFF}
+# where the mantissa would round past the largest value (1.75 and up of e2m1, 1.9375 and up of e2m3,
+# above 1.8125 of e4m3)
+EMAX = {"fp4": 2, "fp6": 2, "fp8": 8}
+CARRY = {"fp4": 0x200000, "fp6": 0x80000, "fp8": 0x17FFFF}
+# half a step past the largest value: itself already too far where the largest has an odd code (e2m1, e2m3)
+PAST = {"fp4": 7.0, "fp6": 7.75, "fp8": 464.0}
 E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 
 
@@ -38,15 +41,15 @@ def listed():
         # the weights of one expert matrix after the other, made ready for serving; float32 masters of an odd width
         dict(name="keep_weights", op="keep", R=28671, K=4095, fmt="fp4", dtype="f32", rows=0),
         # one decoded token at 6 of 160 experts
-        dict(name="ffn_token", op="ffn", T=1, H=5120, I=1536, E=160, k=6, act="swiglu", fmt="fp8", dtype="bf16"),
+        dict(name="ffn_token", op="ffn", T=1, H=5120, I=1536, E=160, k=6, act="swiglu", fmt="fp6", dtype="bf16"),
         # a batch of sequences being decoded: most experts get a few rows, some none
-        dict(name="ffn_decode", op="ffn", T=61, H=5120, I=1536, E=160, k=6, act="swiglu", fmt="fp8", dtype="bf16"),
+        dict(name="ffn_decode", op="ffn", T=61, H=5120, I=1536, E=160, k=6, act="swiglu", fmt="fp6", dtype="bf16"),
         # a prompt at the same experts, activations in 4 bits
         dict(name="ffn_prompt", op="ffn", T=1021, H=5120, I=1536, E=160, k=6, act="swiglu", fmt="fp4", dtype="bf16"),
         # GELU experts of hidden size 1024
-        dict(name="ffn_gelu", op="ffn", T=4001, H=1024, I=4096, E=32, k=2, act="gelu", fmt="fp8", dtype="bf16"),
-        # the largest batch of long prompts at 8 experts, in 8 and in 4 bits
-        dict(name="ffn_batch", op="ffn", T=8192, H=4096, I=14336, E=8, k=2, act="swiglu", fmt="fp8", dtype="bf16"),
+        dict(name="ffn_gelu", op="ffn", T=4001, H=1024, I=4096, E=32, k=2, act="gelu", fmt="fp6", dtype="bf16"),
+        # the largest batch of long prompts at 8 experts, in 6 and in 4 bits
+        dict(name="ffn_batch", op="ffn", T=8192, H=4096, I=14336, E=8, k=2, act="swiglu", fmt="fp6", dtype="bf16"),
         dict(name="ffn_batch_fp4", op="ffn", T=8192, H=4096, I=14336, E=8, k=2, act="swiglu", fmt="fp4", dtype="bf16"),
         # a small step's gradient, float32 rows
         dict(name="combine_bwd_few", op="combine_backward", T=61, k=2, H=1024, dtype="f32"),
@@ -77,7 +80,7 @@ def draw(rng):
     k = min(k, E)
     T = _spread(rng, 1, max(1, min(16384, int(2.5e11 / (H * I * k)))))
     return dict(op=op, T=T, H=H, I=I, E=E, k=k, act=rng.choice(["swiglu", "swiglu", "gelu"]),
-                fmt=rng.choice(["fp8", "fp4"]), dtype="bf16")
+                fmt=rng.choice(["fp6", "fp4"]), dtype="bf16")
 
 
 # ------------------------------------------------------------------- the format, in elementary operations
@@ -90,9 +93,9 @@ def _scale_bytes(v, fmt):
 
 def _round_to(a, fmt):
     """a (float64, at most the format's largest after rounding) to the format's nearest value, ties to even."""
-    if fmt == "fp4":
-        m = a.abs()
-        step = torch.where(m < 2, 0.5, torch.where(m < 4, 1.0, 2.0)).to(a.dtype)
+    if fmt != "fp8":
+        m, first = a.abs(), {"fp4": 0.5, "fp6": 0.125}[fmt]
+        step = torch.where(m < 2, first, torch.where(m < 4, 2 * first, 4 * first)).to(a.dtype)
     else:
         step = torch.exp2((torch.frexp(a).exponent - 1).clamp(min=-6).to(a.dtype) - 3)
     return torch.round(a / step) * step
@@ -288,6 +291,9 @@ def _grid(fmt, dev):
     """Every value of the format that is not negative, ascending."""
     if fmt == "fp4":
         return torch.tensor(E2M1, dtype=torch.float64, device=dev)
+    if fmt == "fp6":
+        return torch.tensor([(8 * (c > 7) + c % 8) * 2.0 ** (max(c // 8, 1) - 4) for c in range(32)],
+                            dtype=torch.float64, device=dev)
     return torch.arange(127, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn).double()
 
 
@@ -297,12 +303,12 @@ def _nearest(x, fmt):
     K = x.shape[-1]
     v = torch.nn.functional.pad(x, (0, -K % BLOCK)).unflatten(-1, (-1, BLOCK))
     grid = _grid(fmt, x.device)
-    past = {"fp4": 7.0, "fp8": 464.0}[fmt]   # half-way past the largest value: to it only from 464 (an even code)
+    past = PAST[fmt]
     top = v.abs().amax(-1, keepdim=True)
     scale = torch.exp2(torch.ceil(torch.log2(top.clamp(min=2.0 ** -140) / past)))
-    over = top / scale >= past if fmt == "fp4" else top / scale > past
+    over = top / scale > past if fmt == "fp8" else top / scale >= past
     scale = torch.where(over, 2 * scale, scale)
-    below = top / (scale / 2) < past if fmt == "fp4" else top / (scale / 2) <= past
+    below = top / (scale / 2) <= past if fmt == "fp8" else top / (scale / 2) < past
     scale = torch.where(below, scale / 2, scale).clamp(2.0 ** -127, 2.0 ** 127)
     a = (v / scale).abs().clamp(max=float(grid[-1]))
     high = torch.searchsorted(grid, a.contiguous()).clamp(max=len(grid) - 1)
