@@ -74,14 +74,17 @@ enum {
     MOE_CHECK_DUPLICATE = 4,  /* moe_stats, moe_dispatch: one token names the same expert twice */
     MOE_CHECK_COUNTS = 8,     /* moe_dispatch: `counts` differs from the counts of topk_idx */
     MOE_CHECK_REPLICAS = 16,  /* moe_dispatch: a negative replica count, or copies beyond max_slots */
-    MOE_CHECK_SLOTS = 32,     /* moe_expert_ffn: slot table not ascending inside [0, M], n_slots
+    MOE_CHECK_SLOTS = 32,     /* moe_expert_ffn, moe_mx_expert_ffn: slot table not ascending inside [0, M], n_slots
                                  outside [0, max_slots], or an expert outside [0, E) */
-    MOE_CHECK_ROWS = 64,      /* moe_combine: an inv_pos entry outside [0, M) */
-    MOE_CHECK_GRADS = 128     /* moe_grad_norm, moe_clip_grads: the norm is infinite or NaN */
+    MOE_CHECK_ROWS = 64,      /* moe_combine, moe_combine_backward: an inv_pos entry outside [0, M);
+                                 moe_mx_dequantize: a row outside [0, R) */
+    MOE_CHECK_GRADS = 128,    /* moe_grad_norm, moe_clip_grads: the norm is infinite or NaN */
+    MOE_CHECK_BLOCKS = 256    /* moe_mx_quantize, moe_mx_expert_ffn (x): a block with a NaN or an infinity */
 };
 
 typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;       /* activations and weights */
 typedef enum { MOE_SWIGLU = 0, MOE_GELU = 1 } moe_act;
+typedef enum { MOE_MX_FP4 = 0, MOE_MX_FP8 = 1, MOE_MX_FP6 = 2 } moe_mx_format; /* e2m1, e4m3, e2m3 in blocks of 32 */
 typedef enum { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 } moe_score;        /* moe_gate: an expert's score of its logit */
 typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
 typedef enum { MOE_GEMM_AUTO = 0, MOE_GEMM_GROUPED = 1, MOE_GEMM_DENSE = 2, MOE_GEMM_GROUPED_SMALL = 3 } moe_gemm_path;
@@ -433,6 +436,82 @@ int moe_expert_ffn_profiled(const void* x_perm, const int32_t* row_src, int64_t 
  */
 int moe_combine(const void* y_perm, moe_dtype dt, int64_t M, const int32_t* inv_pos, const float* topk_w,
                 int64_t T, int k, int H, void* out, int32_t* check, void* stream);
+
+/*
+ * moe_combine_backward -- the gradient of moe_combine, from d_out [T, H] in `dt`:
+ *   d_y[inv_pos[t, i]] = topk_w[t, i] * d_out[t]   ([M, H] in `dt`, rounded once)
+ *   d_topk_w[t, i] = <d_out[t], y[inv_pos[t, i]]>  (fp32 [T, k], summed in fp32 in
+ *                    an order that only T and H decide)
+ *   y        the expert outputs [M, H] in `dt` (y_scale NULL), or as moe_mx_quantize
+ *            keeps them in MOE_MX_FP8: codes [M, H] and y_scale [M, ceil(H / 32)].
+ * inv_pos entries outside [0, M) get d_topk_w 0 and write no row (MOE_CHECK_ROWS);
+ * rows that no entry names are left as they are, and a row that two entries name
+ * holds either's.  d_y may not be y or d_out.
+ * Limits: 1 <= k <= 8, H a multiple of 8, T*k < 2^31; d_out, y and d_y 16-byte
+ * aligned.  The dispatch's own gradient, d_x[t] = sum_i d_x_perm[inv_pos[t, i]],
+ * is moe_combine with unit weights.
+ */
+int moe_combine_backward(const void* d_out, moe_dtype dt, const void* y, const uint8_t* y_scale, int64_t M,
+                         const int32_t* inv_pos, const float* topk_w, int64_t T, int k, int H, void* d_y,
+                         float* d_topk_w, int32_t* check, void* stream);
+
+/* ------------------------------------------------------- microscaled blocks
+ * Rows in blocks of 32 values with one scale each, for weights that are served in
+ * 4 bits and activations that a training step keeps in 8.  A row of K values is
+ * ceil(K / 32) scale bytes b, the scale being 2^(b - 127), and its codes: e2m1
+ * (MOE_MX_FP4: magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6), e2m3 (MOE_MX_FP6: steps of
+ * 1/8 below 2, 1/4 below 4, 1/2 up to 7.5) or e4m3 (MOE_MX_FP8: up to 448), the sign
+ * in the top bit, packed from the low bits of each byte up: ceil(K / 2),
+ * ceil(K * 6 / 8) or K bytes a row (unused bits 0).  A value is its code times its
+ * block's scale.
+ *
+ * moe_mx_quantize -- b is the smallest byte for which the block's largest magnitude
+ * rounds to the format's largest value or less (0 for a block of zeros), codes are
+ * rounded to nearest, ties to even.  A block with a NaN or an infinity gets b = 255
+ * and zero codes, and stands for NaNs (MOE_CHECK_BLOCKS).
+ *   x      [R, K] in `dt`; only the alignment of its elements
+ *   q      [R, bytes of K codes] out;  scale  [R, ceil(K / 32)] out
+ *
+ * moe_mx_dequantize -- out[r] = the values of row rows[r] (rows NULL: n_rows = R,
+ * row r), in `dt`, rounded once (bf16 holds every value of a block whose b is 3 or
+ * more).  rows int32 [n_rows], e.g. moe_dispatch's perm_src: x_perm comes back from
+ * the tokens that were kept.  Entries outside [0, R) give zero rows
+ * (MOE_CHECK_ROWS).
+ * Limits: 1 <= K <= 2^28, at most 2^31 blocks.
+ */
+int moe_mx_quantize(const void* x, moe_dtype dt, int64_t R, int64_t K, moe_mx_format fmt, uint8_t* q, uint8_t* scale,
+                    int32_t* check, void* stream);
+int moe_mx_dequantize(const uint8_t* q, const uint8_t* scale, moe_mx_format fmt, int64_t R, int64_t K,
+                      const int32_t* rows, int64_t n_rows, moe_dtype dt, void* out, int32_t* check, void* stream);
+
+/*
+ * moe_mx_expert_ffn -- moe_expert_ffn on expert weights in 4 bits.  With Q(.) the
+ * values that moe_mx_quantize gives a row's blocks in x_format:
+ *   SwiGLU: h = silu(Q(x) Wg^T) * (Q(x) Wu^T), y = Q(h) Wd^T;  GELU likewise.
+ *   w_gate, w_up, w_down   codes of moe_mx_quantize(..., MOE_MX_FP4): [E, I, H / 2]
+ *            and [E, H, I / 2], with s_gate, s_up [E, I, H / 32], s_down [E, H, I / 32]
+ *   x_format MOE_MX_FP6 (about 2 % noise a value) or MOE_MX_FP4 (about 10 %)
+ *   x, row_src, n_src, the slot table, y_perm   as in moe_expert_ffn; x and y_perm
+ *            in `dt`.  Row_src NULL: n_src is taken as M.
+ * Products are exact on the scaled matrix instructions and summed in fp32; h is formed
+ * in fp32 and quantised from there, y is rounded once.  No host sync.  How rows
+ * are tiled hangs on M / E, and an h next to a rounding's border may fall on its other
+ * side in another tiling.  A row whose x holds a NaN or an infinity is NaN, alone.
+ * Slots are tiled one by one (replicas of one expert are not merged).
+ *   workspace  moe_mx_expert_ffn_workspace_bytes(n_src, M, ...) bytes (n_src = M
+ *            without row_src), rewritten by every call: two calls in flight need two.
+ * Limits: H and I multiples of 128; 1 <= E <= max_slots; H*I/2, 128 times the larger
+ * of H and I, n_src*H/32, M*I/32 and with row_src n_src*H/2 below 0x7e000000.
+ * All tensors 16-byte aligned.
+ * check: MOE_CHECK_SLOTS, MOE_CHECK_BLOCKS (in x).
+ */
+size_t moe_mx_expert_ffn_workspace_bytes(int64_t n_src, int64_t M, int H, int I, int max_slots,
+                                         moe_mx_format x_format); /* [host] */
+int moe_mx_expert_ffn(const void* x, const int32_t* row_src, int64_t n_src, moe_dtype dt, int64_t M, int H, int I,
+                      int E, const int32_t* slot_off, const int32_t* slot_expert, const int32_t* n_slots, int max_slots,
+                      const uint8_t* w_gate, const uint8_t* s_gate, const uint8_t* w_up, const uint8_t* s_up,
+                      const uint8_t* w_down, const uint8_t* s_down, moe_act act, moe_mx_format x_format, void* y_perm,
+                      void* workspace, size_t workspace_bytes, int32_t* check, void* stream);
 
 /* ----------------------------------------------------------- device check
  * moe_check_device_error -- waits for `stream`, then reads the device-check

@@ -51,21 +51,27 @@ __all__ = ["moe_route", "moe_stats_state_bytes", "moe_stats_init", "moe_stats", 
            "moe_gate", "moe_gate_backward", "moe_backward_gated", "moe_layer_norm",
            "moe_layer_norm_backward_workspace_bytes", "moe_layer_norm_backward", "moe_grad_norm_workspace_bytes",
            "moe_grad_norm", "moe_clip_grads", "moe_layer_backward",
+           "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_expert_ffn_workspace_bytes", "moe_mx_expert_ffn",
+           "moe_combine_backward",
            "moe_expert_ffn_profiled", "new_check_word", "CHECK_BITS", "moe_dispatch_noalloc",
            "MoEError", "LIB_PATH", "MOE_F32", "MOE_BF16", "SWIGLU", "GELU", "SOFTMAX", "SIGMOID", "GROUP_MAX",
-           "GROUP_TOP2", "GEMM_AUTO", "GEMM_GROUPED", "GEMM_DENSE", "GEMM_GROUPED_SMALL"]
+           "GROUP_TOP2", "GEMM_AUTO", "GEMM_GROUPED", "GEMM_DENSE", "GEMM_GROUPED_SMALL",
+           "MX_FP4", "MX_FP8", "MX_FP6"]
 
 MOE_F32, MOE_BF16 = 0, 1
 SWIGLU, GELU = 0, 1
 SOFTMAX, SIGMOID = 0, 1
 GROUP_MAX, GROUP_TOP2 = 0, 1
 GEMM_AUTO, GEMM_GROUPED, GEMM_DENSE, GEMM_GROUPED_SMALL = 0, 1, 2, 3
+MX_FP4, MX_FP8, MX_FP6 = 0, 1, 2
+_MX_FORMAT = {"fp4": MX_FP4, "fp8": MX_FP8, "fp6": MX_FP6, MX_FP4: MX_FP4, MX_FP8: MX_FP8, MX_FP6: MX_FP6}
+_DTYPE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 _SCORE = {"softmax": SOFTMAX, "sigmoid": SIGMOID, SOFTMAX: SOFTMAX, SIGMOID: SIGMOID}
 _GROUP_SCORE = {"max": GROUP_MAX, "top2": GROUP_TOP2, GROUP_MAX: GROUP_MAX, GROUP_TOP2: GROUP_TOP2}
 _ACT = {"swiglu": SWIGLU, "gelu": GELU, SWIGLU: SWIGLU, GELU: GELU}
 # bits of the device-check word (include/moe.h MOE_CHECK_*)
 CHECK_BITS = {"logits": 1, "index": 2, "duplicate": 4, "counts": 8, "replicas": 16, "slots": 32, "rows": 64,
-              "grads": 128}
+              "grads": 128, "blocks": 256}
 _PATH = {"auto": GEMM_AUTO, "grouped": GEMM_GROUPED, "dense": GEMM_DENSE, "grouped_small": GEMM_GROUPED_SMALL,
          GEMM_AUTO: GEMM_AUTO, GEMM_GROUPED: GEMM_GROUPED, GEMM_DENSE: GEMM_DENSE,
          GEMM_GROUPED_SMALL: GEMM_GROUPED_SMALL}
@@ -422,6 +428,55 @@ def moe_combine(y_perm: torch.Tensor, inv_pos: torch.Tensor, topk_w: torch.Tenso
     _call("moe_combine", _ptr(y_perm), _dtype_code(y_perm), ctypes.c_int64(M), _ptr(inv_pos), _ptr(topk_w),
           ctypes.c_int64(T), k, H, _ptr(out), _ptr(check), _stream(stream))
     return out
+
+
+def moe_combine_backward(d_out: torch.Tensor, y_perm, inv_pos: torch.Tensor, topk_w: torch.Tensor, d_y=None,
+                         d_topk_w=None, stream=None, check=None):
+    """(d_y [M, H], d_topk_w [T, k]): the gradient of moe_combine.  y_perm: the expert
+    outputs, or the pair (q, scale) that moe_mx_quantize(y_perm, "fp8") kept of them.
+    Rows that no entry of inv_pos names are left as they are (undefined in a d_y
+    allocated here)."""
+    y, y_scale = y_perm if isinstance(y_perm, (tuple, list)) else (y_perm, None)
+    r = binding().combine_backward(d_out, y, y_scale, inv_pos, topk_w, d_y, d_topk_w, stream, check)
+    return r if type(r) is tuple else _failed("moe_combine_backward", r)
+
+
+# -------------------------------------------------------- microscaled blocks
+def moe_mx_quantize(x: torch.Tensor, format="fp4", q=None, scale=None, stream=None, check=None):
+    """(q, scale): the rows of x [..., K] (float32 or bfloat16) in blocks of 32 values
+    with one power-of-two scale each (include/moe.h moe_mx_quantize).  format "fp4"
+    (e2m1, q uint8 [..., ceil(K / 2)]), "fp6" (e2m3, [..., ceil(K * 6 / 8)]) or "fp8"
+    (e4m3, [..., K], which .view(torch.float8_e4m3fn) reads); scale uint8
+    [..., ceil(K / 32)] (e8m0)."""
+    r = binding().mx_quantize(x, _MX_FORMAT[format], q, scale, stream, check)
+    return r if type(r) is tuple else _failed("moe_mx_quantize", r)
+
+
+def moe_mx_dequantize(q: torch.Tensor, scale: torch.Tensor, format="fp4", dtype=torch.bfloat16, cols=None, rows=None,
+                      out=None, stream=None, check=None):
+    """The values that moe_mx_quantize's (q, scale) stand for, [..., K] in float32 or
+    bfloat16; cols: K, where the codes' bytes hold more (odd rows in "fp4").  rows (int32 [n], e.g.
+    moe_dispatch's perm_src): [n, K], row r of the result being row rows[r]."""
+    if dtype not in _DTYPE:
+        raise TypeError(f"values come back in float32 or bfloat16, not {dtype}")
+    r = binding().mx_dequantize(q, scale, _MX_FORMAT[format], _DTYPE[dtype], cols, rows, out, stream, check)
+    return r if type(r) is not int else _failed("moe_mx_dequantize", r)
+
+
+def moe_mx_expert_ffn_workspace_bytes(n_src: int, M: int, H: int, I: int, max_slots: int, x_format="fp6") -> int:
+    """n_src: the rows of x (M where the call has no row_src)."""
+    return int(lib().moe_mx_expert_ffn_workspace_bytes(n_src, M, H, I, max_slots, _MX_FORMAT[x_format]))
+
+
+def moe_mx_expert_ffn(x: torch.Tensor, slot_off, slot_expert, n_slots, w_gate, w_up, w_down, act="swiglu",
+                      x_format="fp6", y_perm=None, workspace=None, stream=None, check=None, row_src=None):
+    """moe_expert_ffn on 4-bit weights: w_gate, w_up (None for GELU) and w_down are the
+    pairs (q, scale) that moe_mx_quantize(w, "fp4") gives.  x_format: the blocks that
+    x and h are quantised to, "fp6" or "fp4".  row_src as in moe_expert_ffn."""
+    gate, up, down = (w_gate, w_up if w_up is not None else (None, None), w_down)
+    r = binding().mx_expert_ffn(x, slot_off, slot_expert, n_slots, gate[0], gate[1], up[0], up[1], down[0], down[1],
+                                _ACT[act], _MX_FORMAT[x_format], y_perm, workspace, stream, check, row_src)
+    return r if type(r) is not int else _failed("moe_mx_expert_ffn", r)
 
 
 # ----------------------------------------------------------------- backward

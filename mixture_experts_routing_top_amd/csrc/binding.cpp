@@ -1,5 +1,5 @@
-// The binding of the gate, layer norm and clipping calls: argument checks, output
-// allocation and the C call in one native function each.
+// The binding of the gate, layer norm, clipping and microscaled-block calls: argument
+// checks, output allocation and the C call in one native function each.
 //
 // These operators take a few microseconds on the GPU for a small batch, less than
 // an interpreter needs to check a call's arguments and allocate its outputs one
@@ -359,9 +359,189 @@ PyObject* clip_grads(PyObject*, Args a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+int64_t blocks_of(int64_t K) { return (K + 31) / 32; }
+
+moe_mx_format format_code(PyObject* o) { return static_cast<moe_mx_format>(small(o)); }
+
+// bits of a code, and the bytes of a row of K
+int64_t code_bits(moe_mx_format fmt) { return fmt == MOE_MX_FP8 ? 8 : fmt == MOE_MX_FP6 ? 6 : 4; }
+int64_t code_bytes(moe_mx_format fmt, int64_t K) { return (K * code_bits(fmt) + 7) / 8; }
+
+// x, format, q, scale, stream, check
+PyObject* mx_quantize(PyObject*, Args a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 6);
+  const at::Tensor& x = tensor(a[0]);
+  const moe_dtype dt = dtype_code(x);
+  on_gpu(x);
+  TORCH_CHECK_VALUE(x.dim() >= 1, "rows of at least one dimension are quantised");
+  const at::Device dev = x.device();
+  const moe_mx_format fmt = format_code(a[1]);
+  const int64_t K = x.size(-1);
+  TORCH_CHECK_VALUE(K >= 1, "rows of no values have no blocks");
+  const int64_t R = x.numel() / K;
+  std::vector<int64_t> shape = x.sizes().vec(), blocks = shape;
+  shape.back() = code_bytes(fmt, K);
+  blocks.back() = blocks_of(K);
+  const Stream s = stream_of(a[4], dev);
+  const at::Tensor q = output(a[2], shape, at::kByte, dev, "q");
+  const at::Tensor scale = output(a[3], blocks, at::kByte, dev, "scale");
+  int32_t* check = check_word(a[5], dev);
+  const int rc = without_gil(dev, [&] {
+    return moe_mx_quantize(x.data_ptr(), dt, R, K, fmt, q.data_ptr<uint8_t>(), scale.data_ptr<uint8_t>(), check, s.raw);
+  });
+  if (rc != MOE_OK) return PyLong_FromLong(rc);
+  return pair(wrap(q), wrap(scale));
+  END_HANDLE_TH_ERRORS
+}
+
+// q, scale, format, dtype (0 float32, 1 bfloat16), cols (None: the codes' own), rows, out, stream, check
+PyObject* mx_dequantize(PyObject*, Args a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 9);
+  const at::Tensor& q = tensor(a[0]);
+  on_gpu(q);
+  const at::Device dev = q.device();
+  const moe_mx_format fmt = format_code(a[2]);
+  TORCH_CHECK_VALUE(q.dim() >= 1 && q.scalar_type() == at::kByte, "q: expected uint8 codes");
+  const int64_t bytes = q.size(-1);
+  const int64_t K = a[4] == Py_None ? bytes * 8 / code_bits(fmt) : whole(a[4]);
+  TORCH_CHECK_VALUE(K >= 1 && code_bytes(fmt, K) == bytes, "q: rows of ", bytes, " bytes do not hold ", K, " values");
+  const int64_t R = q.numel() / bytes;
+  std::vector<int64_t> shape = q.sizes().vec(), blocks = shape;
+  blocks.back() = blocks_of(K);
+  const at::Tensor& scale = tensor(a[1]);
+  expect(scale, blocks, at::kByte, dev, "scale");
+  shape.back() = K;
+  const int32_t* rows = nullptr;
+  int64_t n_rows = R;
+  if (a[5] != Py_None) {
+    const at::Tensor& r = tensor(a[5]);
+    TORCH_CHECK_VALUE(r.dim() == 1, "rows must be int32 [n]");
+    n_rows = r.size(0);
+    rows = static_cast<const int32_t*>(given(a[5], {n_rows}, at::kInt, dev, "rows"));
+    shape = {n_rows, K};
+  }
+  const int code = small(a[3]);
+  const Stream s = stream_of(a[7], dev);
+  const at::Tensor out = output(a[6], shape, code == MOE_BF16 ? at::kBFloat16 : at::kFloat, dev, "out");
+  int32_t* check = check_word(a[8], dev);
+  if (n_rows == 0) return wrap(out);   // (an empty row map may have no address)
+  const int rc = without_gil(dev, [&] {
+    return moe_mx_dequantize(q.data_ptr<uint8_t>(), scale.data_ptr<uint8_t>(), fmt, R, K, rows, n_rows,
+                             static_cast<moe_dtype>(code), out.data_ptr(), check, s.raw);
+  });
+  return rc != MOE_OK ? PyLong_FromLong(rc) : wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+// d_out, y, y_scale (None: y in the dtype), inv_pos, topk_w, d_y, d_topk_w, stream, check
+PyObject* combine_backward(PyObject*, Args a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 9);
+  const at::Tensor& d_out = tensor(a[0]);
+  const moe_dtype dt = dtype_code(d_out);
+  on_gpu(d_out);
+  const at::Device dev = d_out.device();
+  TORCH_CHECK_VALUE(d_out.dim() == 2, "d_out must be [T, H]");
+  const at::Tensor& y = tensor(a[1]);
+  TORCH_CHECK_VALUE(y.dim() == 2, "y_perm must be [M, H]");
+  const int64_t T = d_out.size(0), H = d_out.size(1), M = y.size(0);
+  TORCH_CHECK_VALUE(H <= INT32_MAX, "H out of range");
+  const bool kept = a[2] != Py_None;
+  expect(y, {M, H}, kept ? at::kByte : d_out.scalar_type(), dev, "y_perm");
+  const void* y_scale = given(a[2], {M, blocks_of(H)}, at::kByte, dev, "y_perm's scale");
+  const at::Tensor& w = tensor(a[4]);
+  TORCH_CHECK_VALUE(w.dim() == 2, "topk_w must be [T, k]");
+  const int64_t k = w.size(1);
+  TORCH_CHECK_VALUE(k <= INT32_MAX, "k out of range");
+  expect(w, {T, k}, at::kFloat, dev, "topk_w");
+  const at::Tensor& inv = tensor(a[3]);
+  expect(inv, {T, k}, at::kInt, dev, "inv_pos");
+  const Stream s = stream_of(a[7], dev);
+  const at::Tensor d_y = output(a[5], {M, H}, d_out.scalar_type(), dev, "d_y");
+  const at::Tensor d_w = output(a[6], {T, k}, at::kFloat, dev, "d_topk_w");
+  int32_t* check = check_word(a[8], dev);
+  // an empty scale has no address, and no row to read either
+  const uint8_t none_kept = 0;
+  const auto* scales = kept && M == 0 ? &none_kept : static_cast<const uint8_t*>(y_scale);
+  const int rc = without_gil(dev, [&] {
+    return moe_combine_backward(d_out.data_ptr(), dt, y.data_ptr(), scales, M, inv.data_ptr<int32_t>(),
+                                w.data_ptr<float>(), T, static_cast<int>(k), static_cast<int>(H), d_y.data_ptr(),
+                                d_w.data_ptr<float>(), check, s.raw);
+  });
+  if (rc != MOE_OK) return PyLong_FromLong(rc);
+  return pair(wrap(d_y), wrap(d_w));
+  END_HANDLE_TH_ERRORS
+}
+
+struct Weights {
+  const uint8_t *codes, *scale;
+};
+
+// one of an FFN's matrices: codes [E, N, K / 2] and scale [E, N, K / 32]
+Weights mx_weights(PyObject* codes, PyObject* scale, int64_t E, int64_t N, int64_t K, const at::Device& dev,
+                   const char* name) {
+  return {static_cast<const uint8_t*>(given(codes, {E, N, K / 2}, at::kByte, dev, name)),
+          static_cast<const uint8_t*>(given(scale, {E, N, K / 32}, at::kByte, dev, name))};
+}
+
+// x, slot_off, slot_expert, n_slots, gate codes, gate scale, up codes, up scale, down codes, down scale, act, x_format,
+// y_perm, workspace, stream, check, row_src
+PyObject* mx_expert_ffn(PyObject*, Args a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 17);
+  const at::Tensor& x = tensor(a[0]);
+  const moe_dtype dt = dtype_code(x);
+  on_gpu(x);
+  const at::Device dev = x.device();
+  TORCH_CHECK_VALUE(x.dim() == 2, "x must be [rows, H]");
+  const int64_t n_src = x.size(0), H = x.size(1);
+  int64_t M = n_src;
+  const int32_t* row_src = nullptr;
+  if (a[16] != Py_None) {
+    const at::Tensor& r = tensor(a[16]);
+    TORCH_CHECK_VALUE(r.dim() == 1, "row_src must be int32 [M]");
+    M = r.size(0);
+    row_src = static_cast<const int32_t*>(given(a[16], {M}, at::kInt, dev, "row_src"));
+  }
+  const at::Tensor& gate = tensor(a[4]);
+  TORCH_CHECK_VALUE(gate.dim() == 3, "w_gate: expected codes [E, I, H / 2]");
+  const int64_t E = gate.size(0), I = gate.size(1);
+  TORCH_CHECK_VALUE(H <= INT32_MAX && I <= INT32_MAX && E <= INT32_MAX, "H, I or E out of range");
+  const Weights wg = mx_weights(a[4], a[5], E, I, H, dev, "w_gate"), wu = mx_weights(a[6], a[7], E, I, H, dev, "w_up"),
+                wd = mx_weights(a[8], a[9], E, H, I, dev, "w_down");
+  const at::Tensor& slots = tensor(a[2]);
+  const int64_t max_slots = slots.numel();
+  TORCH_CHECK_VALUE(max_slots < INT32_MAX, "too many slots");
+  expect(slots, {max_slots}, at::kInt, dev, "slot_expert");
+  const at::Tensor& off = tensor(a[1]);
+  expect(off, {max_slots + 1}, at::kInt, dev, "slot_off");
+  const at::Tensor& n_slots = tensor(a[3]);
+  expect(n_slots, {1}, at::kInt, dev, "n_slots");
+  const int act = small(a[10]);
+  const moe_mx_format fmt = format_code(a[11]);
+  const Stream s = stream_of(a[14], dev);
+  const at::Tensor y = output(a[12], {M, H}, x.scalar_type(), dev, "y_perm");
+  const int h = static_cast<int>(H), i = static_cast<int>(I), ms = static_cast<int>(max_slots);
+  const int64_t sources = row_src ? n_src : M;
+  const at::Tensor ws =
+      workspace_of(a[13], moe_mx_expert_ffn_workspace_bytes(sources, M, h, i, ms, fmt), dev, "FFN workspace");
+  int32_t* check = check_word(a[15], dev);
+  const int rc = without_gil(dev, [&] {
+    return moe_mx_expert_ffn(x.data_ptr(), row_src, n_src, dt, M, h, i, static_cast<int>(E), off.data_ptr<int32_t>(),
+                             slots.data_ptr<int32_t>(), n_slots.data_ptr<int32_t>(), ms, wg.codes, wg.scale, wu.codes,
+                             wu.scale, wd.codes, wd.scale, static_cast<moe_act>(act), fmt, y.data_ptr(), ws.data_ptr(),
+                             ws.nbytes(), check, s.raw);
+  });
+  return rc != MOE_OK ? PyLong_FromLong(rc) : wrap(y);
+  END_HANDLE_TH_ERRORS
+}
+
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(gate), METHOD(gate_backward), METHOD(layer_norm), METHOD(layer_norm_backward),
-                         METHOD(clip_grads), {nullptr, nullptr, 0, nullptr}};
+                         METHOD(clip_grads), METHOD(mx_quantize), METHOD(mx_dequantize), METHOD(combine_backward),
+                         METHOD(mx_expert_ffn), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

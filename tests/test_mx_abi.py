@@ -1,0 +1,110 @@
+"""Refusals of the microscaled-block calls, on the CPU: every one is reported before
+anything reaches the GPU.  Workspace sizes."""
+import ctypes
+
+import pytest
+import torch
+
+import mixture_experts_routing_top_amd as moe
+from mixture_experts_routing_top_amd import _native
+
+N, P, BIG = None, 16, 1 << 40
+
+
+def _ffn(x=P, rows=N, n_src=8, dt=1, M=8, H=128, I=256, E=4, off=P, se=P, ns=P, slots=4, wg=P, sg=P, wu=P, su=P, wd=P,
+         sd=P, act=0, fmt=2, y=P, ws=P, wb=BIG):
+    return ("moe_mx_expert_ffn", (x, rows, n_src, dt, M, H, I, E, off, se, ns, slots, wg, sg, wu, su, wd, sd, act, fmt, y, ws,
+                                  wb, N, N))
+
+
+def _combine(d_out=P, dt=1, y=P, ys=P, M=16, inv=P, w=P, T=8, k=2, H=64, d_y=P, d_w=P):
+    return ("moe_combine_backward", (d_out, dt, y, ys, M, inv, w, T, k, H, d_y, d_w, N, N))
+
+
+@pytest.mark.parametrize("call,status,msg", [
+    (("moe_mx_quantize", (P, 2, 4, 64, 0, P, P, N, N)), -1, "dtype"),
+    (("moe_mx_quantize", (P, 1, 4, 64, 3, P, P, N, N)), -1, "format"),
+    (("moe_mx_quantize", (P, 1, -1, 64, 0, P, P, N, N)), -1, "rows"),
+    (("moe_mx_quantize", (P, 1, 4, 0, 0, P, P, N, N)), -1, "K=0"),
+    (("moe_mx_quantize", (P, 1, 4, 1 << 29, 0, P, P, N, N)), -1, "K="),
+    (("moe_mx_quantize", (P, 1, 1 << 32, 64, 0, P, P, N, N)), -2, "2\\^31 blocks"),
+    (("moe_mx_quantize", (N, 1, 4, 64, 0, P, P, N, N)), -1, "null"),
+    (("moe_mx_quantize", (P, 1, 4, 64, 0, P, N, N, N)), -1, "null"),
+    (("moe_mx_quantize", (N, 1, 0, 64, 0, N, N, N, N)), 0, ""),
+    (("moe_mx_dequantize", (P, P, 5, 4, 64, N, 0, 1, P, N, N)), -1, "format"),
+    (("moe_mx_dequantize", (P, P, 0, 4, 64, N, 0, 7, P, N, N)), -1, "dtype"),
+    (("moe_mx_dequantize", (P, P, 0, 4, 64, P, -3, 1, P, N, N)), -1, "rows"),
+    (("moe_mx_dequantize", (P, P, 0, 4, 64, P, 1 << 33, 1, P, N, N)), -2, "blocks"),
+    (("moe_mx_dequantize", (N, P, 0, 4, 64, N, 0, 1, P, N, N)), -1, "null"),
+    (("moe_mx_dequantize", (P, P, 0, 4, 64, N, 0, 1, N, N, N)), -1, "null"),
+    (("moe_mx_dequantize", (N, N, 0, 4, 64, P, 0, 1, N, N, N)), 0, ""),
+    (_combine(dt=3), -1, "dtype"),
+    (_combine(k=9), -1, "k=9"),
+    (_combine(k=0), -1, "k=0"),
+    (_combine(T=-1), -1, "T or M"),
+    (_combine(T=1 << 30), -1, "T or M"),
+    (_combine(H=60), -1, "multiple of 8"),
+    (_combine(H=0), -1, "multiple of 8"),
+    (_combine(inv=N), -1, "null"),
+    (_combine(d_y=N), -1, "null"),
+    (_combine(y=8), -1, "aligned"),
+    (_combine(d_out=24), -1, "aligned"),
+    (_combine(T=0, d_out=N, y=N, inv=N, w=N, d_y=N, d_w=N), 0, ""),
+    (_ffn(dt=2), -1, "dtype"),
+    (_ffn(act=2), -1, "activation"),
+    (_ffn(fmt=1), -1, "x_format"),
+    (_ffn(M=-1), -1, "M out of range"),
+    (_ffn(M=1 << 31), -1, "M out of range"),
+    (_ffn(rows=P, n_src=-1), -1, "n_src"),
+    (_ffn(H=192), -2, "multiples of 128"),
+    (_ffn(I=64), -2, "multiples of 128"),
+    (_ffn(H=1 << 16, I=1 << 16), -2, "tile offsets"),
+    (_ffn(H=1 << 24, I=128), -2, "tile offsets"),
+    (_ffn(rows=P, n_src=1 << 26), -2, "rows for 32-bit"),
+    (_ffn(M=1 << 29), -2, "rows for 32-bit"),
+    (_ffn(E=0), -1, "E <= max_slots"),
+    (_ffn(E=5), -1, "E <= max_slots"),
+    (_ffn(wu=N), -1, "w_up"),
+    (_ffn(su=N), -1, "w_up"),
+    (_ffn(act=1), -1, "GELU"),
+    (_ffn(sd=N), -1, "null"),
+    (_ffn(off=N), -1, "null"),
+    (_ffn(y=N), -1, "null"),
+    (_ffn(x=N), -1, "null"),
+    (_ffn(wd=24), -1, "aligned"),
+    (_ffn(wb=1000), -3, "workspace"),
+    (_ffn(M=0, x=N, y=N), 0, ""),
+])
+def test_refusals(call, status, msg):
+    import re
+    lib = _native.lib()
+    name, args = call
+    assert getattr(lib, name)(*args) == status, lib.moe_last_error()
+    if status:
+        assert re.search(msg, lib.moe_last_error().decode()), lib.moe_last_error()
+
+
+@pytest.mark.parametrize("n_src,M,H,I,slots", [(0, 0, 128, 128, 1), (1, 6, 5120, 1536, 160), (1024, 2048, 256, 384, 12)])
+def test_workspace_holds_what_the_call_keeps(n_src, M, H, I, slots):
+    for fmt, bits in (("fp4", 4), ("fp6", 6)):
+        held = (n_src * H + M * I) * bits // 8 + (n_src * H + M * I) // 32 + 16 * min(M, slots) + 4
+        got = moe.moe_mx_expert_ffn_workspace_bytes(n_src, M, H, I, slots, fmt)
+        assert held <= got <= held + 16 * (M // 16) + 8 * 256
+    assert _native.lib().moe_mx_expert_ffn_workspace_bytes(8, -1, 128, 128, 1, 0) == 0
+    assert _native.lib().moe_mx_expert_ffn_workspace_bytes(8, 8, 128, 128, 1, 1) == 0
+
+
+def test_the_binding_checks_its_arguments():
+    x = torch.zeros((4, 64))
+    for call in (lambda: moe.moe_mx_quantize(x), lambda: moe.moe_mx_dequantize(x.byte(), x.byte()),
+                 lambda: moe.moe_combine_backward(x, x, x.int(), x)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+    with pytest.raises(TypeError):
+        moe.moe_mx_quantize(x.half())
+    with pytest.raises(TypeError):
+        moe.moe_mx_quantize([1.0])
+    with pytest.raises(KeyError):
+        moe.moe_mx_quantize(x, "fp5")
+    with pytest.raises(TypeError, match="float32 or bfloat16"):
+        moe.moe_mx_dequantize(x.byte(), x.byte(), dtype=torch.float16)
