@@ -498,15 +498,14 @@ int moe_mx_dequantize(const uint8_t* q, const uint8_t* scale, moe_mx_format fmt,
  * are tiled hangs on M / E, and an h next to a rounding's border may fall on its other
  * side in another tiling.  A row whose x holds a NaN or an infinity is NaN, alone.
  * Slots are tiled one by one (replicas of one expert are not merged).
- *   workspace  moe_mx_expert_ffn_workspace_bytes(n_src, M, ...) bytes (n_src = M
- *            without row_src), rewritten by every call: two calls in flight need two.
- * Limits: H and I multiples of 128; 1 <= E <= max_slots; H*I/2, 128 times the larger
- * of H and I, n_src*H/32, M*I/32 and with row_src n_src*H/2 below 0x7e000000.
+ *   workspace  moe_mx_expert_ffn_workspace_bytes(M, ...) bytes, rewritten by every
+ *            call: two calls in flight need two.
+ * Limits: H and I multiples of 128 up to 2^22, H*I/2 below 0x7e000000, M times the
+ * larger of H and I at most 2^36; 1 <= E <= max_slots.
  * All tensors 16-byte aligned.
  * check: MOE_CHECK_SLOTS, MOE_CHECK_BLOCKS (in x).
  */
-size_t moe_mx_expert_ffn_workspace_bytes(int64_t n_src, int64_t M, int H, int I, int max_slots,
-                                         moe_mx_format x_format); /* [host] */
+size_t moe_mx_expert_ffn_workspace_bytes(int64_t M, int H, int I, int max_slots, moe_mx_format x_format); /* [host] */
 int moe_mx_expert_ffn(const void* x, const int32_t* row_src, int64_t n_src, moe_dtype dt, int64_t M, int H, int I,
                       int E, const int32_t* slot_off, const int32_t* slot_expert, const int32_t* n_slots, int max_slots,
                       const uint8_t* w_gate, const uint8_t* s_gate, const uint8_t* w_up, const uint8_t* s_up,

@@ -463,9 +463,8 @@ def moe_mx_dequantize(q: torch.Tensor, scale: torch.Tensor, format="fp4", dtype=
     return r if type(r) is not int else _failed("moe_mx_dequantize", r)
 
 
-def moe_mx_expert_ffn_workspace_bytes(n_src: int, M: int, H: int, I: int, max_slots: int, x_format="fp6") -> int:
-    """n_src: the rows of x (M where the call has no row_src)."""
-    return int(lib().moe_mx_expert_ffn_workspace_bytes(n_src, M, H, I, max_slots, _MX_FORMAT[x_format]))
+def moe_mx_expert_ffn_workspace_bytes(M: int, H: int, I: int, max_slots: int, x_format="fp6") -> int:
+    return int(lib().moe_mx_expert_ffn_workspace_bytes(M, H, I, max_slots, _MX_FORMAT[x_format]))
 
 
 def moe_mx_expert_ffn(x: torch.Tensor, slot_off, slot_expert, n_slots, w_gate, w_up, w_down, act="swiglu",

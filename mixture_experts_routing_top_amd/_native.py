@@ -46,7 +46,7 @@ SIGNATURES = {
     "moe_combine_backward": (_i, [_p, _i, _p, _p, _i64, _p, _p, _i64, _i, _i, _p, _p, _p, _p]),
     "moe_mx_quantize": (_i, [_p, _i, _i64, _i64, _i, _p, _p, _p, _p]),
     "moe_mx_dequantize": (_i, [_p, _p, _i, _i64, _i64, _p, _i64, _i, _p, _p, _p]),
-    "moe_mx_expert_ffn_workspace_bytes": (_sz, [_i64, _i64, _i, _i, _i, _i]),
+    "moe_mx_expert_ffn_workspace_bytes": (_sz, [_i64, _i, _i, _i, _i]),
     "moe_mx_expert_ffn": (_i, [_p, _p, _i64, _i, _i64, _i, _i, _i, _p, _p, _p, _i, _p, _p, _p, _p, _p, _p, _i, _i, _p,
                                _p, _sz, _p, _p]),
     "moe_check_device_error": (_i, [_p, _p, _p]),

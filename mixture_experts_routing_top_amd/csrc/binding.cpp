@@ -524,9 +524,8 @@ PyObject* mx_expert_ffn(PyObject*, Args a, Py_ssize_t n) {
   const Stream s = stream_of(a[14], dev);
   const at::Tensor y = output(a[12], {M, H}, x.scalar_type(), dev, "y_perm");
   const int h = static_cast<int>(H), i = static_cast<int>(I), ms = static_cast<int>(max_slots);
-  const int64_t sources = row_src ? n_src : M;
   const at::Tensor ws =
-      workspace_of(a[13], moe_mx_expert_ffn_workspace_bytes(sources, M, h, i, ms, fmt), dev, "FFN workspace");
+      workspace_of(a[13], moe_mx_expert_ffn_workspace_bytes(M, h, i, ms, fmt), dev, "FFN workspace");
   int32_t* check = check_word(a[15], dev);
   const int rc = without_gil(dev, [&] {
     return moe_mx_expert_ffn(x.data_ptr(), row_src, n_src, dt, M, h, i, static_cast<int>(E), off.data_ptr<int32_t>(),

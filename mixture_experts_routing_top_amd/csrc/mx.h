@@ -160,11 +160,11 @@ struct Operand {
 };
 template <int kBits>
 __device__ __forceinline__ Operand encode_block(const float (&v)[32]) {
-  uint32_t m = 0;
+  float m = fabsf(v[0]);   // (a NaN stays: IEEE 754-2019 maximum, two values an instruction)
 #pragma unroll
-  for (int u = 0; u < 32; ++u) m = max(m, __float_as_uint(v[u]) & 0x7fffffffu);
+  for (int u = 1; u < 32; ++u) m = __builtin_elementwise_maximum(m, fabsf(v[u]));
   Operand o;
-  o.byte = scale_byte<kBits>(m);
+  o.byte = scale_byte<kBits>(__float_as_uint(m) & 0x7fffffffu);
   const float s = scale_value(o.byte);
   if constexpr (kBits == kF6) {
     f32x16 even, odd;   // the instruction takes its codes from the two in turn

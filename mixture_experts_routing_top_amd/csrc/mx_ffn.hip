@@ -13,9 +13,9 @@
 //             their codes;
 //   down:     y = Q(h) Wd^T.
 // Two kernels multiply.  tile_kernel: BM rows x 256 weight rows a block, operands
-// straight into LDS, 32x32x64 instructions.  stream_kernel: at most 16 rows by 32
-// columns a block, the weights from memory to registers, K split over the block's
-// waves: for few rows an expert the time is the weights' bytes.
+// straight into LDS, 32x32x64 instructions.  stream_kernel: at most 16 rows by 64
+// weight rows a block, K split over the block's waves: for few rows the time is the
+// weights' bytes.
 //
 // Why 6 bits and not 8.  Lane group g (lane / rows) of an operand holds K = 32 g ..
 // 32 g + 31 and their scale.  The instruction sums eight products at a time, each
@@ -25,10 +25,12 @@
 // of the largest beside them.  e2m3 has e4m3's four significant bits and runs at
 // the 4-bit rate.
 //
-// Activations in the workspace.  A row's codes lie in two planes: 16 bytes a block
-// (all of e2m1, the first two thirds of e2m3), then e2m3's last 8 bytes a block, so
-// that either is loaded in 16-byte pieces.  Their scales are K-major: one dword of
-// four bytes, a K step of 128, for every row in a run.
+// Activations in the workspace, one row for each of the M.  K-major: for every step
+// of 128 K values the rows' pieces follow one another, 64 bytes of codes (all of
+// e2m1, the first two thirds of each block of e2m3), in a second plane e2m3's last 32
+// bytes, and one dword of four scales.  A tile's step is then a run of whole lines
+// whatever K is.  (Row-major codes were gathered through the row map before: 64- and
+// 32-byte pieces, and the L2's request rate bounded the large products.)
 #include <algorithm>
 
 #include "common.h"
@@ -46,16 +48,12 @@ typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kStepK = 128;   // K values of a step: four blocks
-constexpr int kStreamRows = 16, kStreamCols = 32;
+constexpr int kStreamRows = 16;
 
-// One product: rows of A (codes [a_n, K / 2] and for e2m3 [a_n, K / 4], scales
-// K-major [K / 128][a_n] dwords), through a_rows or in place, times the experts'
-// weights (codes [E, N, K / 2], scales [E, N, K / 32]); B1/S1 the up weights beside
-// the gate's.
+// One product: rows of A (K-major planes of M rows) times the experts' weights (codes
+// [E, N, K / 2], scales [E, N, K / 32]); B1/S1 the up weights beside the gate's.
 struct MxGemm {
   const uint8_t *A, *A2, *As;
-  const int32_t* a_rows;
-  int64_t a_n;
   const uint8_t *B0, *B1, *S0, *S1;
   int K, N;
   int64_t M;
@@ -66,27 +64,30 @@ struct MxGemm {
   uint8_t *C2, *Cs;    // h's second plane and scales
 };
 
-// A block's codes and scale to their places: row `row` of n, columns from `col`.
+// A block's codes and scale to their places in planes of M rows.
 template <int kBits>
-__device__ __forceinline__ void store_block(const mx::Operand& o, int64_t row, int64_t n, int K, int col, uint8_t* q,
+__device__ __forceinline__ void store_block(const mx::Operand& o, int64_t row, int64_t M, int block, uint8_t* q,
                                             uint8_t* q2, uint8_t* scale) {
-  *reinterpret_cast<uint4*>(q + (row * K + col) / 2) = o.first;
-  if constexpr (kBits == mx::kF6) *reinterpret_cast<uint2*>(q2 + (row * K + col) / 4) = o.rest;
-  scale[(col / kStepK * n + row) * 4 + (col / mx::kBlock) % 4] = static_cast<uint8_t>(o.byte);
+  const int64_t at = (block / 4 * M + row) * 4 + block % 4;
+  *reinterpret_cast<uint4*>(q + at * 16) = o.first;
+  if constexpr (kBits == mx::kF6) *reinterpret_cast<uint2*>(q2 + at * 8) = o.rest;
+  scale[at] = static_cast<uint8_t>(o.byte);
 }
 
 // ------------------------------------------------------------------- preparation
-// Block 0 lists the row tiles; the others quantise x.
+// Block (0, 0) lists the row tiles; blocks (1 and up, k) quantise step k of the M rows of
+// x (through the row map; rows mapped outside x are zero), one block of 32 a lane.
 template <bool kBf16, int kBits>
-__global__ __launch_bounds__(256) void prepare_kernel(const void* __restrict__ x, int64_t R, int K,
-                                                      uint8_t* __restrict__ q, uint8_t* __restrict__ q2,
-                                                      uint8_t* __restrict__ scale,
+__global__ __launch_bounds__(256) void prepare_kernel(const void* __restrict__ x, const int32_t* __restrict__ row_src,
+                                                      int64_t n_src, int K, uint8_t* __restrict__ q,
+                                                      uint8_t* __restrict__ q2, uint8_t* __restrict__ scale,
                                                       const int32_t* __restrict__ slot_off,
                                                       const int32_t* __restrict__ slot_expert,
                                                       const int32_t* __restrict__ n_slots, int max_slots, int64_t M,
                                                       int E, int rows_per_tile, int cap, int4* __restrict__ tiles,
                                                       int32_t* __restrict__ n_tiles, int32_t* __restrict__ check) {
   if (blockIdx.x == 0) {
+    if (blockIdx.y > 0) return;
     __shared__ int wave_sum[4];
     __shared__ int before;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -134,22 +135,23 @@ __global__ __launch_bounds__(256) void prepare_kernel(const void* __restrict__ x
     if (check) raise_check(check, bad, MOE_CHECK_SLOTS);
     return;
   }
-  const int64_t b = static_cast<int64_t>(blockIdx.x - 1) * 256 + threadIdx.x, per_row = K / mx::kBlock;
+  const int64_t i = static_cast<int64_t>(blockIdx.x - 1) * 256 + threadIdx.x, row = i >> 2;
+  const int block = static_cast<int>(blockIdx.y) * 4 + static_cast<int>(i & 3);
   bool bad = false;
-  if (b < R * per_row) {
-    const int64_t row = b / per_row;
-    const int col = static_cast<int>(b - row * per_row) * mx::kBlock;
-    float v[32];
+  if (row < M) {
+    const int64_t src = row_src ? row_src[row] : row;
+    float v[32] = {};
+    if (src >= 0 && src < n_src)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float part[8];
-      rows::unpack8<kBf16>(rows::load8<kBf16>(x, row * K + col + 8 * u), part);
+      for (int u = 0; u < 4; ++u) {
+        float part[8];
+        rows::unpack8<kBf16>(rows::load8<kBf16>(x, src * K + block * mx::kBlock + 8 * u), part);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[8 * u + i] = part[i];
-    }
+        for (int j = 0; j < 8; ++j) v[8 * u + j] = part[j];
+      }
     const mx::Operand o = mx::encode_block<kBits>(v);
     bad = o.byte == 255;
-    store_block<kBits>(o, row, R, K, col, q, q2, scale);
+    store_block<kBits>(o, row, M, block, q, q2, scale);
   }
   if (check) raise_check(check, bad, MOE_CHECK_BLOCKS);
 }
@@ -201,20 +203,36 @@ __device__ __forceinline__ bool place(int total_m, int n_col_tiles, int b, int* 
   return true;
 }
 
+// z Phi(z), the exact GELU: Phi(-|z|) = e^(-z^2 / 2) P(t) / 2, t = 1 / (1 + p |z| / sqrt 2),
+// Abramowitz and Stegun 7.1.26, off by at most 0.75e-7 |z|; thirteen instructions and two
+// of the quarter rate, a third of what erff takes.
+__device__ __forceinline__ float fast_gelu(float z) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3275911f * 0.70710678f, 1.f));
+  float p = fmaf(t, 0.5f * 1.061405429f, -0.5f * 1.453152027f);
+  p = fmaf(p, t, 0.5f * 1.421413741f);
+  p = fmaf(p, t, -0.5f * 0.284496736f);
+  p = fmaf(p, t, 0.5f * 0.254829592f) * t;
+  const float tail = p * __builtin_amdgcn_exp2f(z * z * -0.72134752f);
+  return fmaxf(z, 0.f) - fabsf(z * tail);
+}
+
 // What the epilogue makes of the accumulators.
 enum MxEpi { kMxSwiGLU = 0, kMxGELU = 1, kMxBf16 = 2, kMxF32 = 3 };
 constexpr int mats(int epi) { return epi == kMxSwiGLU ? 2 : 1; }
 
 // ---- large batches ---------------------------------------------------------------
+// LDS: three stages of A (a K step of 128: two planes and the scales), stages of the
+// weights' codes of kBStep K values, and two buffers of the weights' scales for 512.
+// 256-row tiles take the weights 256 K values at a time: whole 128-byte lines of a
+// weight row.  64- and 128-row tiles take 128, and 64-row tiles fit twice on a CU.
 template <int kBits, int BM>
 struct TileShape {
-  static constexpr int kABytes = BM * 64;                  // a step's rows of A, first plane
-  static constexpr int kA2Bytes = kBits == mx::kF6 ? (BM < 128 ? 128 : BM) * 32 : 0;
-  static constexpr int kBBytes = 256 * 64;
-  static constexpr int kA2 = kABytes, kB = kA2 + kA2Bytes, kScales = kB + kBBytes;
-  static constexpr int kStage = kScales + 512 * 4;         // 256 weight rows' and up to 256 rows' dwords
-  static constexpr int kStages = BM == 64 || (kBits == mx::kF6 && BM == 256) ? 3 : 4;
-  static constexpr int kLds = kStages * kStage;
+  static constexpr int kBStep = BM == 256 ? 256 : 128;
+  static constexpr int kABytes = BM * 64, kA2Bytes = kBits == mx::kF6 ? BM * 32 : 0;
+  static constexpr int kA2 = kABytes, kAScales = kA2 + kA2Bytes, kAStage = kAScales + BM * 4, kAStages = 3;
+  static constexpr int kBStage = 256 * kBStep / 2, kBStages = kBStep == 256 ? 2 : 3;
+  static constexpr int kB = kAStages * kAStage, kBScales = kB + kBStages * kBStage;
+  static constexpr int kLds = kBScales + 2 * 256 * 16;
 };
 
 #pragma clang diagnostic push
@@ -234,10 +252,11 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void tile_kernel(const MxGem
   constexpr int WM = BM == 256 ? 2 : 1, WN = 4 / WM;      // the waves' grid
   constexpr int TM = BM / WM / 32, TN = 256 / WN / 32;    // 32 x 32 tiles a wave
   constexpr int NMAT = mats(EPI);
-  constexpr int PA = S::kABytes / 4096, PA2 = S::kA2Bytes / 4096, PB = S::kBBytes / 4096;   // 16-byte loads a lane and step
-  constexpr int L = PA + PA2 + PB + 2;                                                      // and all loads
+  constexpr int PA = S::kABytes / 4096, PB = S::kBStage / 4096;   // 16-byte loads a lane: a step of A, a stage of weights
+  constexpr int PA2 = (S::kA2Bytes + 4095) / 4096;
+  constexpr int LA = PA + PA2 + 1;                                // loads of a step of A, its scales with them
+  constexpr bool kWide = S::kBStep == 256;
   constexpr int NSUB = 256 / NMAT;                                // output columns a block
-  constexpr int ST = S::kStages;
   __shared__ __align__(1024) char lds[S::kLds];
   int mt, nt;
   if (!place(*g.n_tiles, g.n_col_tiles, blockIdx.x, &mt, &nt)) return;
@@ -249,69 +268,50 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void tile_kernel(const MxGem
   const int K = g.K, KT = K / kStepK;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int b_bytes = K / 2, a2_bytes = K / 4, s_bytes = K / mx::kBlock;   // a row's codes (A's as the weights') and scales
-
-  // sources: A by the row map, or the tile's own rows; one expert's weights
-  const int64_t first = g.a_rows ? 0 : row0, span = g.a_rows ? g.a_n : n;
-  const u32x4 ra = dma_rsrc(g.A + first * b_bytes, span * b_bytes);
-  const u32x4 ra2 = kBits == mx::kF6 ? dma_rsrc(g.A2 + first * a2_bytes, span * a2_bytes) : ra;
-  const u32x4 rsa = dma_rsrc(g.As, g.a_n * 4 * KT);
+  const int b_bytes = K / 2, s_bytes = K / mx::kBlock;   // a weight row's codes and scales
   const int64_t wofs = static_cast<int64_t>(e) * g.N;
   const int64_t b_all = static_cast<int64_t>(g.N) * b_bytes, s_all = static_cast<int64_t>(g.N) * s_bytes;
   const u32x4 rb0 = dma_rsrc(g.B0 + wofs * b_bytes, b_all), rs0 = dma_rsrc(g.S0 + wofs * s_bytes, s_all);
   const u32x4 rb1 = NMAT == 2 ? dma_rsrc(g.B1 + wofs * b_bytes, b_all) : rb0;
   const u32x4 rs1 = NMAT == 2 ? dma_rsrc(g.S1 + wofs * s_bytes, s_all) : rs0;
 
-  // Lane offsets of this wave's loads.  LDS rows hold a step (64 bytes of the first
-  // plane and of the weights, 32 of the second) in 16-byte chunks, chunk c at c ^
-  // swizzle(row): the loads write LDS in lane order, so the lane picks the chunk
-  // that belongs there.  Rows past the tile's and rows mapped outside x get an
-  // offset past the descriptor's end and read as zero.
-  auto source = [&](int r) -> int {
-    if (r >= n) return -1;
-    if (!g.a_rows) return r;
-    const int src = g.a_rows[row0 + r];
-    return src < g.a_n ? src : -1;
-  };
-  int offa[PA], offa2[PA2 ? PA2 : 1], offb[PB], offsa, offsb;
-#pragma unroll
-  for (int p = 0; p < PA; ++p) {
-    const int idx = (p * 4 + wave) * 64 + lane, r = idx / 4, src = source(r);
-    offa[p] = src >= 0 ? src * b_bytes + ((idx % 4) ^ ((r >> 2) & 3)) * 16 : kGatherOut;
-  }
-#pragma unroll
-  for (int p = 0; p < PA2; ++p) {
-    const int idx = (p * 4 + wave) * 64 + lane, r = idx / 2, src = source(r);
-    offa2[p] = src >= 0 ? src * a2_bytes + ((idx % 2) ^ ((r >> 3) & 1)) * 16 : kGatherOut;
-  }
-  {
-    const int r = wave * 64 + lane, src = r < BM ? source(r) : -1;
-    offsa = src >= 0 ? static_cast<int>(first + src) * 4 : kGatherOut;
-  }
-#pragma unroll
-  for (int p = 0; p < PB; ++p) {
-    const int idx = (p * 4 + wave) * 64 + lane, r = idx / 4;
-    const int c = (idx % 4) ^ ((r >> 2) & 3);
-    offb[p] = (n0 + (NMAT == 2 ? r % 128 : r)) * b_bytes + c * 16;
-  }
-  {
-    const int r = wave * 64 + lane;
-    offsb = (n0 + (NMAT == 2 ? r % 128 : r)) * s_bytes;
-  }
+  // Lane offsets of this wave's loads.  LDS rows hold a step in 16-byte chunks, chunk c at
+  // c ^ swizzle(row): the loads write LDS in lane order, so the lane picks the chunk that
+  // belongs there.  Rows past the tile's lie past A's descriptors, columns past N past the
+  // weights'; they read as zero.
+  const int ra_ = wave * 16 + lane / 4, offa = ra_ * 64 + ((lane % 4) ^ ((ra_ >> 2) & 3)) * 16;           // + 64 rows a load
+  const int ra2_ = wave * 32 + lane / 2, offa2 = ra2_ * 32 + ((lane % 2) ^ ((ra2_ >> 3) & 1)) * 16;       // + 128 rows
+  const int rsa_ = wave % (BM / 64) * 64 + lane;                                                          // (waves share rows)
+  const int rb_ = kWide ? wave * 8 + lane / 8 : wave * 16 + lane / 4;                                     // + 32 or 64 rows
+  const int offb = (n0 + rb_) * b_bytes + (kWide ? (lane % 8) ^ swz(rb_) : (lane % 4) ^ ((rb_ >> 2) & 3)) * 16;
+  const int offsb = (n0 + (wave * 64 + lane) % NSUB) * s_bytes;
+  const int b_pass = (kWide ? 32 : 64) * b_bytes;
   const unsigned lds0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(
       (__attribute__((address_space(3))) char*)lds));
-  const int a_step = static_cast<int>(g.a_n) * 4;
-  auto issue = [&](int kt, int stage) {
-    const unsigned base = lds0 + stage * S::kStage;
-#pragma unroll
-    for (int p = 0; p < PA; ++p) load_lds(ra, offa[p] + kt * 64, base + (p * 4 + wave) * 1024);
-#pragma unroll
-    for (int p = 0; p < PA2; ++p) load_lds(ra2, offa2[p] + kt * 32, base + S::kA2 + (p * 4 + wave) * 1024);
-#pragma unroll
-    for (int p = 0; p < PB; ++p)
-      load_lds(NMAT == 2 && p >= PB / 2 ? rb1 : rb0, offb[p] + kt * 64, base + S::kB + (p * 4 + wave) * 1024);
-    load_lds4(NMAT == 2 && wave >= 2 ? rs1 : rs0, offsb + kt * 4, base + S::kScales + wave * 256);
-    load_lds4(rsa, offsa == kGatherOut ? kGatherOut : offsa + kt * a_step, base + S::kScales + 1024 + wave * 256);
+  // Load q of step kt of A.  Past the last step the descriptors are empty: nothing is
+  // read, and the count of loads in flight stays the same.
+  auto issue_a = [&](int q, int kt, int stage) {
+    const int64_t at = static_cast<int64_t>(kt) * g.M + row0;
+    const int64_t rows = kt < KT ? n : 0;
+    const unsigned base = lds0 + stage;
+    if (q < PA) {
+      load_lds(dma_rsrc(g.A + at * 64, rows * 64), offa + q * 4096, base + (q * 4 + wave) * 1024);
+    } else if (q < PA + PA2 && (BM > 64 || wave < 2)) {
+      const int p = q - PA;
+      load_lds(dma_rsrc(g.A2 + at * 32, rows * 32), offa2 + p * 4096, base + S::kA2 + (p * 4 + wave) * 1024);
+    } else {   // (also waves 2 and 3 of a 64-row tile in the second plane's place)
+      load_lds4(dma_rsrc(g.As + at * 4, rows * 4), rsa_ * 4, base + S::kAScales + wave % (BM / 64) * 256);
+    }
+  };
+  // Load p of stage ks of the weights; the scales of group kg (512 K values).
+  auto issue_b = [&](int p, int ks, int stage) {
+    const unsigned past = ks * S::kBStep < K ? 0u : static_cast<unsigned>(kGatherOut);
+    load_lds(NMAT == 2 && p >= PB / 2 ? rb1 : rb0, offb + p % (PB / NMAT) * b_pass + ks * (S::kBStep / 2) + past,
+             lds0 + stage + (p * 4 + wave) * 1024);
+  };
+  auto issue_scales = [&](int kg) {
+    const unsigned past = kg * 512 < K ? 0u : static_cast<unsigned>(kGatherOut);
+    load_lds(NMAT == 2 && wave >= 2 ? rs1 : rs0, offsb + kg * 16 + past, lds0 + S::kBScales + (kg & 1) * 4096 + wave * 1024);
   };
 
   f32x16 acc[TM][TN];
@@ -325,60 +325,128 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void tile_kernel(const MxGem
   // the weight tiles of this wave: NMAT == 2: gate rows, then up rows 128 on
   const int half = lane >> 5, lr = lane & 31;
   auto b_row = [&](int j) { return NMAT == 2 ? (j < TN / 2 ? 0 : 128) + wn * (TN / 2) * 32 + (j % (TN / 2)) * 32 : wn * TN * 32 + j * 32; };
-  auto compute = [&](int stage) {
-    const char* base = lds + stage * S::kStage;
-    const char* a = base + (wm * TM * 32 + lr) * 64;
-    const char* a2 = base + S::kA2 + (wm * TM * 32 + lr) * 32 + half * 8;
-    const char* b = base + S::kB + lr * 64;
-    const uint32_t* sc = reinterpret_cast<const uint32_t*>(base + S::kScales);
-    uint32_t sa[TM], sb[TN];
-#pragma unroll
-    for (int i = 0; i < TM; ++i) sa[i] = sc[256 + wm * TM * 32 + i * 32 + lr] >> (8 * half);
-#pragma unroll
-    for (int j = 0; j < TN; ++j) sb[j] = sc[b_row(j) + lr] >> (8 * half);
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      i32x4 fb[TN];
-      Frag fa[TM];
-      const int chunk = ((2 * s + half) ^ ((lr >> 2) & 3)) * 16;
-#pragma unroll
-      for (int j = 0; j < TN; ++j) fb[j] = *reinterpret_cast<const i32x4*>(b + b_row(j) * 64 + chunk);
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        fa[i].first = *reinterpret_cast<const i32x4*>(a + i * 32 * 64 + chunk);
-        if constexpr (kBits == mx::kF6)
-          fa[i].rest = *reinterpret_cast<const i32x2*>(a2 + i * 32 * 32 + (s ^ ((lr >> 3) & 1)) * 16);
-      }
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[i][j] = s == 0 ? mma32<kBits, 0>(fb[j], fa[i], acc[i][j], sb[j], sa[i])
-                             : mma32<kBits, 2>(fb[j], fa[i], acc[i][j], sb[j], sa[i]);
+  // Fragment read r of half step s: weight tile 0, the A tiles, the other weight tiles; a
+  // step's scales come with its first half.  oa, ob: the stages' places in LDS; for wide
+  // stages of the weights `odd` says which half of the stage.
+  i32x4 fb[2][TN];
+  Frag fa[2][TM];
+  uint32_t sa[TM], sb[TN], next_sa[TM], next_sb[TN];
+  const int a_row = wm * TM * 32 + lr;
+  const int at_a = a_row * 64 + (half ^ ((lr >> 2) & 3)) * 16;                            // second half step: two chunks on
+  const int at_a2 = S::kA2 + a_row * 32 + ((lr >> 3) & 1) * 16 + half * 8;                // (one on)
+  const int at_b = kWide ? lr * 128 + (half ^ swz(lr)) * 16 : lr * 64 + (half ^ ((lr >> 2) & 3)) * 16;
+  const int at_sa = S::kAScales + a_row * 4, at_sb = S::kBScales + lr * 16;
+  constexpr int NR = TM + TN, NM = TM * TN;
+  constexpr int kReads = (2 * NR + NM - 1) / NM;   // reads an instruction: all of them in the half's first half
+  auto frag = [&](int r, int oa, int ob, int odd, int s, int os) {
+    if (r >= 1 && r <= TM) {
+      const int i = r - 1;
+      fa[s][i].first = *reinterpret_cast<const i32x4*>(lds + ((at_a ^ (32 * s)) + oa) + i * 32 * 64);
+      if constexpr (kBits == mx::kF6)
+        fa[s][i].rest = *reinterpret_cast<const i32x2*>(lds + ((at_a2 ^ (16 * s)) + oa) + i * 32 * 32);
+      if (s == 0) next_sa[i] = *reinterpret_cast<const uint32_t*>(lds + (at_sa + oa) + i * 128);
+    } else {
+      const int j = r == 0 ? 0 : r - TM;
+      fb[s][j] = *reinterpret_cast<const i32x4*>(lds + ((at_b ^ (64 * odd + 32 * s)) + ob) + b_row(j) * (kWide ? 128 : 64));
+      if (s == 0) next_sb[j] = *reinterpret_cast<const uint32_t*>(lds + (at_sb + os) + b_row(j) * 16);
     }
   };
+  auto mma = [&](int m, int s) {
+    const int i = m % TM, j = m / TM;
+    acc[i][j] = s == 0 ? mma32<kBits, 0>(fb[s][j], fa[s][i], acc[i][j], sb[j], sa[i])
+                       : mma32<kBits, 2>(fb[s][j], fa[s][i], acc[i][j], sb[j], sa[i]);
+  };
 
-  // Stage kt % ST holds step kt.  A step waits for its own loads (those of the ST
-  // - 2 steps after it stay in flight), meets the other waves, and loads into the
-  // stage that all of them left in the step before.
+  // A step's two halves run on registers that were read during the half before.  In the
+  // middle of step kt the loads of step kt + 1 are awaited, those issued after them stay
+  // in flight, and the waves meet: what step kt held in LDS has been read then and takes
+  // the loads of step kt + 3, which are issued over this half and the next step's first
+  // (in one half they filled the load queue and held the wave up).  Wide weights: the
+  // stage that an odd step ends takes the stage after next over three halves.
+  // An odd count of steps is made even by one on zeros: no A is loaded for it and its
+  // weights' scales are 2^-127.
+  const int steps = (KT + 1) & ~1;
+  int a_here = 0, a_free = 2 * S::kAStage, b_here = 0, b_free = (S::kBStages - 1) * S::kBStage;   // (free: the last step's)
+  constexpr int kA1 = LA / 2, kA2 = LA - LA / 2, kB1 = kWide ? 3 : PB / 2, kB2 = kWide ? 6 : PB;
+  auto half_step = [&](int kt, auto odd_, auto second_) {
+    constexpr int odd = decltype(odd_)::value, second = decltype(second_)::value;
+    constexpr int kA = odd ? kA1 : kA2, kA_ = odd ? kA2 : kA1;     // of A issued in this step's second half, the last one's
+    constexpr int from_a = second ? 0 : kA_, to_a = second ? kA : LA;
+    constexpr int from_b = kWide ? (odd ? 0 : second ? kB2 : kB1) : second ? 0 : kB1;
+    constexpr int to_b = kWide ? (odd ? (second ? kB1 : 0) : second ? PB : kB2) : second ? kB1 : PB;
+    constexpr int LS = second && !odd, LB = to_b - from_b, LT = LS + LB + to_a - from_a;
+    const int a_next = a_here + S::kAStage == S::kB ? 0 : a_here + S::kAStage;
+    constexpr bool new_b = !kWide || odd;
+    const int b_next = !new_b ? b_here : b_here + S::kBStage == S::kBStages * S::kBStage ? 0 : b_here + S::kBStage;
+    const int os = (kt + 1) % 4 * 4 + (kt + 1) / 4 % 2 * 4096;
+    const int a_stage = second ? a_here : a_free, a_kt = second ? kt + 3 : kt + 2;
+    const int b_stage = kWide ? (odd ? b_here : b_free) : second ? b_here : b_free;
+    const int b_ks = kWide ? (kt + odd) / 2 + 1 : a_kt;
+    int rd = 0, ld = 0;
 #pragma unroll
-  for (int kt = 0; kt < ST - 1; ++kt)
-    if (kt < KT) issue(kt, kt);
-  int kt = 0;
-  for (; kt + ST - 1 < KT;) {
+    for (int m = 0; m < NM; ++m) {
+      mma(m, second);
 #pragma unroll
-    for (int u = 0; u < ST; ++u) {
-      if (kt + ST - 1 >= KT) break;
-      wait_vm<(ST - 2) * L>();
-      __syncthreads();
-      issue(kt + ST - 1, (u + ST - 1) % ST);
-      compute(u);
-      ++kt;
+      for (; rd < NR && rd <= m * kReads; ++rd) {
+        if constexpr (second) frag(rd, a_next, S::kB + b_next, kWide ? odd ^ 1 : 0, 0, os);
+        else frag(rd, a_here, S::kB + b_here, kWide ? odd : 0, 1, 0);
+      }
+#pragma unroll
+      for (; ld < LT && ld * NM < (m + 1) * LT; ++ld) {
+        if (ld < LB) {
+          issue_b(from_b + ld, b_ks, S::kB + b_stage);
+        } else if (LS && ld == LB) {
+          if (kt % 4 == 0) issue_scales(kt / 4 + 1);
+        } else {
+          issue_a(from_a + ld - LB - LS, a_kt, a_stage);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (second) {
+      a_free = a_here;
+      a_here = a_next;
+      if (new_b) {
+        b_free = b_here;
+        b_here = b_next;
+      }
+    }
+  };
+  auto step = [&](int kt, auto odd_) {
+    constexpr int odd = decltype(odd_)::value;
+    const uint32_t live = kt < KT ? ~0u : 0u;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) sa[i] = next_sa[i] >> (8 * half);   // this lane's two bytes lowest
+#pragma unroll
+    for (int j = 0; j < TN; ++j) sb[j] = (next_sb[j] & live) >> (8 * half);
+    half_step(kt, odd_, std::integral_constant<int, 0>{});
+    wait_vm<kWide ? (odd ? LA : LA + kB2) : LA + PB>();
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+    half_step(kt, odd_, std::integral_constant<int, 1>{});
+  };
+  issue_scales(0);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int q = 0; q < LA; ++q) issue_a(q, k, k * S::kAStage);
+    if (!kWide || k == 0)
+#pragma unroll
+      for (int p = 0; p < PB; ++p) issue_b(p, k, S::kB + k * S::kBStage);
+  }
+#pragma unroll
+  for (int p = 0; p < kB1; ++p) issue_b(p, kWide ? 1 : 2, S::kB + b_free);
+#pragma unroll
+  for (int q = 0; q < kA1; ++q) issue_a(q, 2, a_free);
+  wait_vm<LA + kA1 + kB1 + (kWide ? 0 : PB)>();
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < NR; ++r) frag(r, 0, S::kB, 0, 0, 0);
+  for (int kt = 0; kt < steps; kt += 2) {
+    step(kt, std::integral_constant<int, 0>{});
+    step(kt + 1, std::integral_constant<int, 1>{});
   }
   wait_vm<0>();
-  __syncthreads();
-  for (; kt < KT; ++kt) compute(kt % ST);
 
   // ---- epilogue: lane (half, lr) holds row lr's columns 8 q + 4 half + i of each 32
   if constexpr (EPI == kMxSwiGLU || EPI == kMxGELU) {
@@ -388,7 +456,7 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void tile_kernel(const MxGem
     auto value = [&](int b, int u) {
       const int i = b / TC, j = b % TC;
       if constexpr (NMAT == 2) return swiglu_h(acc[i][j][u], acc[i][j + TC][u]);
-      else return gelu_h(acc[i][j][u]);
+      else return fast_gelu(acc[i][j][u]);
     };
 #pragma unroll
     for (int b = 0; b < TM * TC; b += 2) {
@@ -402,7 +470,7 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void tile_kernel(const MxGem
       const mx::Operand o = mx::encode_block<kBits>(v);
       const int mine = b + half, i = mine / TC, j = mine % TC;
       const int r = (wm * TM + i) * 32 + lr, col = n0 + (wn * TC + j) * 32;
-      if (r < n && col < g.N) store_block<kBits>(o, row0 + r, g.M, g.N, col, static_cast<uint8_t*>(g.C), g.C2, g.Cs);
+      if (r < n && col < g.N) store_block<kBits>(o, row0 + r, g.M, col / mx::kBlock, static_cast<uint8_t*>(g.C), g.C2, g.Cs);
     }
   } else {
 #pragma unroll
@@ -437,115 +505,137 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void tile_kernel(const MxGem
 }
 
 // ---- few rows an expert ------------------------------------------------------------
-constexpr int kStreamWaves = 4, kStreamUnroll = 4;
+// At most 16 rows by four 16-row weight tiles (two of the gate and two of the up
+// weights, or 64 columns of y).  Wave w takes the w-th part of K, through a ring of its
+// own in LDS, and the parts are added in wave order.  Why LDS, where nothing is shared:
+// a load instruction takes the address path one cycle for every line that a quarter
+// wave touches, and an operand's quarter is 16 weight rows; loaded in runs of 64 bytes
+// a row it is four (measured: 64 against 16 cycles for 1 KB), and the operands' own
+// loads came to 4.2 TB/s.
+template <int kBits, int NT>
+struct StreamShape {   // a wave's LDS: stages of one K step, two buffers of four steps' weight scales
+  static constexpr int kRing = NT == 2 ? 4 : 3;
+  static constexpr int kA = NT * 1024, kA2 = kA + 1024, kAScales = kA2 + (kBits == mx::kF6 ? 512 : 0);
+  static constexpr int kStage = kAScales + 64;
+  static constexpr int kBScales = kRing * kStage, kWave = kBScales + 2 * NT * 256;
+};
 
-template <int kBits, int EPI>
-__global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(const MxGemm g) {
-  constexpr int NMAT = mats(EPI), NT = 2 * NMAT;   // 16-column weight tiles: two of each matrix
-  __shared__ f32x4 part[kStreamWaves - 1][NT][64];
+template <int kBits, int EPI, int NT, int kStreamWaves>
+__global__ __launch_bounds__(64 * kStreamWaves, 2) void stream_kernel(const MxGemm g) {
+  using S = StreamShape<kBits, NT>;
+  constexpr int NMAT = mats(EPI), NC = NT / NMAT, kCols = 16 * NC, R = S::kRing;
+  constexpr int L = NT + 2 + (kBits == mx::kF6 ? 1 : 0);   // a step's loads (without the weights' scales)
+  __shared__ __align__(1024) char lds[kStreamWaves * S::kWave];
   const int mt = blockIdx.x / g.n_col_tiles, nt = blockIdx.x - mt * g.n_col_tiles;
+  const int4 tile = g.tiles[mt];   // (the list has room for every block of the grid)
   if (mt >= *g.n_tiles) return;
-  const int4 tile = g.tiles[mt];
   const int e = __builtin_amdgcn_readfirstlane(tile.x);
   const int64_t row0 = __builtin_amdgcn_readfirstlane(tile.y);
   const int n = __builtin_amdgcn_readfirstlane(tile.z) - static_cast<int>(row0);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, grp = lane >> 4;
-  const int K = g.K, KT = K / kStepK;
-  const int b_bytes = K / 2, a2_bytes = K / 4, s_bytes = K / mx::kBlock;
+  const int K = g.K, KT = K / kStepK, n0 = nt * kCols;
+  const int b_bytes = K / 2, s_bytes = K / mx::kBlock;
   const int64_t wofs = static_cast<int64_t>(e) * g.N;
   const int64_t b_all = static_cast<int64_t>(g.N) * b_bytes, s_all = static_cast<int64_t>(g.N) * s_bytes;
-  const __amdgpu_buffer_rsrc_t rb0 = rsrc(g.B0 + wofs * b_bytes, b_all), rs0 = rsrc(g.S0 + wofs * s_bytes, s_all);
-  const __amdgpu_buffer_rsrc_t rb1 = NMAT == 2 ? rsrc(g.B1 + wofs * b_bytes, b_all) : rb0;
-  const __amdgpu_buffer_rsrc_t rs1 = NMAT == 2 ? rsrc(g.S1 + wofs * s_bytes, s_all) : rs0;
-  // rows past the tile's and rows mapped outside x read as zero: their offsets lie
-  // past the descriptors' ends
-  int src = lr < n ? lr : -1;
-  if (g.a_rows && lr < n) {
-    src = g.a_rows[row0 + lr];
-    if (src >= g.a_n) src = -1;
-  }
-  const int64_t first = g.a_rows ? 0 : row0, span = g.a_rows ? g.a_n : n;
-  const __amdgpu_buffer_rsrc_t ra = rsrc(g.A + first * b_bytes, span * b_bytes);
-  const __amdgpu_buffer_rsrc_t ra2 = kBits == mx::kF6 ? rsrc(g.A2 + first * a2_bytes, span * a2_bytes) : ra;
-  const __amdgpu_buffer_rsrc_t rsa = rsrc(g.As, g.a_n * 4 * KT);
-  const int offa = src < 0 ? kGatherOut : src * b_bytes + grp * 16;
-  const int offa2 = src < 0 ? kGatherOut : src * a2_bytes + grp * 8;
-  const int offsa = src < 0 ? kGatherOut : static_cast<int>(first + src) * 4;
-  const int a_step = static_cast<int>(g.a_n) * 4;
-  const int col0 = nt * kStreamCols + lr;
-  int offb[2], offs[2];
+  const u32x4 rb0 = dma_rsrc(g.B0 + wofs * b_bytes, b_all), rs0 = dma_rsrc(g.S0 + wofs * s_bytes, s_all);
+  const u32x4 rb1 = NMAT == 2 ? dma_rsrc(g.B1 + wofs * b_bytes, b_all) : rb0;
+  const u32x4 rs1 = NMAT == 2 ? dma_rsrc(g.S1 + wofs * s_bytes, s_all) : rs0;
+  char* const mine = lds + wave * S::kWave;
+  const unsigned at0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(
+      (__attribute__((address_space(3))) char*)lds)) + wave * S::kWave;
+  // a load's 16 rows of 64 bytes; chunk c of a row at c ^ swizzle(row)
+  const int r4 = lane / 4, run = r4 * 64 + ((lane % 4) ^ ((r4 >> 2) & 3)) * 16;
+  const int offb = (n0 + r4) * b_bytes + (run - r4 * 64), b_tile = 16 * b_bytes;
+  const int offsb = (n0 + lane % kCols) * s_bytes;
+  const int begin = KT * wave / kStreamWaves, end = KT * (wave + 1) / kStreamWaves;
+  auto issue = [&](int kt) {   // past the end every offset lies past its descriptor's end
+    const unsigned base = at0 + (kt - begin) % R * S::kStage;
+    const unsigned past = kt < end ? 0u : static_cast<unsigned>(kGatherOut);
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    offb[c] = (col0 + 16 * c) * b_bytes + grp * 16;
-    offs[c] = (col0 + 16 * c) * s_bytes;
-  }
+    for (int j = 0; j < NT; ++j)
+      load_lds(NMAT == 2 && j >= NC ? rb1 : rb0, offb + j % NC * b_tile + kt * 64 + past, base + j * 1024);
+    const int64_t at = static_cast<int64_t>(kt) * g.M + row0;
+    const int64_t rows = kt < end ? n : 0;
+    load_lds(dma_rsrc(g.A + at * 64, rows * 64), run, base + S::kA);
+    if (kBits == mx::kF6 && lane < 32) load_lds(dma_rsrc(g.A2 + at * 32, rows * 32), lane * 16, base + S::kA2);
+    if (lane < 16) load_lds4(dma_rsrc(g.As + at * 4, rows * 4), lane * 4, base + S::kAScales);
+  };
+  auto issue_scales = [&](int kg) {   // steps begin + 4 kg and three on
+    const int off = offsb + (begin + 4 * kg) * 4;
+    const unsigned to = at0 + S::kBScales + (kg & 1) * (NT * 256);
+    if (lane < kCols) load_lds(rs0, off, to);
+    if (NMAT == 2 && lane >= kCols) load_lds(rs1, off, to);
+  };
   f32x4 acc[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int end = KT * (wave + 1) / kStreamWaves;
-  for (int k0 = KT * wave / kStreamWaves; k0 < end; k0 += kStreamUnroll) {
-    i32x4 w[kStreamUnroll][NT], sw[NT];
-    Frag a[kStreamUnroll];
-    uint32_t sa[kStreamUnroll];
+  issue_scales(0);
 #pragma unroll
-    for (int j = 0; j < NT; ++j) sw[j] = load16(j >= 2 ? rs1 : rs0, offs[j % 2] + k0 * 4);   // four steps' scales
+  for (int u = 0; u < R; ++u) issue(begin + u);
+  for (int kt = begin; kt < end; ++kt) {
+    const int k = kt - begin;
+    wait_vm<(R - 1) * L>();
+    asm volatile("" ::: "memory");
+    const char* const at = mine + k % R * S::kStage;
+    const int chunk = (grp ^ ((lr >> 2) & 3)) * 16;
+    i32x4 w[NT];
+    uint32_t sw[NT];
+    Frag a{};
 #pragma unroll
-    for (int u = 0; u < kStreamUnroll; ++u) {
-      if (k0 + u >= end) break;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) w[u][j] = load16(j >= 2 ? rb1 : rb0, offb[j % 2] + (k0 + u) * 64);
-      a[u].first = load16(ra, offa + (k0 + u) * 64);
-      if constexpr (kBits == mx::kF6)
-        a[u].rest = __builtin_bit_cast(i32x2, __builtin_amdgcn_raw_buffer_load_b64(ra2, offa2 + (k0 + u) * 32, 0, 0));
-      sa[u] = __builtin_amdgcn_raw_buffer_load_b32(rsa, src < 0 ? kGatherOut : offsa + (k0 + u) * a_step, 0, 0);
+    for (int j = 0; j < NT; ++j) {
+      w[j] = *reinterpret_cast<const i32x4*>(at + (16 * j + lr) * 64 + chunk);
+      sw[j] = *reinterpret_cast<const uint32_t*>(mine + S::kBScales + (k / 4 & 1) * (NT * 256) + (16 * j + lr) * 16 + k % 4 * 4);
     }
+    a.first = *reinterpret_cast<const i32x4*>(at + S::kA + lr * 64 + chunk);
+    if constexpr (kBits == mx::kF6) a.rest = *reinterpret_cast<const i32x2*>(at + S::kA2 + lr * 32 + grp * 8);
+    const uint32_t sa = *reinterpret_cast<const uint32_t*>(at + S::kAScales + lr * 4);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage is read: its next loads may land
+    if (k % 4 == 0 && kt + 4 < end) issue_scales(k / 4 + 1);
+    issue(kt + R);
 #pragma unroll
-    for (int u = 0; u < kStreamUnroll; ++u) {
-      if (k0 + u >= end) break;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        acc[j] = mma16<kBits>(w[u][j], a[u], acc[j], static_cast<uint32_t>(sw[j][u]) >> (8 * grp), sa[u] >> (8 * grp));
-    }
+    for (int j = 0; j < NT; ++j) acc[j] = mma16<kBits>(w[j], a, acc[j], sw[j] >> (8 * grp), sa >> (8 * grp));
   }
+  wait_vm<0>();
+  asm volatile("" ::: "memory");
+  f32x4(*const part)[64] = reinterpret_cast<f32x4(*)[64]>(mine);
   if (wave > 0)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) part[wave - 1][j][lane] = acc[j];
+    for (int j = 0; j < NT; ++j) part[j][lane] = acc[j];
   __syncthreads();
   if (wave == 0) {
 #pragma unroll
-    for (int u = 0; u < kStreamWaves - 1; ++u)
+    for (int u = 1; u < kStreamWaves; ++u)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[j] += part[u][j][lane];
+      for (int j = 0; j < NT; ++j) acc[j] += reinterpret_cast<const f32x4(*)[64]>(lds + u * S::kWave)[j][lane];
   }
-  // wave 0's lane (grp, lr) holds row lr's columns 16 c + 4 grp + i
-  const int64_t row = row0 + lr;
-  const int col = nt * kStreamCols;
+  // wave 0's lane (grp, lr) holds row lr's columns 16 j + 4 grp + i
   if constexpr (EPI == kMxSwiGLU || EPI == kMxGELU) {
-    __shared__ float h[kStreamRows][kStreamCols + 1];   // a row's block goes to one lane
+    float(*const h)[kCols + 1] = reinterpret_cast<float(*)[kCols + 1]>(lds);   // a row's block goes to one lane
     if (wave == 0) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           float v;
-          if constexpr (NMAT == 2) v = swiglu_h(acc[c][u], acc[2 + c][u]);
-          else v = gelu_h(acc[c][u]);
+          if constexpr (NMAT == 2) v = swiglu_h(acc[c][u], acc[NC + c][u]);
+          else v = fast_gelu(acc[c][u]);
           h[lr][16 * c + 4 * grp + u] = v;
         }
     }
     __syncthreads();
-    if (threadIdx.x >= n) return;
+    const int r = threadIdx.x % kStreamRows, c = threadIdx.x / kStreamRows;
+    if (r >= n || c >= kCols / mx::kBlock) return;
     float v[32];
 #pragma unroll
-    for (int u = 0; u < 32; ++u) v[u] = h[threadIdx.x][u];
-    store_block<kBits>(mx::encode_block<kBits>(v), row0 + threadIdx.x, g.M, g.N, col, static_cast<uint8_t*>(g.C), g.C2, g.Cs);
+    for (int u = 0; u < 32; ++u) v[u] = h[r][32 * c + u];
+    store_block<kBits>(mx::encode_block<kBits>(v), row0 + r, g.M, n0 / mx::kBlock + c, static_cast<uint8_t*>(g.C), g.C2, g.Cs);
   } else {
     if (wave > 0 || lr >= n) return;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < NT; ++c) {
       const float v[4] = {acc[c][0], acc[c][1], acc[c][2], acc[c][3]};
-      const int64_t at = row * g.N + col + 16 * c + 4 * grp;
+      const int64_t at = (row0 + lr) * g.N + n0 + 16 * c + 4 * grp;
       if constexpr (EPI == kMxBf16) store4(static_cast<uint16_t*>(g.C) + at, v);
       else store4(static_cast<float*>(g.C) + at, v);
     }
@@ -558,19 +648,29 @@ struct MxLayout {
   int cap;
 };
 
-// Rows of a tile.  By the average rows an expert: few rows are bound by the
-// weights' bytes, many by the matrix cores.
-int rows_per_tile(int64_t M, int E) {
+// Rows of a tile, from the rows and the rows an expert has on average, fitted to
+// sweeps over 160 experts of 5120 x 1536, 64 of 2048 x 1408, 16 of 6144 x 10752, 8 of
+// 4096 x 14336 and 32 of 1024 x 4096 (GELU), us a call in 6 bits:
+//   up to 128 rows the stream: 64 rows at 8 experts 177 against 194 in 64-row tiles, 128
+//     rows at 32 experts 35 against 35; at 256 rows and 16 experts 460 against 413.
+//   64-row tiles (two blocks on a CU, so one's fill and epilogue run beside the other's
+//     products) while products are few or K is short: rows * H^2 <= 2^30.  38 rows an
+//     expert at H = 5120 512 against 514 in 128-row tiles; 250 at H = 1024 104 against
+//     129; but 76 at H = 5120 722 against 687.
+//   256-row tiles from 128 rows an expert: at H = 6144 544 against 601 in 128-row tiles.
+int rows_per_tile(int64_t M, int E, int H) {
   const int64_t avg = M / E;
-  return avg <= 16 ? kStreamRows : avg <= 96 ? 64 : avg <= 192 ? 128 : 256;
+  if (M <= 128) return kStreamRows;
+  if (avg * H * H <= (int64_t(1) << 30)) return 64;
+  return avg < 128 ? 128 : 256;
 }
 
 // Whatever E a call gives, the list has room for the smallest tiles.
-MxLayout mx_layout(int64_t n_src, int64_t M, int H, int I, int max_slots, moe_mx_format fmt) {
+MxLayout mx_layout(int64_t M, int H, int I, int max_slots, moe_mx_format fmt) {
   MxLayout w{};
   size_t at = 0;
   auto take = [&](size_t n) { size_t p = at; at = moe::align_up(at + n, 256); return p; };
-  const size_t x_values = static_cast<size_t>(n_src) * H, h_values = static_cast<size_t>(M) * I;
+  const size_t x_values = static_cast<size_t>(M) * H, h_values = static_cast<size_t>(M) * I;
   w.xq = take(x_values / 2);
   w.xq2 = take(fmt == MOE_MX_FP6 ? x_values / 4 : 0);
   w.xs = take(x_values / mx::kBlock);
@@ -584,15 +684,41 @@ MxLayout mx_layout(int64_t n_src, int64_t M, int H, int I, int max_slots, moe_mx
   return w;
 }
 
+// Few rows.  Narrow blocks (32 columns instead of 64) where the wide ones come to fewer
+// than 7 for every 4 CUs: 4096 columns and two experts 16.4 against 23 us; 5120 and six,
+// 480 blocks, 8.9 against 7.8.  Eight waves a block where each CU has one block at most.
+template <int kBits, int EPI>
+int launch_stream(MxGemm p, int64_t row_tiles, hipStream_t s, const char* what) {
+  constexpr int kWide = 64 / mats(EPI);
+  constexpr bool kCanNarrow = EPI == kMxBf16 || EPI == kMxF32 || EPI == kMxGELU;
+  const bool narrow = kCanNarrow && row_tiles * ceil_div(p.N, kWide) < 448;
+  const int cols = narrow ? kWide / 2 : kWide;
+  p.n_col_tiles = p.N / cols;
+  const int64_t blocks = row_tiles * p.n_col_tiles;
+  if (blocks >= (int64_t(1) << 23)) return moe::fail(MOE_ERR_UNSUPPORTED, "moe_mx_expert_ffn: %lld blocks in one launch", (long long)blocks);
+  const unsigned grid = static_cast<unsigned>(blocks);
+  const bool deep = blocks <= 256 && p.K / kStepK >= 16;
+  if constexpr (kCanNarrow) {
+    if (narrow) {
+      if (deep) stream_kernel<kBits, EPI, 2, 8><<<grid, 512, 0, s>>>(p);
+      else stream_kernel<kBits, EPI, 2, 4><<<grid, 256, 0, s>>>(p);
+      return moe::hip_status(hipGetLastError(), what);
+    }
+  }
+  if (deep) stream_kernel<kBits, EPI, 4, 8><<<grid, 512, 0, s>>>(p);
+  else stream_kernel<kBits, EPI, 4, 4><<<grid, 256, 0, s>>>(p);
+  return moe::hip_status(hipGetLastError(), what);
+}
+
 template <int kBits, int EPI>
 int launch_product(MxGemm p, int bm, int64_t row_tiles, hipStream_t s, const char* what) {
-  const int64_t cols = bm == kStreamRows ? kStreamCols : 256 / mats(EPI);
+  if (bm == kStreamRows) return launch_stream<kBits, EPI>(p, row_tiles, s, what);
+  const int64_t cols = 256 / mats(EPI);
   p.n_col_tiles = static_cast<int>(ceil_div(p.N, cols));
   const int64_t blocks = row_tiles * p.n_col_tiles;
   if (blocks >= (int64_t(1) << 24)) return moe::fail(MOE_ERR_UNSUPPORTED, "moe_mx_expert_ffn: %lld blocks in one launch", (long long)blocks);
   const unsigned grid = static_cast<unsigned>(blocks);
-  if (bm == kStreamRows) stream_kernel<kBits, EPI><<<grid, 64 * kStreamWaves, 0, s>>>(p);
-  else if (bm == 64) tile_kernel<kBits, EPI, 64><<<grid, 256, 0, s>>>(p);
+  if (bm == 64) tile_kernel<kBits, EPI, 64><<<grid, 256, 0, s>>>(p);
   else if (bm == 128) tile_kernel<kBits, EPI, 128><<<grid, 256, 0, s>>>(p);
   else tile_kernel<kBits, EPI, 256><<<grid, 256, 0, s>>>(p);
   return moe::hip_status(hipGetLastError(), what);
@@ -609,10 +735,9 @@ int run(MxGemm up, MxGemm down, bool swiglu, bool bf16, int bm, int64_t row_tile
 
 }  // namespace
 
-extern "C" size_t moe_mx_expert_ffn_workspace_bytes(int64_t n_src, int64_t M, int H, int I, int max_slots,
-                                                    moe_mx_format x_format) {
-  if (n_src < 0 || M < 0 || H < 1 || I < 1 || max_slots < 1 || (x_format != MOE_MX_FP4 && x_format != MOE_MX_FP6)) return 0;
-  return mx_layout(n_src, M, H, I, max_slots, x_format).bytes;
+extern "C" size_t moe_mx_expert_ffn_workspace_bytes(int64_t M, int H, int I, int max_slots, moe_mx_format x_format) {
+  if (M < 0 || H < 1 || I < 1 || max_slots < 1 || (x_format != MOE_MX_FP4 && x_format != MOE_MX_FP6)) return 0;
+  return mx_layout(M, H, I, max_slots, x_format).bytes;
 }
 
 extern "C" int moe_mx_expert_ffn(const void* x, const int32_t* row_src, int64_t n_src, moe_dtype dt, int64_t M, int H,
@@ -632,15 +757,10 @@ extern "C" int moe_mx_expert_ffn(const void* x, const int32_t* row_src, int64_t 
   if (n_src < 0) return fail(MOE_ERR_INVALID_ARG, "%s: negative n_src", who);
   if (H < 128 || I < 128 || H % 128 || I % 128)
     return fail(MOE_ERR_UNSUPPORTED, "%s: H and I must be positive multiples of 128 (H=%d I=%d)", who, H, I);
-  // 31-bit offsets: an expert matrix's codes, a tile's rows and the gathered x's, the
-  // scales of all rows
-  const int64_t kLimit = kGatherLimit;
-  if (static_cast<int64_t>(H) * I / 2 >= kLimit || static_cast<int64_t>(std::max(H, I)) * 128 >= kLimit)
-    return fail(MOE_ERR_UNSUPPORTED, "%s: H or I too large for 32-bit tile offsets", who);
-  if ((row_src && n_src * (H / 2) >= kLimit) || n_src * (H / mx::kBlock) >= kLimit || M * (I / mx::kBlock) >= kLimit)
-    return fail(MOE_ERR_UNSUPPORTED, "%s: too many rows for 32-bit offsets (M=%lld, n_src=%lld)", who, (long long)M,
-                (long long)n_src);
-  if (n_src >= (int64_t(1) << 34) / H) return fail(MOE_ERR_UNSUPPORTED, "%s: x holds 2^34 values or more", who);
+  // 31-bit offsets into an expert's codes; a launch's K steps and lanes
+  if (static_cast<int64_t>(H) * I / 2 >= kGatherLimit || H > (1 << 22) || I > (1 << 22))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: H or I too large for 32-bit offsets", who);
+  if (M >= (int64_t(1) << 36) / std::max(H, I)) return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^36 values of x or h", who);
   if (E < 1 || max_slots < E) return fail(MOE_ERR_INVALID_ARG, "%s: need 1 <= E <= max_slots", who);
   if (act == MOE_SWIGLU && (!w_up || !s_up)) return fail(MOE_ERR_INVALID_ARG, "%s: SwiGLU needs w_up", who);
   if (act == MOE_GELU && (w_up || s_up)) return fail(MOE_ERR_INVALID_ARG, "%s: GELU takes no w_up (pass NULL)", who);
@@ -651,7 +771,7 @@ extern "C" int moe_mx_expert_ffn(const void* x, const int32_t* row_src, int64_t 
                         static_cast<const void*>(s_gate), static_cast<const void*>(s_up), static_cast<const void*>(s_down),
                         static_cast<const void*>(y_perm), static_cast<const void*>(workspace)})
     if (p && !aligned16(p)) return fail(MOE_ERR_INVALID_ARG, "%s: operands must be 16-byte aligned", who);
-  const MxLayout w = mx_layout(n_src, M, H, I, max_slots, x_format);
+  const MxLayout w = mx_layout(M, H, I, max_slots, x_format);
   if (workspace_bytes < w.bytes)
     return fail(MOE_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", who, workspace_bytes, w.bytes);
   if (M == 0) return MOE_OK;
@@ -660,12 +780,12 @@ extern "C" int moe_mx_expert_ffn(const void* x, const int32_t* row_src, int64_t 
   auto at = [&](size_t offset) { return reinterpret_cast<uint8_t*>(ws + offset); };
   int4* const tiles = reinterpret_cast<int4*>(ws + w.tiles);
   int32_t* const n_tiles = reinterpret_cast<int32_t*>(ws + w.n_tiles);
-  const int bm = rows_per_tile(M, E);
+  const int bm = rows_per_tile(M, E, H);
   const int64_t row_tiles = M / bm + std::min<int64_t>(M, max_slots);
-  const unsigned grid = static_cast<unsigned>(ceil_div(n_src * (H / mx::kBlock), 256) + 1);
+  const dim3 grid(static_cast<unsigned>(ceil_div(M * 4, 256) + 1), H / kStepK);
   auto prepare = [&](auto kernel) {
-    kernel<<<grid, 256, 0, s>>>(x, n_src, H, at(w.xq), at(w.xq2), at(w.xs), slot_off, slot_expert, n_slots, max_slots, M, E, bm, w.cap, tiles,
-                                n_tiles, check);
+    kernel<<<grid, 256, 0, s>>>(x, row_src, n_src, H, at(w.xq), at(w.xq2), at(w.xs), slot_off, slot_expert, n_slots,
+                                max_slots, M, E, bm, w.cap, tiles, n_tiles, check);
   };
   const bool bf16 = dt == MOE_BF16, fp6 = x_format == MOE_MX_FP6;
   if (bf16) prepare(fp6 ? prepare_kernel<true, mx::kF6> : prepare_kernel<true, mx::kF4>);
@@ -675,8 +795,6 @@ extern "C" int moe_mx_expert_ffn(const void* x, const int32_t* row_src, int64_t 
   up.A = at(w.xq);
   up.A2 = at(w.xq2);
   up.As = at(w.xs);
-  up.a_rows = row_src;
-  up.a_n = n_src;
   up.B0 = w_gate;
   up.B1 = w_up;
   up.S0 = s_gate;
@@ -693,8 +811,6 @@ extern "C" int moe_mx_expert_ffn(const void* x, const int32_t* row_src, int64_t 
   down.A = at(w.hq);
   down.A2 = at(w.hq2);
   down.As = at(w.hs);
-  down.a_rows = nullptr;
-  down.a_n = M;
   down.B0 = w_down;
   down.S0 = s_down;
   down.B1 = down.S1 = nullptr;

@@ -312,7 +312,8 @@ def _assert_ffn(y, xv, rows, table, wts, act, fmt, dtype):
 
 
 CASES = [
-    # counts, H, I: few rows (single ones, 16, 17), both tile paths' edges, columns that do not fill a tile
+    # counts, H, I: few rows (single ones, 16, 17; short and long sums, many columns), the edges of 64-, 128- and
+    # 256-row tiles, odd counts of K steps, columns that do not fill a tile
     ([1], 128, 128),
     ([1, 0, 2, 0], 256, 384),
     ([16, 17, 1, 0, 33], 640, 128),
@@ -320,6 +321,11 @@ CASES = [
     ([130, 128, 1, 120], 512, 384),
     ([300, 256, 511, 0], 128, 640),
     ([257], 1152, 128),
+    ([3, 0, 1], 2176, 2048),
+    ([16] * 8, 2048, 128),
+    ([126, 125, 130, 123], 2944, 384),
+    ([300, 256, 511, 0], 2176, 640),
+    ([257, 300], 2048, 128),
 ]
 
 
@@ -339,11 +345,11 @@ def test_ffn(fmt, act, dtype, counts, H, I):
 
 
 @pytest.mark.parametrize("fmt", X_FORMATS)
-@pytest.mark.parametrize("counts", [[3, 0, 5, 9], [70, 2, 31, 90], [200, 150, 300, 129]])
+@pytest.mark.parametrize("counts", [[3, 0, 5, 9], [70, 2, 31, 90], [60, 100, 70, 50], [200, 150, 300, 129]])
 def test_ffn_gathers_rows(fmt, counts):
     """Rows by a map: repeated, unordered, out of range (zero rows); replica slots and spare slots; y whole."""
-    H, I, E = 256, 256, 2
     M, T = sum(counts), 50
+    H, I, E = 2176 if M > 300 else 384, 256, 2
     x = _rows((T, H), torch.bfloat16, 4)
     src = torch.randint(0, T, (M,), generator=torch.Generator().manual_seed(1)).int()
     src[1], src[M // 2], src[M - 1] = -1, T, 2 ** 31 - 1
@@ -358,8 +364,8 @@ def test_ffn_gathers_rows(fmt, counts):
 @pytest.mark.parametrize("counts", [[5, 4], [60, 50], [150, 120], [260, 270]])
 def test_ffn_rows_stand_alone(fmt, counts):
     """A NaN in x leaves the other rows as they were; a row of zeros gives zeros."""
-    H, I = 256, 128
     M = sum(counts)
+    H, I = 256 if M < 500 else 2176, 128
     wts = (_weights(2, I, H, 1), _weights(2, I, H, 2), _weights(2, H, I, 3))
     x = _rows((M, H), torch.bfloat16, 8)
     x[2] = 0
@@ -411,7 +417,7 @@ def test_ffn_on_streams_and_in_graphs():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     x, y = xs[0].clone(), torch.empty_like(xs[0])
-    ws = torch.empty(moe.moe_mx_expert_ffn_workspace_bytes(M, M, H, I, 3), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(moe.moe_mx_expert_ffn_workspace_bytes(M, H, I, 3), dtype=torch.uint8, device="cuda")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         q, s = moe.moe_mx_quantize(x, "fp8")

@@ -58,10 +58,9 @@ def _combine(d_out=P, dt=1, y=P, ys=P, M=16, inv=P, w=P, T=8, k=2, H=64, d_y=P, 
     (_ffn(rows=P, n_src=-1), -1, "n_src"),
     (_ffn(H=192), -2, "multiples of 128"),
     (_ffn(I=64), -2, "multiples of 128"),
-    (_ffn(H=1 << 16, I=1 << 16), -2, "tile offsets"),
-    (_ffn(H=1 << 24, I=128), -2, "tile offsets"),
-    (_ffn(rows=P, n_src=1 << 26), -2, "rows for 32-bit"),
-    (_ffn(M=1 << 29), -2, "rows for 32-bit"),
+    (_ffn(H=1 << 16, I=1 << 16), -2, "32-bit offsets"),
+    (_ffn(H=1 << 23, I=128), -2, "32-bit offsets"),
+    (_ffn(M=1 << 29), -2, "2\\^36 values"),
     (_ffn(E=0), -1, "E <= max_slots"),
     (_ffn(E=5), -1, "E <= max_slots"),
     (_ffn(wu=N), -1, "w_up"),
@@ -84,14 +83,14 @@ def test_refusals(call, status, msg):
         assert re.search(msg, lib.moe_last_error().decode()), lib.moe_last_error()
 
 
-@pytest.mark.parametrize("n_src,M,H,I,slots", [(0, 0, 128, 128, 1), (1, 6, 5120, 1536, 160), (1024, 2048, 256, 384, 12)])
-def test_workspace_holds_what_the_call_keeps(n_src, M, H, I, slots):
+@pytest.mark.parametrize("M,H,I,slots", [(0, 128, 128, 1), (6, 5120, 1536, 160), (2048, 256, 384, 12)])
+def test_workspace_holds_what_the_call_keeps(M, H, I, slots):
     for fmt, bits in (("fp4", 4), ("fp6", 6)):
-        held = (n_src * H + M * I) * bits // 8 + (n_src * H + M * I) // 32 + 16 * min(M, slots) + 4
-        got = moe.moe_mx_expert_ffn_workspace_bytes(n_src, M, H, I, slots, fmt)
+        held = M * (H + I) * bits // 8 + M * (H + I) // 32 + 16 * min(M, slots) + 4
+        got = moe.moe_mx_expert_ffn_workspace_bytes(M, H, I, slots, fmt)
         assert held <= got <= held + 16 * (M // 16) + 8 * 256
-    assert _native.lib().moe_mx_expert_ffn_workspace_bytes(8, -1, 128, 128, 1, 0) == 0
-    assert _native.lib().moe_mx_expert_ffn_workspace_bytes(8, 8, 128, 128, 1, 1) == 0
+    assert _native.lib().moe_mx_expert_ffn_workspace_bytes(-1, 128, 128, 1, 0) == 0
+    assert _native.lib().moe_mx_expert_ffn_workspace_bytes(8, 128, 128, 1, 1) == 0
 
 
 def test_the_binding_checks_its_arguments():
