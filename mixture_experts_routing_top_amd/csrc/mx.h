@@ -100,53 +100,121 @@ __device__ __forceinline__ void decode8_fp4(uint32_t q, float scale, float (&v)[
   }
 }
 
-// Rows in blocks: lane `tid` of a thread block takes units of eight values, four
-// lanes a block of 32, so a wave reads 1 or 2 KB in a run; the block's largest
-// magnitude is two DPP steps.  A thread block's units are 256 * kUnits in a row of
-// the flat order (row, unit), and a row has 4 * ceil(K / 32) of them.
+// Rows in blocks: a lane takes a unit of V values, 32 / V lanes a block, so that a wave's
+// access to the values is one run of 1 KB (V = 8 bf16, 4 float) and the block's largest
+// magnitude two or three DPP steps.  A thread block's units are 256 * kUnits in a row of
+// the flat order (row, unit).
+//
+// Addresses are a uniform 64-bit row base and 32-bit offsets from it: a block's units lie in
+// two rows where a row has as many units as a block, and in a few thousand values at most
+// otherwise.  (64-bit products for every unit were as long as the rest of the work.)
 template <int kUnits>
 struct Units {
   int64_t row0;
   uint32_t rem, per_row;
+  bool wide;   // rows row0 and row0 + 1 alone
   __device__ __forceinline__ Units(int64_t block, uint32_t units_per_row) : per_row(units_per_row) {
     const int64_t base = block * (256 * kUnits);
     row0 = base / per_row;
     rem = static_cast<uint32_t>(base - row0 * per_row);
+    wide = per_row >= 256 * kUnits;
   }
-  __device__ __forceinline__ void at(int j, int64_t* row, uint32_t* unit) const {
-    const uint32_t v = rem + j * 256 + threadIdx.x, r = v / per_row;
-    *row = row0 + r;
-    *unit = v - r * per_row;
+  // unit j of this thread: in row row0 + r
+  __device__ __forceinline__ void at(int j, uint32_t* r, uint32_t* unit) const {
+    const uint32_t v = rem + j * 256 + threadIdx.x;
+    if (wide) {
+      *r = v >= per_row;
+      *unit = *r ? v - per_row : v;
+    } else {
+      *r = v / per_row;
+      *unit = v - *r * per_row;
+    }
   }
 };
 
-// The scale byte of the block that this lane's eight values are a quarter of (the
-// four lanes together).
-template <int kBits>
-__device__ __forceinline__ uint32_t quad_scale(const float (&v)[8]) {
-  uint32_t m = 0;
+// Two floats to bf16, rounded to nearest even by the conversion instruction.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+
+// V consecutive values from element i on (the last n of a row): 16 bytes, with only the
+// elements' own alignment.
+template <bool kBf16, int V>
+__device__ __forceinline__ void load_values(const void* p, uint32_t i, int n, float (&v)[V]) {
+  if constexpr (V == 8) {
+    rows::unpack8<kBf16>(rows::load8_part<kBf16>(p, i, n), v);
+  } else {
+    const float* q = static_cast<const float*>(p) + i;
+    if (n >= 4) __builtin_memcpy(v, q, 16);
+    else
 #pragma unroll
-  for (int u = 0; u < 8; ++u) m = max(m, __float_as_uint(v[u]) & 0x7fffffffu);
+      for (int u = 0; u < 4; ++u) v[u] = u < n ? q[u] : 0.f;
+  }
+}
+// Stores of whole pieces go past the caches: they are not read again soon.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+template <bool kBf16, int V>
+__device__ __forceinline__ void store_values(void* p, uint32_t i, int n, const float (&v)[V]) {
+  if (n < V) {
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+      if (u < n) rows::store1<kBf16>(p, i + u, v[u]);
+    return;
+  }
+  uint32_t w[kBf16 ? V / 2 : V];
+#pragma unroll
+  for (int u = 0; u < V; ++u) {
+    if constexpr (!kBf16) w[u] = __float_as_uint(v[u]);
+    else if (u % 2 == 0) w[u / 2] = pack_bf16(v[u], v[u + 1]);
+  }
+  u32x4* q = reinterpret_cast<u32x4*>(static_cast<char*>(p) + static_cast<uint64_t>(i) * (kBf16 ? 2 : 4));
+#pragma unroll
+  for (int u = 0; u < (kBf16 ? V / 2 : V); u += 4)
+    __builtin_nontemporal_store((u32x4{w[u], w[u + 1], w[u + 2], w[u + 3]}), q + u / 4);
+}
+
+// The scale byte of the block that this lane's V values are a part of (its lanes together).
+template <int kBits, int V>
+__device__ __forceinline__ uint32_t shared_scale(const float (&v)[V]) {
+  float a = fabsf(v[0]);   // (a NaN stays: IEEE 754-2019 maximum)
+#pragma unroll
+  for (int u = 1; u < V; ++u) a = __builtin_elementwise_maximum(a, fabsf(v[u]));
+  uint32_t m = __float_as_uint(a) & 0x7fffffffu;
   m = max(m, static_cast<uint32_t>(dpp_partner<1>(static_cast<int>(m))));
   m = max(m, static_cast<uint32_t>(dpp_partner<2>(static_cast<int>(m))));
+  if constexpr (V == 4) m = max(m, static_cast<uint32_t>(dpp_partner<4>(static_cast<int>(m))));
   return scale_byte<kBits>(m);
 }
 
-// The codes of eight values, kBits bytes of them.
-template <int kBits>
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], uint32_t byte) {
+// The codes of V values, V * kBits / 8 bytes of them.
+template <int kBits, int V>
+__device__ __forceinline__ uint2 encode(const float (&v)[V], uint32_t byte) {
   if (byte == 255) return make_uint2(0, 0);
   const float s = scale_value(byte);
-  if constexpr (kBits == kF8) return make_uint2(encode4_fp8(v[0], v[1], v[2], v[3], s), encode4_fp8(v[4], v[5], v[6], v[7], s));
-  else if constexpr (kBits == kF6) return encode8_fp6(v, 127 - static_cast<int>(byte));
-  else return make_uint2(encode8_fp4(v, s), 0);
+  if constexpr (V == 4) {
+    static_assert(kBits != kF6, "e2m3 codes of four values end inside a byte");
+    if constexpr (kBits == kF8) return make_uint2(encode4_fp8(v[0], v[1], v[2], v[3], s), 0);
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[0], v[1], s, 0);
+    return make_uint2(__builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[2], v[3], s, 1), 0);
+  } else if constexpr (kBits == kF8) {
+    return make_uint2(encode4_fp8(v[0], v[1], v[2], v[3], s), encode4_fp8(v[4], v[5], v[6], v[7], s));
+  } else if constexpr (kBits == kF6) {
+    return encode8_fp6(v, 127 - static_cast<int>(byte));
+  } else {
+    return make_uint2(encode8_fp4(v, s), 0);
+  }
 }
-template <int kBits>
-__device__ __forceinline__ void decode8(uint2 q, uint32_t byte, float (&v)[8]) {
+template <int kBits, int V>
+__device__ __forceinline__ void decode(uint2 q, uint32_t byte, float (&v)[V]) {
   const float s = scale_value(byte);
-  if constexpr (kBits == kF8) decode8_fp8(q, s, v);
-  else if constexpr (kBits == kF6) decode8_fp6(q, s, v);
-  else decode8_fp4(q.x, s, v);
+  float w[8];
+  if constexpr (kBits == kF8) decode8_fp8(q, s, w);
+  else if constexpr (kBits == kF6) decode8_fp6(q, s, w);
+  else decode8_fp4(q.x, s, w);
+#pragma unroll
+  for (int u = 0; u < V; ++u) v[u] = w[u];
 }
 
 // A whole block in one lane, as an operand of the matrix instructions: 16 bytes of

@@ -4,8 +4,8 @@
 // gradient of the weighted combine, from expert outputs in the dtype or kept in
 // 8-bit blocks.
 //
-// All three are bound by memory: every value is read once and written once, eight
-// values a lane, in accesses that a wave makes to one run of addresses.  mx.h has the format and the split of a row over lanes.
+// All three are bound by memory: every value is read once and written once, 16 bytes
+// of them a lane, in accesses that a wave makes to one run of addresses.  mx.h has the format and the split of a row over lanes.
 #include <type_traits>
 
 #include "common.h"
@@ -17,37 +17,44 @@ namespace {
 using moe::ceil_div;
 using namespace rows;
 
+// Values a lane: 16 bytes, but eight floats where four e2m3 codes would end inside a byte.
+template <bool kBf16, int kBits>
+constexpr int kLane = kBf16 || kBits == mx::kF6 ? 8 : 4;
+
 template <bool kBf16, int kBits, int kUnits>
 __global__ __launch_bounds__(256) void quantize_kernel(const void* __restrict__ x, int64_t R, int K, uint32_t blocks,
                                                        uint8_t* __restrict__ q, uint8_t* __restrict__ scale,
                                                        int32_t* __restrict__ check) {
-  const mx::Units<kUnits> units(blockIdx.x, 4 * blocks);
-  const int64_t row_bytes = mx::code_bytes(kBits, K);
-  Raw8<kBf16> raw[kUnits];
-  int64_t row[kUnits];
-  uint32_t unit[kUnits];
+  constexpr int V = kLane<kBf16, kBits>, P = mx::kBlock / V, kBytes = V * kBits / 8;
+  const mx::Units<kUnits> units(blockIdx.x, P * blocks);
+  const uint32_t row_bytes = static_cast<uint32_t>(mx::code_bytes(kBits, K));
+  const char* const xb = static_cast<const char*>(x) + units.row0 * K * (kBf16 ? 2 : 4);
+  uint8_t* const qb = q + units.row0 * row_bytes;
+  uint8_t* const sb = scale + units.row0 * blocks;
+  const uint32_t rows = static_cast<uint32_t>(min<int64_t>(R - units.row0, 1 << 30));
+  float v[kUnits][V];
+  uint32_t r[kUnits], unit[kUnits];
   int n[kUnits];
 #pragma unroll
   for (int j = 0; j < kUnits; ++j) {
-    units.at(j, &row[j], &unit[j]);
-    n[j] = row[j] < R ? max(0, min(8, K - static_cast<int>(unit[j] * 8))) : 0;
-    raw[j] = Raw8<kBf16>{};
-    if (n[j] > 0) raw[j] = load8_part<kBf16>(x, row[j] * K + unit[j] * 8, n[j]);
+    units.at(j, &r[j], &unit[j]);
+    n[j] = r[j] < rows ? max(0, min(V, K - static_cast<int>(unit[j] * V))) : 0;
+#pragma unroll
+    for (int u = 0; u < V; ++u) v[j][u] = 0.f;
+    if (n[j] > 0) mx::load_values<kBf16, V>(xb, r[j] * K + unit[j] * V, n[j], v[j]);
   }
   bool bad = false;
 #pragma unroll
   for (int j = 0; j < kUnits; ++j) {
-    float v[8];
-    unpack8<kBf16>(raw[j], v);
-    const uint32_t byte = mx::quad_scale<kBits>(v);   // (a block's four lanes are in one row, or past the last)
+    const uint32_t byte = mx::shared_scale<kBits, V>(v[j]);   // (a block's lanes are in one row, or past the last)
     bad |= byte == 255;
-    const uint2 c = mx::encode8<kBits>(v, byte);
-    if (row[j] >= R) continue;
-    if ((unit[j] & 3) == 0) scale[row[j] * blocks + (unit[j] >> 2)] = static_cast<uint8_t>(byte);
-    uint8_t* p = q + row[j] * row_bytes + static_cast<int64_t>(unit[j]) * kBits;
+    const uint2 c = mx::encode<kBits, V>(v[j], byte);
+    if (r[j] >= rows) continue;
+    if (unit[j] % P == 0) sb[r[j] * blocks + unit[j] / P] = static_cast<uint8_t>(byte);
+    uint8_t* const p = qb + (r[j] * row_bytes + unit[j] * kBytes);
     const int bytes = static_cast<int>(mx::code_bytes(kBits, n[j]));
-    if (bytes == kBits) {
-      __builtin_memcpy(p, &c, kBits);
+    if (bytes == kBytes) {
+      __builtin_memcpy(p, &c, kBytes);
     } else {
       for (int u = 0; u < bytes; ++u) p[u] = static_cast<uint8_t>((u < 4 ? c.x : c.y) >> (8 * (u & 3)));
     }
@@ -60,115 +67,126 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* __restri
                                                          int64_t R, int K, uint32_t blocks,
                                                          const int32_t* __restrict__ map, int64_t n_rows,
                                                          void* __restrict__ out, int32_t* __restrict__ check) {
-  const mx::Units<kUnits> units(blockIdx.x, 4 * blocks);
+  constexpr int V = kLane<kBf16, kBits>, P = mx::kBlock / V, kBytes = V * kBits / 8;
+  const mx::Units<kUnits> units(blockIdx.x, P * blocks);
   const int64_t row_bytes = mx::code_bytes(kBits, K);
+  char* const ob = static_cast<char*>(out) + units.row0 * K * (kBf16 ? 2 : 4);
+  const uint32_t rows = static_cast<uint32_t>(min<int64_t>(n_rows - units.row0, 1 << 30));
+  // a wide row's block reads two rows at most, through uniform loads of the map
+  auto source = [&](int64_t row) -> int64_t { return row < n_rows ? (map ? map[row] : row) : -1; };
+  const int64_t src0 = units.wide ? source(units.row0) : 0, src1 = units.wide ? source(units.row0 + 1) : 0;
   uint2 c[kUnits];
-  uint32_t byte[kUnits], unit[kUnits];
-  int64_t row[kUnits];
+  uint32_t byte[kUnits], r[kUnits], unit[kUnits];
+  int64_t src[kUnits];
   int n[kUnits];
   bool bad = false;
 #pragma unroll
   for (int j = 0; j < kUnits; ++j) {
-    units.at(j, &row[j], &unit[j]);
-    n[j] = row[j] < n_rows ? max(0, min(8, K - static_cast<int>(unit[j] * 8))) : 0;
+    units.at(j, &r[j], &unit[j]);
+    n[j] = r[j] < rows ? max(0, min(V, K - static_cast<int>(unit[j] * V))) : 0;
+    src[j] = units.wide ? (r[j] ? src1 : src0) : n[j] > 0 ? source(units.row0 + r[j]) : -1;
+    if (n[j] == 0 || src[j] < 0 || src[j] >= R) src[j] = -1;
+    bad |= n[j] > 0 && src[j] < 0;   // such a row is zero
+  }
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) {
     c[j] = make_uint2(0, 0);
     byte[j] = 127;
-    if (n[j] == 0) continue;
-    const int64_t src = map ? map[row[j]] : row[j];
-    if (src < 0 || src >= R) {   // such a row is zero
-      bad = true;
-      continue;
-    }
-    const uint8_t* p = q + src * row_bytes + static_cast<int64_t>(unit[j]) * kBits;
+    if (src[j] < 0) continue;
+    const uint8_t* const p = q + src[j] * row_bytes + unit[j] * kBytes;
     const int bytes = static_cast<int>(mx::code_bytes(kBits, n[j]));
-    if (bytes == kBits) {
-      __builtin_memcpy(&c[j], p, kBits);
+    if (bytes == kBytes) {
+      __builtin_memcpy(&c[j], p, kBytes);
     } else {
       for (int u = 0; u < bytes; ++u) (u < 4 ? c[j].x : c[j].y) |= static_cast<uint32_t>(p[u]) << (8 * (u & 3));
     }
-    byte[j] = scale[src * blocks + (unit[j] >> 2)];
+    byte[j] = scale[src[j] * blocks + unit[j] / P];
   }
 #pragma unroll
   for (int j = 0; j < kUnits; ++j) {
     if (n[j] == 0) continue;
-    float v[8];
-    mx::decode8<kBits>(c[j], byte[j], v);
-    store8_part<kBf16>(out, row[j] * K + unit[j] * 8, n[j], v);
+    float v[V];
+    mx::decode<kBits, V>(c[j], byte[j], v);
+    mx::store_values<kBf16, V>(ob, r[j] * K + unit[j] * V, n[j], v);
   }
   if (check) raise_check(check, bad, MOE_CHECK_ROWS);
 }
 
 // d_y[inv[t,i]] = w[t,i] d_out[t] and d_w[t,i] = <d_out[t], y[inv[t,i]]>.  kWaves
-// waves a token (kWaves = 1: four tokens a block), eight values of the row and of
-// each of its k expert rows a lane and step.
-template <bool kBf16, bool kKept, int kWaves>
+// waves a token (kWaves = 1: four tokens a block), eight values of the row and of each
+// of its KK expert rows a lane and step, all loads of a step before its sums.
+template <bool kBf16, bool kKept, int kWaves, int KK>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const void* __restrict__ d_out, const void* __restrict__ y,
                                                                const uint8_t* __restrict__ y_scale, int64_t M,
                                                                const int32_t* __restrict__ inv_pos,
-                                                               const float* __restrict__ topk_w, int64_t T, int k,
-                                                               int H, uint32_t blocks, void* __restrict__ d_y,
+                                                               const float* __restrict__ topk_w, int64_t T, int H,
+                                                               uint32_t blocks, void* __restrict__ d_y,
                                                                float* __restrict__ d_topk_w,
                                                                int32_t* __restrict__ check) {
-  __shared__ float part[4][moe::kMaxTopK];
+  __shared__ float part[4][KK];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = kWaves == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + wave : blockIdx.x;
   if (kWaves == 1 && t >= T) return;
-  int64_t at[moe::kMaxTopK];
-  float w[moe::kMaxTopK], acc[moe::kMaxTopK];
+  int64_t at[KK];   // (an entry outside [0, M) reads row 0 and writes nothing)
+  bool there[KK];
+  float w[KK], acc[KK];
   bool bad = false;
 #pragma unroll
-  for (int i = 0; i < moe::kMaxTopK; ++i) {
-    at[i] = -1;
-    w[i] = acc[i] = 0.f;
-    if (i < k) {
-      const int32_t r = inv_pos[t * k + i];
-      if (r >= 0 && r < M) at[i] = r;
-      else bad = true;
-      w[i] = topk_w[t * k + i];
-    }
+  for (int i = 0; i < KK; ++i) {
+    const int32_t r = __builtin_amdgcn_readfirstlane(inv_pos[t * KK + i]);
+    there[i] = r >= 0 && r < M;
+    at[i] = there[i] ? r : 0;
+    bad |= !there[i];
+    w[i] = topk_w[t * KK + i];
+    acc[i] = 0.f;
   }
-  for (int c = (kWaves == 1 ? 0 : wave * 64) + lane; c * 8 < H; c += kWaves * 64) {
-    float o[8];
-    unpack8<kBf16>(load8<kBf16>(d_out, t * H + c * 8), o);
+  const int chunks = M > 0 ? H / 8 : 0;
+  for (int c = (kWaves == 1 ? 0 : wave * 64) + lane; c < chunks; c += kWaves * 64) {
+    const Raw8<kBf16> raw = load8<kBf16>(d_out, t * H + c * 8);
+    uint2 q[KK];
+    uint32_t byte[KK];
+    Raw8<kBf16> yr[KK];
 #pragma unroll
-    for (int i = 0; i < moe::kMaxTopK; ++i) {
-      if (i >= k || at[i] < 0) continue;
-      float v[8], s = 0.f, p[8];
-      float scale = 1.f;
+    for (int i = 0; i < KK; ++i) {
       if constexpr (kKept) {
-        uint2 q;
-        __builtin_memcpy(&q, static_cast<const uint8_t*>(y) + at[i] * H + c * 8, 8);
-        scale = mx::scale_value(y_scale[at[i] * blocks + (c >> 2)]);
-        mx::decode8_fp8(q, 1.f, v);
+        __builtin_memcpy(&q[i], static_cast<const uint8_t*>(y) + at[i] * H + c * 8, 8);
+        byte[i] = y_scale[at[i] * blocks + (c >> 2)];
       } else {
-        unpack8<kBf16>(load8<kBf16>(y, at[i] * H + c * 8), v);
+        yr[i] = load8<kBf16>(y, at[i] * H + c * 8);
       }
+    }
+    float o[8];
+    unpack8<kBf16>(raw, o);
+#pragma unroll
+    for (int i = 0; i < KK; ++i) {
+      float v[8], s = 0.f, p[8];
+      if constexpr (kKept) mx::decode8_fp8(q[i], 1.f, v);
+      else unpack8<kBf16>(yr[i], v);
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         s = fmaf(o[u], v[u], s);
         p[u] = w[i] * o[u];
       }
-      acc[i] = fmaf(s, scale, acc[i]);
-      store8_part<kBf16>(d_y, at[i] * H + c * 8, 8, p);
+      acc[i] = fmaf(s, kKept ? mx::scale_value(byte[i]) : 1.f, acc[i]);
+      if (there[i]) mx::store_values<kBf16, 8>(static_cast<char*>(d_y) + at[i] * H * (kBf16 ? 2 : 4), c * 8, 8, p);
     }
   }
 #pragma unroll
-  for (int i = 0; i < moe::kMaxTopK; ++i) {
-    if (i >= k) break;
-    const float v = wave_sum(acc[i]);
+  for (int i = 0; i < KK; ++i) {
+    const float v = there[i] ? wave_sum(acc[i]) : 0.f;
     if constexpr (kWaves == 1) {
-      if (lane == 0) d_topk_w[t * k + i] = v;
+      if (lane == 0) d_topk_w[t * KK + i] = v;
     } else if (lane == 0) {
       part[wave][i] = v;
     }
   }
   if constexpr (kWaves > 1) {
     __syncthreads();
-    if (threadIdx.x < k) {
+    if (threadIdx.x < KK) {
       float v = part[0][threadIdx.x];
 #pragma unroll
       for (int u = 1; u < kWaves; ++u) v += part[u][threadIdx.x];
-      d_topk_w[t * k + threadIdx.x] = v;
+      d_topk_w[t * KK + threadIdx.x] = v;
     }
   }
   if (check) raise_check(check, bad, MOE_CHECK_ROWS);
@@ -193,7 +211,7 @@ bool many(int64_t units) { return units >= int64_t(256) * 256 * kManyUnits * 4; 
 template <bool kBf16, int kBits>
 void launch_quantize(const void* x, int64_t R, int K, uint8_t* q, uint8_t* scale, int32_t* check, hipStream_t s) {
   const uint32_t blocks = static_cast<uint32_t>(ceil_div(K, mx::kBlock));
-  const int64_t units = R * blocks * 4;
+  const int64_t units = R * blocks * (mx::kBlock / kLane<kBf16, kBits>);
   if (many(units))
     quantize_kernel<kBf16, kBits, kManyUnits><<<static_cast<unsigned>(ceil_div(units, 256 * kManyUnits)), 256, 0, s>>>(
         x, R, K, blocks, q, scale, check);
@@ -206,7 +224,7 @@ template <bool kBf16, int kBits>
 void launch_dequantize(const uint8_t* q, const uint8_t* scale, int64_t R, int K, const int32_t* rows, int64_t n_rows,
                        void* out, int32_t* check, hipStream_t s) {
   const uint32_t blocks = static_cast<uint32_t>(ceil_div(K, mx::kBlock));
-  const int64_t units = n_rows * blocks * 4;
+  const int64_t units = n_rows * blocks * (mx::kBlock / kLane<kBf16, kBits>);
   if (many(units))
     dequantize_kernel<kBf16, kBits, kManyUnits><<<static_cast<unsigned>(ceil_div(units, 256 * kManyUnits)), 256, 0, s>>>(
         q, scale, R, K, blocks, rows, n_rows, out, check);
@@ -215,18 +233,22 @@ void launch_dequantize(const uint8_t* q, const uint8_t* scale, int64_t R, int K,
         q, scale, R, K, blocks, rows, n_rows, out, check);
 }
 
-template <bool kBf16, bool kKept>
+template <bool kBf16, bool kKept, int KK>
 void launch_combine_backward(const void* d_out, const void* y, const uint8_t* y_scale, int64_t M, const int32_t* inv_pos,
                              const float* topk_w, int64_t T, int k, int H, void* d_y, float* d_topk_w, int32_t* check,
                              hipStream_t s) {
+  if constexpr (KK < moe::kMaxTopK)
+    if (k != KK)
+      return launch_combine_backward<kBf16, kKept, KK + 1>(d_out, y, y_scale, M, inv_pos, topk_w, T, k, H, d_y, d_topk_w,
+                                                           check, s);
   const uint32_t blocks = static_cast<uint32_t>(ceil_div(H, mx::kBlock));
   // a wave a token once there are waves for every SIMD; else a block a token
   if (T >= 4096)
-    combine_backward_kernel<kBf16, kKept, 1><<<static_cast<unsigned>(ceil_div(T, 4)), 256, 0, s>>>(
-        d_out, y, y_scale, M, inv_pos, topk_w, T, k, H, blocks, d_y, d_topk_w, check);
+    combine_backward_kernel<kBf16, kKept, 1, KK><<<static_cast<unsigned>(ceil_div(T, 4)), 256, 0, s>>>(
+        d_out, y, y_scale, M, inv_pos, topk_w, T, H, blocks, d_y, d_topk_w, check);
   else
-    combine_backward_kernel<kBf16, kKept, 4><<<static_cast<unsigned>(T), 256, 0, s>>>(
-        d_out, y, y_scale, M, inv_pos, topk_w, T, k, H, blocks, d_y, d_topk_w, check);
+    combine_backward_kernel<kBf16, kKept, 4, KK><<<static_cast<unsigned>(T), 256, 0, s>>>(
+        d_out, y, y_scale, M, inv_pos, topk_w, T, H, blocks, d_y, d_topk_w, check);
 }
 
 }  // namespace
@@ -286,11 +308,11 @@ extern "C" int moe_combine_backward(const void* d_out, moe_dtype dt, const void*
     if (p && !aligned16(p)) return fail(MOE_ERR_INVALID_ARG, "moe_combine_backward: rows must be 16-byte aligned");
   const hipStream_t s = as_stream(stream);
   if (dt == MOE_BF16) {
-    if (y_scale) launch_combine_backward<true, true>(d_out, y, y_scale, M, inv_pos, topk_w, T, k, H, d_y, d_topk_w, check, s);
-    else launch_combine_backward<true, false>(d_out, y, y_scale, M, inv_pos, topk_w, T, k, H, d_y, d_topk_w, check, s);
+    if (y_scale) launch_combine_backward<true, true, 1>(d_out, y, y_scale, M, inv_pos, topk_w, T, k, H, d_y, d_topk_w, check, s);
+    else launch_combine_backward<true, false, 1>(d_out, y, y_scale, M, inv_pos, topk_w, T, k, H, d_y, d_topk_w, check, s);
   } else {
-    if (y_scale) launch_combine_backward<false, true>(d_out, y, y_scale, M, inv_pos, topk_w, T, k, H, d_y, d_topk_w, check, s);
-    else launch_combine_backward<false, false>(d_out, y, y_scale, M, inv_pos, topk_w, T, k, H, d_y, d_topk_w, check, s);
+    if (y_scale) launch_combine_backward<false, true, 1>(d_out, y, y_scale, M, inv_pos, topk_w, T, k, H, d_y, d_topk_w, check, s);
+    else launch_combine_backward<false, false, 1>(d_out, y, y_scale, M, inv_pos, topk_w, T, k, H, d_y, d_topk_w, check, s);
   }
   return hip_status(hipGetLastError(), "moe_combine_backward launch");
 }

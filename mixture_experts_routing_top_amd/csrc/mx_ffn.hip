@@ -485,7 +485,7 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void tile_kernel(const MxGem
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int u = 0; u < D; ++u)
-            d[q][u] = D == 2 ? f32_to_bf16_bits(acc[i][j][4 * q + 2 * u]) | (f32_to_bf16_bits(acc[i][j][4 * q + 2 * u + 1]) << 16)
+            d[q][u] = D == 2 ? mx::pack_bf16(acc[i][j][4 * q + 2 * u], acc[i][j][4 * q + 2 * u + 1])
                              : __float_as_uint(acc[i][j][4 * q + u]);
         uint32_t o[4 * D];   // the halves trade: sixteen adjacent columns each
 #pragma unroll
