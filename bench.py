@@ -67,6 +67,9 @@ def parse():
     ap.add_argument("--train", action="store_true",
                     help="time a training step of the DeepSeek-V2-shaped layer (grouped gate, residual norm, "
                          "backward, clipping) and each of its operators")
+    ap.add_argument("--few-bits", action="store_true",
+                    help="the Mixtral-shaped layer in few bits next to bf16: forward pass on 4-bit weights, and "
+                         "forward and backward pass with activations kept in 8 bits")
     ap.add_argument("--pipeline", action="store_true",
                     help="horizontal-split pipeline and memory kernels on CU-masked streams (Mixtral layer)")
     ap.add_argument("--predict", action="store_true",
@@ -824,6 +827,59 @@ def train_bench(moe, synth, torch, np, steps=5, warmup=2):
                       "operators_ms": {name: timed(fn) for name, fn in parts.items()}}}
 
 
+def few_bits_bench(moe, synth, torch, np, steps=10, warmup=3):
+    """The Mixtral-shaped layer held in few bits, each beside the same layer in bf16 (random
+    values): the forward pass on 4-bit weights (T = 8192, 64 and 1), and a forward and
+    backward pass with x and the outputs kept in 8 bits between the two, with the bytes kept."""
+    cfg = synth.CONFIGS["mixtral"]
+    T, H, I, E, k = cfg.T, cfg.H, cfg.I, cfg.E, cfg.k
+    gen = torch.Generator(device="cuda").manual_seed(0)
+
+    def rnd(*shape, scale=1.0):
+        return torch.randn(shape, generator=gen, device="cuda", dtype=torch.bfloat16).mul_(scale)
+
+    wts = [rnd(E, I, H, scale=H ** -0.5), rnd(E, I, H, scale=H ** -0.5), rnd(E, H, I, scale=I ** -0.5)]
+    packed = [moe.moe_mx_quantize(w, "fp4") for w in wts]
+    x, d_out = rnd(T, H), rnd(T, H, scale=0.1)
+    logits = torch.from_numpy(synth.logits(cfg, 0, 0)).cuda()
+
+    def timed(fn):
+        for _ in range(warmup):
+            fn()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(steps):
+            fn()
+        b.record()
+        torch.cuda.synchronize()
+        return round(a.elapsed_time(b) / steps, 4)
+
+    def held(t):
+        return t.numel() * t.element_size() if hasattr(t, "numel") else sum(held(v) for v in t if v is not None)
+
+    rec = {"workload": f"Mixtral-shaped layer H={H} I={I} E={E} k={k}, bf16 activations",
+           "weights_gb": {"bf16": round(held(wts) / 1e9, 3), "4-bit": round(held(packed) / 1e9, 3)}}
+    for rows in (T, 64, 1):
+        xs, lg, ms = x[:rows].contiguous(), logits[:rows].contiguous(), {}
+        for name, w, kw in (("bf16", wts, {}), ("4-bit, x in 6", packed, dict(x_format="fp6")),
+                            ("4-bit, x in 4", packed, dict(x_format="fp4"))):
+            bufs = {}
+            ms[name] = timed(lambda: moe.moe_layer_forward(xs, lg, k, *w, path="auto", bufs=bufs, **kw))
+        rec[f"forward_ms_T{rows}"] = ms
+    ws = torch.empty(moe.moe_backward_mx_workspace_bytes(torch.bfloat16, T, k, H, I, E), dtype=torch.uint8, device="cuda")
+    for name, kw in (("rows in bf16", dict(copy_rows=True)), ("rows in 8 bits", dict(keep="fp8"))):
+        bufs, f = {}, {}
+
+        def forward():
+            f.update(moe.moe_layer_forward(x, logits, k, *wts, bufs=bufs, **kw))
+
+        fwd = timed(forward)
+        kept = held([f.get(n) for n in ("x_perm", "y_perm", "kept_x", "kept_y") if f.get(n) is not None])
+        rec[name] = {"forward_ms": fwd, "kept_mb": round(kept / 1e6, 1), "backward_ms": timed(
+            lambda: moe.moe_layer_backward(f, logits, *wts, d_out, workspace=ws))}
+    return {"few_bits": rec}
+
+
 def vs_hipblaslt(moe, torch, np, reps=10):
     """The library's GEMMs next to the vendor library on the same dense shapes
     (one expert holding all M = 16384 rows, so no partial tiles): the gate/up GEMM
@@ -917,6 +973,9 @@ def main():
         return
     if a.train:
         print(json.dumps(train_bench(moe, synth, torch, np)), flush=True)
+        return
+    if a.few_bits:
+        print(json.dumps(few_bits_bench(moe, synth, torch, np)), flush=True)
         return
     if a.stats:
         print(json.dumps(stats_bench(moe, synth, torch, np)), flush=True)

@@ -10,7 +10,10 @@
  * moe_stats_load_state (window variants) and moe_backward (the gradients);
  * moe_gate in the place of moe_route (biased, grouped, sigmoid gates),
  * moe_layer_norm after the combine (residual sum and norm), and moe_grad_norm
- * and moe_clip_grads after the backward pass.
+ * and moe_clip_grads after the backward pass; and for a layer held in few bits
+ * moe_mx_quantize, moe_mx_dequantize, moe_mx_expert_ffn (4-bit weights in the place
+ * of moe_expert_ffn), moe_combine_backward and moe_backward_mx (activations kept in
+ * 8 bits).
  *
  * Sources (page title, section):
  *   [PF]   "PopFetcher: Towards Accelerated Mixture-of-Experts Training Via
@@ -77,7 +80,7 @@ enum {
     MOE_CHECK_SLOTS = 32,     /* moe_expert_ffn, moe_mx_expert_ffn: slot table not ascending inside [0, M], n_slots
                                  outside [0, max_slots], or an expert outside [0, E) */
     MOE_CHECK_ROWS = 64,      /* moe_combine, moe_combine_backward: an inv_pos entry outside [0, M);
-                                 moe_mx_dequantize: a row outside [0, R) */
+                                 moe_mx_dequantize: a row outside [0, R); moe_backward_mx: either */
     MOE_CHECK_GRADS = 128,    /* moe_grad_norm, moe_clip_grads: the norm is infinite or NaN */
     MOE_CHECK_BLOCKS = 256    /* moe_mx_quantize, moe_mx_expert_ffn (x): a block with a NaN or an infinity */
 };
@@ -568,6 +571,25 @@ int moe_backward_gated(const void* x_perm, const void* y_perm, moe_dtype dt, int
                        const int32_t* expert_off, const void* w_gate, const void* w_up, const void* w_down,
                        moe_act act, const void* d_out, void* d_x, float* d_topk_w, void* d_w_gate, void* d_w_up,
                        void* d_w_down, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_backward_mx -- moe_backward_gated from activations kept in 8 bits: x by token,
+ * codes [T, H] and x_scale [T, H / 32] of moe_mx_quantize(x, MOE_MX_FP8), and y_perm
+ * by row, codes [M, H] and y_scale [M, H / 32]; perm_src from moe_dispatch (row r is
+ * token perm_src[r]).  The gradients are moe_backward_gated's at the values that the
+ * blocks stand for, x_perm's in `dt`: each is off by at most 2^-4 of itself, or by
+ * 2^-10 of its block's scale where that is more.  The weights stay as they are.  The
+ * workspace holds x_perm too.  With a check word, MOE_CHECK_ROWS for an entry of
+ * perm_src or inv_pos out of range (its row counts as zero).
+ * Limits: those of moe_backward, and T*k*H at most 2^36.
+ */
+size_t moe_backward_mx_workspace_bytes(moe_dtype dt, int64_t T, int k, int H, int I, int E, moe_act act); /* [host] */
+int moe_backward_mx(const uint8_t* x, const uint8_t* x_scale, const uint8_t* y_perm, const uint8_t* y_scale,
+                    moe_dtype dt, int64_t T, int k, int H, int I, int E, const int32_t* perm_src,
+                    const float* topk_w, const int32_t* inv_pos, const int32_t* expert_off, const void* w_gate,
+                    const void* w_up, const void* w_down, moe_act act, const void* d_out, void* d_x,
+                    float* d_topk_w, void* d_w_gate, void* d_w_up, void* d_w_down, void* workspace,
+                    size_t workspace_bytes, int32_t* check, void* stream);
 
 /* --------------------------------------------------------------- layer norm
  * moe_layer_norm -- the residual sum and layer norm that follow a layer:

@@ -20,6 +20,12 @@ scores or weights that are not renormalised.  In training, moe_backward (or
 moe_backward_gated and moe_gate_backward) and moe_layer_norm_backward give the
 gradients, and moe_clip_grads bounds their global norm.
 
+A layer in few bits: moe_mx_quantize gives expert weights in blocks of 32 4-bit
+values with one scale, which moe_mx_expert_ffn multiplies as they are, and
+activations in 8 bits, which moe_backward_mx (and moe_combine_backward) read in the
+place of x_perm and y_perm; moe_mx_dequantize gives the values back.  In
+moe_layer_forward: weights given as pairs (q, scale), and keep="fp8".
+
 Those calls take microseconds on small batches, so their arguments are checked
 and their outputs allocated in a native module (csrc/binding.cpp); the others
 go through ctypes.
@@ -52,7 +58,7 @@ __all__ = ["moe_route", "moe_stats_state_bytes", "moe_stats_init", "moe_stats", 
            "moe_layer_norm_backward_workspace_bytes", "moe_layer_norm_backward", "moe_grad_norm_workspace_bytes",
            "moe_grad_norm", "moe_clip_grads", "moe_layer_backward",
            "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_expert_ffn_workspace_bytes", "moe_mx_expert_ffn",
-           "moe_combine_backward",
+           "moe_combine_backward", "moe_backward_mx_workspace_bytes", "moe_backward_mx",
            "moe_expert_ffn_profiled", "new_check_word", "CHECK_BITS", "moe_dispatch_noalloc",
            "MoEError", "LIB_PATH", "MOE_F32", "MOE_BF16", "SWIGLU", "GELU", "SOFTMAX", "SIGMOID", "GROUP_MAX",
            "GROUP_TOP2", "GEMM_AUTO", "GEMM_GROUPED", "GEMM_DENSE", "GEMM_GROUPED_SMALL",
@@ -529,6 +535,62 @@ def moe_backward_gated(x_perm, y_perm, topk_idx, topk_w, inv_pos, expert_off, w_
                      w_up, w_down, d_out, act, out, workspace, stream)
 
 
+def moe_backward_mx_workspace_bytes(dtype, T: int, k: int, H: int, I: int, E: int, act="swiglu") -> int:
+    code = dtype if isinstance(dtype, int) else (MOE_BF16 if dtype == torch.bfloat16 else MOE_F32)
+    return int(lib().moe_backward_mx_workspace_bytes(code, ctypes.c_int64(T), k, H, I, E, _ACT[act]))
+
+
+def _kept(pair, shape, dev, name):
+    """The (q, scale) of rows kept in 8 bits, checked against [rows, H]."""
+    if not isinstance(pair, (tuple, list)) or len(pair) != 2 or any(t is None for t in pair):
+        raise ValueError(f"{name}: expected the pair (q, scale) that moe_mx_quantize(..., 'fp8') gives")
+    return (_out(pair[0], shape, torch.uint8, dev, name),
+            _out(pair[1], (shape[0], -(-shape[1] // 32)), torch.uint8, dev, f"{name}'s scale"))
+
+
+def moe_backward_mx(x, y_perm, perm_src, topk_w, inv_pos, expert_off, w_gate, w_up, w_down, d_out, act="swiglu",
+                    out=None, workspace=None, stream=None, check=None):
+    """moe_backward_gated from activations kept in 8 bits: x by token and y_perm by row,
+    each the pair (q, scale) of moe_mx_quantize(..., "fp8"); perm_src, inv_pos and
+    expert_off from moe_dispatch (copy=False serves).  dict(d_x, d_topk_w, d_w_gate,
+    d_w_up, d_w_down), in d_out's dtype, which the weights have too."""
+    T, H = d_out.shape
+    k = topk_w.shape[1]
+    E, I, _ = w_gate.shape
+    M, dt, dev = T * k, d_out.dtype, d_out.device
+    code, act_code = _dtype_code(d_out), _ACT[act]
+    x, y_perm = _kept(x, (T, H), dev, "x"), _kept(y_perm, (M, H), dev, "y_perm")
+    given = [("perm_src", perm_src, (M,), torch.int32), ("topk_w", topk_w, (T, k), torch.float32),
+             ("inv_pos", inv_pos, (T, k), torch.int32), ("expert_off", expert_off, (E + 1,), torch.int32),
+             ("w_gate", w_gate, (E, I, H), dt), ("w_down", w_down, (E, H, I), dt)]
+    if w_up is not None:
+        given.append(("w_up", w_up, (E, I, H), dt))
+    for name, t, shape, dtype in given:
+        if t is None:
+            raise ValueError(f"{name}: missing")
+        _out(t, shape, dtype, dev, name)
+    if check is not None:
+        _out(check, (1,), torch.int32, dev, "check")
+    o = dict(out or {})
+    need = moe_backward_mx_workspace_bytes(dt, T, k, H, I, E, act)
+    shapes = {"d_x": ((T, H), dt), "d_topk_w": ((T, k), torch.float32), "d_w_gate": ((E, I, H), dt),
+              "d_w_up": ((E, I, H), dt), "d_w_down": ((E, H, I), dt)}
+    if w_up is None:
+        del shapes["d_w_up"]
+    with _on(stream, dev):
+        for name, (shape, dtype) in shapes.items():
+            o[name] = _out(o.get(name), shape, dtype, dev, name)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else \
+            _bytes_of(workspace, need, "backward workspace")
+    with torch.cuda.device(dev) if dev.type == "cuda" else contextlib.nullcontext():
+        _call("moe_backward_mx", _ptr(x[0]), _ptr(x[1]), _ptr(y_perm[0]), _ptr(y_perm[1]), code, ctypes.c_int64(T), k, H,
+              I, E, _ptr(perm_src), _ptr(topk_w), _ptr(inv_pos), _ptr(expert_off), _ptr(w_gate), _ptr(w_up),
+              _ptr(w_down), act_code, _ptr(d_out), _ptr(o["d_x"]), _ptr(o["d_topk_w"]), _ptr(o["d_w_gate"]),
+              _ptr(o.get("d_w_up")), _ptr(o["d_w_down"]), _ptr(workspace),
+              ctypes.c_size_t(workspace.numel() * workspace.element_size()), _ptr(check), _stream(stream))
+    return o
+
+
 # --------------------------------------------------------------- layer norm
 def moe_layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, residual=None, y=None, x_sum=None,
                    stream=None):
@@ -597,7 +659,7 @@ def _norm_formula(norm):
 def moe_layer_forward(x, logits, k, w_gate, w_up, w_down, act="swiglu", replica_budget=0, stats_state=None,
                       stats_dims=None, layer=0, it=0, prev_topk_idx=None, path="grouped", bufs=None, stream=None,
                       planned_replicas=None, check=None, ffn_events=None, copy_rows=False, gate=None, residual=None,
-                      norm=None):
+                      norm=None, keep=None, x_format=None):
     """route -> stats -> dispatch -> FFN -> combine, all on `stream`.
 
     The dispatch writes the row map and the slot table but copies no rows: the
@@ -625,16 +687,36 @@ def moe_layer_forward(x, logits, k, w_gate, w_up, w_down, act="swiglu", replica_
     `x_sum`.  With shared `bufs` the next call writes over this one's result: a
     layer whose backward pass is to follow needs bufs of its own until then.
     The result also records the gate's and the norm's formulas, which
-    moe_layer_backward compares."""
+    moe_layer_backward compares.
+
+    Weights given as the pairs (q, scale) of moe_mx_quantize(w, "fp4") go through
+    moe_mx_expert_ffn (x_format: "fp6" unless given, or "fp4"); such a layer has no
+    backward pass.  keep="fp8": the result holds kept_x (by token) and kept_y (by
+    row), the pairs (q, scale) from which moe_layer_backward runs moe_backward_mx, and
+    no x_perm or y_perm.  All that the backward pass reads is then allocated anew by
+    this call, and the layers may share `bufs`."""
     T, E = logits.shape
     H = x.shape[1]
-    I = w_gate.shape[1]
+    quantised = isinstance(w_gate, (tuple, list))
+    if quantised:
+        if keep is not None:
+            raise ValueError("keep: a layer on 4-bit weights has no backward pass")
+        if ffn_events is not None or path not in ("grouped", "auto", GEMM_GROUPED, GEMM_AUTO):
+            raise ValueError("4-bit weights: no ffn_events, and no path but the grouped one")
+        x_format = "fp6" if x_format is None else x_format
+    elif x_format is not None:
+        raise ValueError("x_format: the weights are not quantised")
+    if keep not in (None, "fp8", MX_FP8):
+        raise ValueError(f"keep: rows are kept in 'fp8', not {keep!r}")
+    if keep is not None and copy_rows:
+        raise ValueError("copy_rows keeps the rows in their dtype and keep in 8 bits: give one")
+    I = w_gate[0].shape[1] if quantised else w_gate.shape[1]
     dev = x.device
     if residual is not None and norm is None:
         raise ValueError("residual: the sum is taken before a norm (pass norm)")
     max_slots = E + replica_budget
     b = bufs if bufs is not None else {}
-    key = (T, k, E, H, I, max_slots, x.dtype, str(dev), copy_rows)
+    key = (T, k, E, H, I, max_slots, x.dtype, str(dev), copy_rows, x_format, keep)
     if b.get("_key") != key:
         b.clear()
         b["_key"] = key
@@ -643,18 +725,20 @@ def moe_layer_forward(x, logits, k, w_gate, w_up, w_down, act="swiglu", replica_
         names += ["counts", "p_seq", "replicas"] + (["cond", "pred_next"] if layer + 1 < stats_dims[0] else [])
     if any(name not in b for name in names):
         sizes = {"ws_d": (moe_dispatch_workspace_bytes(T, k, E), torch.uint8), "y_perm": ((T * k, H), x.dtype),
-                 "ws_f": (moe_expert_ffn_workspace_bytes(x.dtype, T * k, H, I, max_slots), torch.uint8),
+                 "ws_f": (moe_mx_expert_ffn_workspace_bytes(T * k, H, I, max_slots, x_format) if quantised else
+                          moe_expert_ffn_workspace_bytes(x.dtype, T * k, H, I, max_slots), torch.uint8),
                  "counts": (E, torch.int32), "p_seq": (E, torch.float32), "replicas": (E, torch.int32),
                  "cond": ((E, E), torch.float32), "pred_next": (E, torch.float32)}
         with _on(stream, dev):
             for name in names:
                 if name not in b:
                     b[name] = torch.empty(sizes[name][0], dtype=sizes[name][1], device=dev)
+    o = b if keep is None else {}   # what a backward pass reads: with keep, this call's own
     if gate is None:
-        idx, w = moe_route(logits, k, b.get("idx"), b.get("w"), stream, check)
+        idx, w = moe_route(logits, k, o.get("idx"), o.get("w"), stream, check)
     else:
-        idx, w = moe_gate(logits, k, topk_idx=b.get("idx"), topk_w=b.get("w"), stream=stream, check=check, **gate)
-    b["idx"], b["w"] = idx, w
+        idx, w = moe_gate(logits, k, topk_idx=o.get("idx"), topk_w=o.get("w"), stream=stream, check=check, **gate)
+    o["idx"], o["w"] = idx, w
     res = {"idx": idx, "w": w, "gate_formula": _gate_formula(gate), "norm_formula": _norm_formula(norm)}
     replicas, counts = None, None
     if stats_state is not None:
@@ -669,36 +753,48 @@ def moe_layer_forward(x, logits, k, w_gate, w_up, w_down, act="swiglu", replica_
     if planned_replicas is not None:
         replicas = planned_replicas
         res["replicas"] = planned_replicas
-    d = moe_dispatch(x, idx, E, replicas, max_slots, b.get("disp"), b["ws_d"], stream, counts, check,
+    d = moe_dispatch(x, idx, E, replicas, max_slots, o.get("disp"), b["ws_d"], stream, counts, check,
                      replica_budget=replica_budget if replicas is None else 0, copy=copy_rows)
-    b["disp"] = d
+    o["disp"] = d
     ffn_in, row_src = (d["x_perm"], None) if copy_rows else (x, d["perm_src"])
-    if ffn_events is None:
+    if quantised:
+        y = moe_mx_expert_ffn(ffn_in, d["slot_off"], d["slot_expert"], d["n_slots"], w_gate, w_up, w_down, act,
+                              x_format, b["y_perm"], b["ws_f"], stream, check, row_src=row_src)
+    elif ffn_events is None:
         y = moe_expert_ffn(ffn_in, d["slot_off"], d["slot_expert"], d["n_slots"], w_gate, w_up, w_down, act,
                            path, b["y_perm"], b["ws_f"], stream, check, row_src=row_src)
     else:
         y = moe_expert_ffn_profiled(ffn_in, d["slot_off"], d["slot_expert"], d["n_slots"], w_gate, w_up, w_down,
                                     ffn_events, act, path, b["y_perm"], b["ws_f"], stream, check, row_src=row_src)
-    if residual is not None and "out" in b and residual.data_ptr() == b["out"].data_ptr():
-        del b["out"]   # the last layer's output is still to be read: the combine writes another
-    out = moe_combine(y, d["inv_pos"], w, b.get("out"), stream, check)
-    b["out"] = out
+    if residual is not None and "out" in o and residual.data_ptr() == o["out"].data_ptr():
+        del o["out"]   # the last layer's output is still to be read: the combine writes another
+    out = moe_combine(y, d["inv_pos"], w, o.get("out"), stream, check)
+    o["out"] = out
     res.update(d)
-    res.update(y_perm=y, out=out)
+    res["out"] = out
+    if keep is None:
+        res["y_perm"] = y
+    else:
+        res.update(kept_x=moe_mx_quantize(x, "fp8", stream=stream, check=check),
+                   kept_y=moe_mx_quantize(y, "fp8", stream=stream, check=check))
+    if quantised:
+        res["x_format"] = x_format
     if norm is not None:
-        b["normed"], x_sum = moe_layer_norm(out, residual=residual, y=b.get("normed"),
-                                            x_sum=b.get("x_sum") if residual is not None else None, stream=stream,
+        o["normed"], x_sum = moe_layer_norm(out, residual=residual, y=o.get("normed"),
+                                            x_sum=o.get("x_sum") if residual is not None else None, stream=stream,
                                             **norm)
-        res.update(normed=b["normed"], x_sum=x_sum)
+        res.update(normed=o["normed"], x_sum=x_sum)
         if x_sum is not None:
-            b["x_sum"] = x_sum
+            o["x_sum"] = x_sum
     return res
 
 
 def moe_layer_backward(fwd, logits, w_gate, w_up, w_down, d_out, act="swiglu", gate=None, norm=None, d_x_sum=None,
                        max_norm=None, eps: float = 1e-6, workspace=None, stream=None, check=None):
-    """The backward pass of moe_layer_forward(copy_rows=True), whose result is `fwd`:
-    norm -> combine, experts and dispatch -> gate.
+    """The backward pass of moe_layer_forward(copy_rows=True) or (keep="fp8"), whose
+    result is `fwd`: norm -> combine, experts and dispatch -> gate.  From rows kept in
+    8 bits it gives the gradients at the values that those stand for
+    (moe_backward_mx), in less than half the memory between the passes.
 
     d_out is the gradient of fwd["normed"] where the layer had a norm (pass the
     same `norm` and `gate` dicts: another score, renorm, scale, eps or a missing
@@ -710,8 +806,11 @@ def moe_layer_backward(fwd, logits, w_gate, w_up, w_down, d_out, act="swiglu", g
     residual, d_residual (the same tensor; d_x does not hold it).  max_norm: the
     weights' gradients (experts and norm) are clipped in place to that global norm,
     and the result holds grad_norm."""
-    if fwd.get("x_perm") is None:
-        raise ValueError("the forward pass must keep its rows: moe_layer_forward(copy_rows=True)")
+    if "x_format" in fwd or isinstance(w_gate, (tuple, list)):
+        raise ValueError("a layer on 4-bit weights has no backward pass")
+    kept = "kept_x" in fwd
+    if not kept and fwd.get("x_perm") is None:
+        raise ValueError("the forward pass must keep its rows: moe_layer_forward(copy_rows=True) or keep='fp8'")
     if norm is not None and "normed" not in fwd:
         raise ValueError("norm: the forward pass ran without a norm")
     for name, given, formula in (("gate", gate, _gate_formula), ("norm", norm, _norm_formula)):
@@ -730,10 +829,15 @@ def moe_layer_backward(fwd, logits, w_gate, w_up, w_down, d_out, act="swiglu", g
     elif d_x_sum is not None:
         raise ValueError("d_x_sum: the layer had no norm")
     run = moe_backward if gate is None else moe_backward_gated
-    res.update(run(fwd["x_perm"], fwd["y_perm"], fwd["idx"], fwd["w"], fwd["inv_pos"], fwd["expert_off"], w_gate, w_up,
-                   w_down, d_out, act, workspace=workspace, stream=stream))
-    if gate is not None:
-        opts = {key: gate[key] for key in ("score", "renorm", "scale") if key in gate}
+    if kept:
+        res.update(moe_backward_mx(fwd["kept_x"], fwd["kept_y"], fwd["perm_src"], fwd["w"], fwd["inv_pos"],
+                                   fwd["expert_off"], w_gate, w_up, w_down, d_out, act, workspace=workspace,
+                                   stream=stream, check=check))
+    else:
+        res.update(run(fwd["x_perm"], fwd["y_perm"], fwd["idx"], fwd["w"], fwd["inv_pos"], fwd["expert_off"], w_gate,
+                       w_up, w_down, d_out, act, workspace=workspace, stream=stream))
+    if gate is not None or kept:   # (moe_route is the softmax gate with renormalised weights)
+        opts = {key: gate[key] for key in ("score", "renorm", "scale") if key in gate} if gate is not None else {}
         res["d_logits"] = moe_gate_backward(logits, fwd["idx"], res["d_topk_w"], stream=stream, check=check, **opts)
     if max_norm is not None:
         names = ("d_w_gate", "d_w_up", "d_w_down", "d_weight", "d_bias")
@@ -760,6 +864,8 @@ def moe_layer_forward_pipelined(x, logits, k, w_gate, w_up, w_down, act="swiglu"
     layer at the end; `bufs` caches the per-chunk buffers between calls."""
     T, E = logits.shape
     H = x.shape[1]
+    if isinstance(w_gate, (tuple, list)):
+        raise ValueError("4-bit weights: moe_layer_forward takes them (a chunk's rows may be tiled, and rounded, otherwise)")
     I = w_gate.shape[1]
     dev = x.device
     cs = compute_stream if compute_stream is not None else torch.cuda.current_stream()

@@ -35,6 +35,9 @@ SIGNATURES = {
                           _p, _sz, _p]),
     "moe_backward_gated": (_i, [_p, _p, _i, _i64, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _i, _p, _p, _p, _p, _p,
                                 _p, _p, _sz, _p]),
+    "moe_backward_mx_workspace_bytes": (_sz, [_i, _i64, _i, _i, _i, _i, _i]),
+    "moe_backward_mx": (_i, [_p, _p, _p, _p, _i, _i64, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _i, _p, _p, _p, _p,
+                             _p, _p, _p, _sz, _p, _p]),
     "moe_gate": (_i, [_p, _i, _i64, _i, _i, _i, _p, _i, _i, _i, _i, _f, _p, _p, _p, _p]),
     "moe_gate_backward": (_i, [_p, _i, _i64, _i, _i, _i, _i, _f, _p, _p, _p, _p, _p]),
     "moe_layer_norm": (_i, [_p, _p, _i, _i64, _i, _p, _p, _i, _f, _p, _p, _p]),

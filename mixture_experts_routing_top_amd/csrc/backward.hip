@@ -30,6 +30,12 @@
 // tiles take K-contiguous operands only, so for fp32 the weights are
 // transposed first and the activations transposed into per-expert K ranges
 // padded to the K step.
+//
+// moe_backward_mx: the same from x kept by token and y kept by row in 8-bit blocks.
+// x_perm comes back into the workspace through the row map, and step 1 is
+// moe_combine_backward, which decodes y as it reads it; the rest is unchanged.  A layer
+// then keeps T H (1 + k) 33/32 bytes from its forward to its backward pass, where x_perm
+// and y_perm in bf16 are T k H 4 (8192 tokens, k = 2, H = 4096: 99 MiB for 256).
 #include <algorithm>
 
 #include "common.h"
@@ -274,8 +280,18 @@ BwdLayout bwd_layout(moe_dtype dt, int64_t T, int k, int H, int I, int E, moe_ac
   return w;
 }
 
+// What moe_backward_mx has in the place of x_perm and y_perm.
+struct Kept {
+  const uint8_t *x, *x_scale, *y, *y_scale;
+  const int32_t* perm_src;
+  int32_t* check;
+};
+
+// x_perm's place in moe_backward_mx's workspace, behind moe_backward's.
+size_t kept_rows_at(const BwdLayout& L) { return moe::align_up(L.bytes, 256); }
+
 template <bool kBf16>
-int run_backward(const void* x_perm, const void* y_perm, int64_t n_tok, int k, int H, int I, int E,
+int run_backward(const Kept* kept, const void* x_perm, const void* y_perm, int64_t n_tok, int k, int H, int I, int E,
                  const int32_t* topk_idx, const float* topk_w, const int32_t* inv_pos, const int32_t* expert_off,
                  const void* w_gate, const void* w_up, const void* w_down, bool swiglu, const void* d_out,
                  void* d_x, float* d_logits, float* d_topk_w, void* d_w_gate, void* d_w_up, void* d_w_down, char* ws,
@@ -312,7 +328,16 @@ int run_backward(const void* x_perm, const void* y_perm, int64_t n_tok, int k, i
 
   // 1. gate + combine transpose
   const int chunks = static_cast<int>(static_cast<int64_t>(H) * S / 16);
-  if (n_tok > 0)
+  if (kept) {
+    constexpr moe_dtype kDt = kBf16 ? MOE_BF16 : MOE_F32;
+    x_perm = at(kept_rows_at(L));
+    if (int rc = moe_mx_dequantize(kept->x, kept->x_scale, MOE_MX_FP8, n_tok, H, kept->perm_src, M, kDt,
+                                   at(kept_rows_at(L)), kept->check, s))
+      return rc;
+    if (int rc = moe_combine_backward(d_out, kDt, kept->y, kept->y_scale, M, inv_pos, topk_w, n_tok, k, H, dy, d_topk_w,
+                                      kept->check, s))
+      return rc;
+  } else if (n_tok > 0)
     gate_backward_kernel<kBf16><<<static_cast<unsigned>(n_tok), kTok, 0, s>>>(
         static_cast<const uint4*>(d_out), static_cast<const uint4*>(y_perm), M, topk_idx, topk_w, inv_pos, k, E,
         chunks, reinterpret_cast<uint4*>(dy), d_logits, d_topk_w);
@@ -463,7 +488,7 @@ extern "C" size_t moe_backward_workspace_bytes(moe_dtype dt, int64_t T, int k, i
 
 namespace {
 
-int backward(const char* who, const void* x_perm, const void* y_perm, moe_dtype dt, int64_t T, int k, int H, int I,
+int backward(const char* who, const Kept* kept, const void* x_perm, const void* y_perm, moe_dtype dt, int64_t T, int k, int H, int I,
                             int E, const int32_t* topk_idx, const float* topk_w, const int32_t* inv_pos,
                             const int32_t* expert_off, const void* w_gate, const void* w_up, const void* w_down,
                             moe_act act, const void* d_out, void* d_x, float* d_logits, float* d_topk_w, void* d_w_gate,
@@ -497,20 +522,26 @@ int backward(const char* who, const void* x_perm, const void* y_perm, moe_dtype 
   if (act == MOE_GELU && (w_up || d_w_up)) return fail(MOE_ERR_INVALID_ARG, "%s: GELU takes no w_up/d_w_up", who);
   if (!expert_off || !w_gate || !w_down || !d_w_gate || !d_w_down || !workspace || (act == MOE_SWIGLU && !d_w_up))
     return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
-  if (T > 0 && (!x_perm || !y_perm || !topk_idx || !topk_w || !inv_pos || !d_out || !d_x ||
-                !(d_logits || d_topk_w)))
+  if (T > 0 && (kept ? !kept->x || !kept->x_scale || !kept->y || !kept->y_scale || !kept->perm_src
+                     : !x_perm || !y_perm || !topk_idx))
     return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (T > 0 && (!topk_w || !inv_pos || !d_out || !d_x || !(d_logits || d_topk_w)))
+    return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (kept && T * k > (int64_t(1) << 31) / (H / 32))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^31 blocks of 32 values", who);
   const void* ptrs[] = {x_perm, y_perm, w_gate, w_up, w_down, d_out, d_x, d_w_gate, d_w_up, d_w_down, workspace};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return fail(MOE_ERR_INVALID_ARG, "%s: operands must be 16-byte aligned", who);
-  if (workspace_bytes < L.bytes)
-    return fail(MOE_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", who, workspace_bytes, L.bytes);
+  if (kept && kept->y && !aligned16(kept->y)) return fail(MOE_ERR_INVALID_ARG, "%s: operands must be 16-byte aligned", who);
+  const size_t need = kept ? kept_rows_at(L) + static_cast<size_t>(T * k) * H * elem_bytes(dt) : L.bytes;
+  if (workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", who, workspace_bytes, need);
   const hipStream_t s = as_stream(stream);
   char* ws = static_cast<char*>(workspace);
   return dt == MOE_BF16
-             ? run_backward<true>(x_perm, y_perm, T, k, H, I, E, topk_idx, topk_w, inv_pos, expert_off, w_gate, w_up,
+             ? run_backward<true>(kept, x_perm, y_perm, T, k, H, I, E, topk_idx, topk_w, inv_pos, expert_off, w_gate, w_up,
                                   w_down, act == MOE_SWIGLU, d_out, d_x, d_logits, d_topk_w, d_w_gate, d_w_up, d_w_down, ws, L, s)
-             : run_backward<false>(x_perm, y_perm, T, k, H, I, E, topk_idx, topk_w, inv_pos, expert_off, w_gate,
+             : run_backward<false>(kept, x_perm, y_perm, T, k, H, I, E, topk_idx, topk_w, inv_pos, expert_off, w_gate,
                                    w_up, w_down, act == MOE_SWIGLU, d_out, d_x, d_logits, d_topk_w, d_w_gate, d_w_up, d_w_down,
                                    ws, L, s);
 }
@@ -522,7 +553,7 @@ extern "C" int moe_backward(const void* x_perm, const void* y_perm, moe_dtype dt
                             const int32_t* expert_off, const void* w_gate, const void* w_up, const void* w_down,
                             moe_act act, const void* d_out, void* d_x, float* d_logits, void* d_w_gate,
                             void* d_w_up, void* d_w_down, void* workspace, size_t workspace_bytes, void* stream) {
-  return backward("moe_backward", x_perm, y_perm, dt, T, k, H, I, E, topk_idx, topk_w, inv_pos, expert_off, w_gate,
+  return backward("moe_backward", nullptr, x_perm, y_perm, dt, T, k, H, I, E, topk_idx, topk_w, inv_pos, expert_off, w_gate,
                   w_up, w_down, act, d_out, d_x, d_logits, nullptr, d_w_gate, d_w_up, d_w_down, workspace,
                   workspace_bytes, stream);
 }
@@ -533,7 +564,24 @@ extern "C" int moe_backward_gated(const void* x_perm, const void* y_perm, moe_dt
                                   const void* w_down, moe_act act, const void* d_out, void* d_x, float* d_topk_w,
                                   void* d_w_gate, void* d_w_up, void* d_w_down, void* workspace,
                                   size_t workspace_bytes, void* stream) {
-  return backward("moe_backward_gated", x_perm, y_perm, dt, T, k, H, I, E, topk_idx, topk_w, inv_pos, expert_off,
+  return backward("moe_backward_gated", nullptr, x_perm, y_perm, dt, T, k, H, I, E, topk_idx, topk_w, inv_pos, expert_off,
+                  w_gate, w_up, w_down, act, d_out, d_x, nullptr, d_topk_w, d_w_gate, d_w_up, d_w_down, workspace,
+                  workspace_bytes, stream);
+}
+
+extern "C" size_t moe_backward_mx_workspace_bytes(moe_dtype dt, int64_t T, int k, int H, int I, int E, moe_act act) {
+  if (T < 0 || k < 1 || H < 1 || I < 1 || E < 1 || (dt != MOE_F32 && dt != MOE_BF16)) return 0;
+  return kept_rows_at(bwd_layout(dt, T, k, H, I, E, act)) + static_cast<size_t>(T * k) * H * moe::elem_bytes(dt);
+}
+
+extern "C" int moe_backward_mx(const uint8_t* x, const uint8_t* x_scale, const uint8_t* y_perm, const uint8_t* y_scale,
+                               moe_dtype dt, int64_t T, int k, int H, int I, int E, const int32_t* perm_src,
+                               const float* topk_w, const int32_t* inv_pos, const int32_t* expert_off,
+                               const void* w_gate, const void* w_up, const void* w_down, moe_act act,
+                               const void* d_out, void* d_x, float* d_topk_w, void* d_w_gate, void* d_w_up,
+                               void* d_w_down, void* workspace, size_t workspace_bytes, int32_t* check, void* stream) {
+  const Kept kept{x, x_scale, y_perm, y_scale, perm_src, check};
+  return backward("moe_backward_mx", &kept, nullptr, nullptr, dt, T, k, H, I, E, nullptr, topk_w, inv_pos, expert_off,
                   w_gate, w_up, w_down, act, d_out, d_x, nullptr, d_topk_w, d_w_gate, d_w_up, d_w_down, workspace,
                   workspace_bytes, stream);
 }

@@ -58,7 +58,7 @@ extern "C" int moe_check_device_error(const int32_t* check, int32_t* bits, void*
       {MOE_CHECK_COUNTS, "counts differ from the routing"},
       {MOE_CHECK_REPLICAS, "negative replica count or copies beyond max_slots"},
       {MOE_CHECK_SLOTS, "invalid slot table"},
-      {MOE_CHECK_ROWS, "inv_pos entry outside [0, M)"},
+      {MOE_CHECK_ROWS, "inv_pos entry outside [0, M), or a row outside [0, R)"},
       {MOE_CHECK_GRADS, "non-finite gradient norm"},
       {MOE_CHECK_BLOCKS, "non-finite values in a quantised block"},
   };
