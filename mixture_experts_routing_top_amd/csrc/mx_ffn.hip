@@ -12,7 +12,7 @@
 //             adjacent columns of a row, quantises them in registers and writes
 //             their codes;
 //   down:     y = Q(h) Wd^T.
-// Two kernels multiply.  tile_kernel: BM rows x 256 weight rows a block, operands
+// Two kernels multiply.  tile_kernel: BM rows x 128 or 256 weight rows a block, operands
 // straight into LDS, 32x32x64 instructions.  stream_kernel: at most 16 rows by 64
 // weight rows a block, K split over the block's waves: for few rows the time is the
 // weights' bytes.
@@ -221,18 +221,22 @@ enum MxEpi { kMxSwiGLU = 0, kMxGELU = 1, kMxBf16 = 2, kMxF32 = 3 };
 constexpr int mats(int epi) { return epi == kMxSwiGLU ? 2 : 1; }
 
 // ---- large batches ---------------------------------------------------------------
-// LDS: three stages of A (a K step of 128: two planes and the scales), stages of the
-// weights' codes of kBStep K values, and two buffers of the weights' scales for 512.
-// 256-row tiles take the weights 256 K values at a time: whole 128-byte lines of a
-// weight row.  64- and 128-row tiles take 128, and 64-row tiles fit twice on a CU.
+// A block: BM rows by BN weight rows.  LDS: stages of A (a K step of 128: two planes and
+// the scales), stages of the weights' codes, 256 K values each, and two buffers of the
+// weights' scales for 512.
+// 256 K values are whole 128-byte lines of a weight row: 64-byte pieces a step apart
+// fetched a third of the lines twice (61 tokens of 160 experts, 64-row tiles: 5.8
+// million requests to memory against 4.5 million, 191 us against 177).
+// 64- and 128-row tiles fit twice on a CU, so that one's fill and epilogue run beside the
+// other's products; 64-row tiles have room for one stage more of both (173 us).
 template <int kBits, int BM>
 struct TileShape {
-  static constexpr int kBStep = BM == 256 ? 256 : 128;
+  static constexpr int BN = BM == 256 ? 256 : 128;
   static constexpr int kABytes = BM * 64, kA2Bytes = kBits == mx::kF6 ? BM * 32 : 0;
-  static constexpr int kA2 = kABytes, kAScales = kA2 + kA2Bytes, kAStage = kAScales + BM * 4, kAStages = 3;
-  static constexpr int kBStage = 256 * kBStep / 2, kBStages = kBStep == 256 ? 2 : 3;
+  static constexpr int kA2 = kABytes, kAScales = kA2 + kA2Bytes, kAStage = kAScales + BM * 4, kAStages = BM == 64 ? 4 : 3;
+  static constexpr int kBStage = BN * 128, kBStages = BM == 64 ? 3 : 2;
   static constexpr int kB = kAStages * kAStage, kBScales = kB + kBStages * kBStage;
-  static constexpr int kLds = kBScales + 2 * 256 * 16;
+  static constexpr int kLds = kBScales + 2 * BN * 16;
 };
 
 #pragma clang diagnostic push
@@ -247,16 +251,15 @@ __device__ __forceinline__ void load_lds4(const u32x4& r, int off, unsigned lds_
 #pragma clang diagnostic pop
 
 template <int kBits, int EPI, int BM>
-__global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void tile_kernel(const MxGemm g) {
+__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void tile_kernel(const MxGemm g) {
   using S = TileShape<kBits, BM>;
-  constexpr int WM = BM == 256 ? 2 : 1, WN = 4 / WM;      // the waves' grid
-  constexpr int TM = BM / WM / 32, TN = 256 / WN / 32;    // 32 x 32 tiles a wave
+  constexpr int BN = S::BN;
+  constexpr int TM = BM / 2 / 32, TN = BN / 2 / 32;               // 32 x 32 tiles a wave, of 2 x 2 waves
   constexpr int NMAT = mats(EPI);
   constexpr int PA = S::kABytes / 4096, PB = S::kBStage / 4096;   // 16-byte loads a lane: a step of A, a stage of weights
   constexpr int PA2 = (S::kA2Bytes + 4095) / 4096;
   constexpr int LA = PA + PA2 + 1;                                // loads of a step of A, its scales with them
-  constexpr bool kWide = S::kBStep == 256;
-  constexpr int NSUB = 256 / NMAT;                                // output columns a block
+  constexpr int NSUB = BN / NMAT;                               // output columns a block
   __shared__ __align__(1024) char lds[S::kLds];
   int mt, nt;
   if (!place(*g.n_tiles, g.n_col_tiles, blockIdx.x, &mt, &nt)) return;
@@ -267,7 +270,7 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void tile_kernel(const MxGem
   const int n0 = nt * NSUB;
   const int K = g.K, KT = K / kStepK;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / WN, wn = wave % WN;
+  const int wm = wave / 2, wn = wave % 2;
   const int b_bytes = K / 2, s_bytes = K / mx::kBlock;   // a weight row's codes and scales
   const int64_t wofs = static_cast<int64_t>(e) * g.N;
   const int64_t b_all = static_cast<int64_t>(g.N) * b_bytes, s_all = static_cast<int64_t>(g.N) * s_bytes;
@@ -282,10 +285,10 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void tile_kernel(const MxGem
   const int ra_ = wave * 16 + lane / 4, offa = ra_ * 64 + ((lane % 4) ^ ((ra_ >> 2) & 3)) * 16;           // + 64 rows a load
   const int ra2_ = wave * 32 + lane / 2, offa2 = ra2_ * 32 + ((lane % 2) ^ ((ra2_ >> 3) & 1)) * 16;       // + 128 rows
   const int rsa_ = wave % (BM / 64) * 64 + lane;                                                          // (waves share rows)
-  const int rb_ = kWide ? wave * 8 + lane / 8 : wave * 16 + lane / 4;                                     // + 32 or 64 rows
-  const int offb = (n0 + rb_) * b_bytes + (kWide ? (lane % 8) ^ swz(rb_) : (lane % 4) ^ ((rb_ >> 2) & 3)) * 16;
-  const int offsb = (n0 + (wave * 64 + lane) % NSUB) * s_bytes;
-  const int b_pass = (kWide ? 32 : 64) * b_bytes;
+  const int rb_ = wave * 8 + lane / 8, offb = (n0 + rb_) * b_bytes + ((lane % 8) ^ swz(rb_)) * 16;        // + 32 rows
+  const int wsb = wave % (BN / 64);                                                                       // (and the scales')
+  const int offsb = (n0 + (wsb * 64 + lane) % NSUB) * s_bytes;
+  const int b_pass = 32 * b_bytes;
   const unsigned lds0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(
       (__attribute__((address_space(3))) char*)lds));
   // Load q of step kt of A.  Past the last step the descriptors are empty: nothing is
@@ -305,13 +308,13 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void tile_kernel(const MxGem
   };
   // Load p of stage ks of the weights; the scales of group kg (512 K values).
   auto issue_b = [&](int p, int ks, int stage) {
-    const unsigned past = ks * S::kBStep < K ? 0u : static_cast<unsigned>(kGatherOut);
-    load_lds(NMAT == 2 && p >= PB / 2 ? rb1 : rb0, offb + p % (PB / NMAT) * b_pass + ks * (S::kBStep / 2) + past,
+    const unsigned past = ks * 256 < K ? 0u : static_cast<unsigned>(kGatherOut);
+    load_lds(NMAT == 2 && p >= PB / 2 ? rb1 : rb0, offb + p % (PB / NMAT) * b_pass + ks * 128 + past,
              lds0 + stage + (p * 4 + wave) * 1024);
   };
   auto issue_scales = [&](int kg) {
     const unsigned past = kg * 512 < K ? 0u : static_cast<unsigned>(kGatherOut);
-    load_lds(NMAT == 2 && wave >= 2 ? rs1 : rs0, offsb + kg * 16 + past, lds0 + S::kBScales + (kg & 1) * 4096 + wave * 1024);
+    load_lds(NMAT == 2 && wsb >= BN / 128 ? rs1 : rs0, offsb + kg * 16 + past, lds0 + S::kBScales + (kg & 1) * (BN * 16) + wsb * 1024);
   };
 
   f32x16 acc[TM][TN];
@@ -324,17 +327,17 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void tile_kernel(const MxGem
 
   // the weight tiles of this wave: NMAT == 2: gate rows, then up rows 128 on
   const int half = lane >> 5, lr = lane & 31;
-  auto b_row = [&](int j) { return NMAT == 2 ? (j < TN / 2 ? 0 : 128) + wn * (TN / 2) * 32 + (j % (TN / 2)) * 32 : wn * TN * 32 + j * 32; };
+  auto b_row = [&](int j) { return NMAT == 2 ? (j < TN / 2 ? 0 : BN / 2) + wn * (TN / 2) * 32 + (j % (TN / 2)) * 32 : wn * TN * 32 + j * 32; };
   // Fragment read r of half step s: weight tile 0, the A tiles, the other weight tiles; a
-  // step's scales come with its first half.  oa, ob: the stages' places in LDS; for wide
-  // stages of the weights `odd` says which half of the stage.
+  // step's scales come with its first half.  oa, ob: the stages' places in LDS; `odd`
+  // says which half of the weights' stage.
   i32x4 fb[2][TN];
   Frag fa[2][TM];
   uint32_t sa[TM], sb[TN], next_sa[TM], next_sb[TN];
   const int a_row = wm * TM * 32 + lr;
   const int at_a = a_row * 64 + (half ^ ((lr >> 2) & 3)) * 16;                            // second half step: two chunks on
   const int at_a2 = S::kA2 + a_row * 32 + ((lr >> 3) & 1) * 16 + half * 8;                // (one on)
-  const int at_b = kWide ? lr * 128 + (half ^ swz(lr)) * 16 : lr * 64 + (half ^ ((lr >> 2) & 3)) * 16;
+  const int at_b = lr * 128 + (half ^ swz(lr)) * 16;
   const int at_sa = S::kAScales + a_row * 4, at_sb = S::kBScales + lr * 16;
   constexpr int NR = TM + TN, NM = TM * TN;
   constexpr int kReads = (2 * NR + NM - 1) / NM;   // reads an instruction: all of them in the half's first half
@@ -347,7 +350,7 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void tile_kernel(const MxGem
       if (s == 0) next_sa[i] = *reinterpret_cast<const uint32_t*>(lds + (at_sa + oa) + i * 128);
     } else {
       const int j = r == 0 ? 0 : r - TM;
-      fb[s][j] = *reinterpret_cast<const i32x4*>(lds + ((at_b ^ (64 * odd + 32 * s)) + ob) + b_row(j) * (kWide ? 128 : 64));
+      fb[s][j] = *reinterpret_cast<const i32x4*>(lds + ((at_b ^ (64 * odd + 32 * s)) + ob) + b_row(j) * 128);
       if (s == 0) next_sb[j] = *reinterpret_cast<const uint32_t*>(lds + (at_sb + os) + b_row(j) * 16);
     }
   };
@@ -360,36 +363,35 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void tile_kernel(const MxGem
   // A step's two halves run on registers that were read during the half before.  In the
   // middle of step kt the loads of step kt + 1 are awaited, those issued after them stay
   // in flight, and the waves meet: what step kt held in LDS has been read then and takes
-  // the loads of step kt + 3, which are issued over this half and the next step's first
-  // (in one half they filled the load queue and held the wave up).  Wide weights: the
-  // stage that an odd step ends takes the stage after next over three halves.
+  // the loads of step kt + kAStages, which are issued over this half and the next step's
+  // first (in one half they filled the load queue and held the wave up).  The weights'
+  // stage that an odd step ends is filled again over three halves.
+  // The wait counts what follows the last load of A for kt + 1: A of the steps behind it,
+  // and of the weights a whole stage where they have three, else those of two halves.
   // An odd count of steps is made even by one on zeros: no A is loaded for it and its
   // weights' scales are 2^-127.
   const int steps = (KT + 1) & ~1;
-  int a_here = 0, a_free = 2 * S::kAStage, b_here = 0, b_free = (S::kBStages - 1) * S::kBStage;   // (free: the last step's)
-  constexpr int kA1 = LA / 2, kA2 = LA - LA / 2, kB1 = kWide ? 3 : PB / 2, kB2 = kWide ? 6 : PB;
+  int a_here = 0, a_free = (S::kAStages - 1) * S::kAStage, b_here = 0, b_free = (S::kBStages - 1) * S::kBStage;   // (free: the last step's)
+  constexpr int kA1 = LA / 2, kA2 = LA - LA / 2, kB1 = (3 * PB + 7) / 8, kB2 = 3 * PB / 4;
   auto half_step = [&](int kt, auto odd_, auto second_) {
     constexpr int odd = decltype(odd_)::value, second = decltype(second_)::value;
     constexpr int kA = odd ? kA1 : kA2, kA_ = odd ? kA2 : kA1;     // of A issued in this step's second half, the last one's
     constexpr int from_a = second ? 0 : kA_, to_a = second ? kA : LA;
-    constexpr int from_b = kWide ? (odd ? 0 : second ? kB2 : kB1) : second ? 0 : kB1;
-    constexpr int to_b = kWide ? (odd ? (second ? kB1 : 0) : second ? PB : kB2) : second ? kB1 : PB;
+    constexpr int from_b = odd ? 0 : second ? kB2 : kB1, to_b = odd ? (second ? kB1 : 0) : second ? PB : kB2;
     constexpr int LS = second && !odd, LB = to_b - from_b, LT = LS + LB + to_a - from_a;
     const int a_next = a_here + S::kAStage == S::kB ? 0 : a_here + S::kAStage;
-    constexpr bool new_b = !kWide || odd;
-    const int b_next = !new_b ? b_here : b_here + S::kBStage == S::kBStages * S::kBStage ? 0 : b_here + S::kBStage;
-    const int os = (kt + 1) % 4 * 4 + (kt + 1) / 4 % 2 * 4096;
-    const int a_stage = second ? a_here : a_free, a_kt = second ? kt + 3 : kt + 2;
-    const int b_stage = kWide ? (odd ? b_here : b_free) : second ? b_here : b_free;
-    const int b_ks = kWide ? (kt + odd) / 2 + 1 : a_kt;
+    const int b_next = !odd ? b_here : b_here + S::kBStage == S::kBStages * S::kBStage ? 0 : b_here + S::kBStage;
+    const int os = (kt + 1) % 4 * 4 + (kt + 1) / 4 % 2 * (BN * 16);
+    const int a_stage = second ? a_here : a_free, a_kt = second ? kt + S::kAStages : kt + S::kAStages - 1;
+    const int b_stage = odd ? b_here : b_free, b_ks = (kt + odd) / 2 + S::kBStages - 1;
     int rd = 0, ld = 0;
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
       mma(m, second);
 #pragma unroll
       for (; rd < NR && rd <= m * kReads; ++rd) {
-        if constexpr (second) frag(rd, a_next, S::kB + b_next, kWide ? odd ^ 1 : 0, 0, os);
-        else frag(rd, a_here, S::kB + b_here, kWide ? odd : 0, 1, 0);
+        if constexpr (second) frag(rd, a_next, S::kB + b_next, odd ^ 1, 0, os);
+        else frag(rd, a_here, S::kB + b_here, odd, 1, 0);
       }
 #pragma unroll
       for (; ld < LT && ld * NM < (m + 1) * LT; ++ld) {
@@ -406,7 +408,7 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void tile_kernel(const MxGem
     if constexpr (second) {
       a_free = a_here;
       a_here = a_next;
-      if (new_b) {
+      if (odd) {
         b_free = b_here;
         b_here = b_next;
       }
@@ -420,25 +422,25 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void tile_kernel(const MxGem
 #pragma unroll
     for (int j = 0; j < TN; ++j) sb[j] = (next_sb[j] & live) >> (8 * half);
     half_step(kt, odd_, std::integral_constant<int, 0>{});
-    wait_vm<kWide ? (odd ? LA : LA + kB2) : LA + PB>();
+    wait_vm<BM == 64 ? 2 * LA + PB : odd ? LA : LA + kB2>();
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
     half_step(kt, odd_, std::integral_constant<int, 1>{});
   };
   issue_scales(0);
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < S::kAStages - 1; ++k) {
 #pragma unroll
     for (int q = 0; q < LA; ++q) issue_a(q, k, k * S::kAStage);
-    if (!kWide || k == 0)
+    if (k < S::kBStages - 1)
 #pragma unroll
       for (int p = 0; p < PB; ++p) issue_b(p, k, S::kB + k * S::kBStage);
   }
 #pragma unroll
-  for (int p = 0; p < kB1; ++p) issue_b(p, kWide ? 1 : 2, S::kB + b_free);
+  for (int p = 0; p < kB1; ++p) issue_b(p, S::kBStages - 1, S::kB + b_free);
 #pragma unroll
-  for (int q = 0; q < kA1; ++q) issue_a(q, 2, a_free);
-  wait_vm<LA + kA1 + kB1 + (kWide ? 0 : PB)>();
+  for (int q = 0; q < kA1; ++q) issue_a(q, S::kAStages - 1, a_free);
+  wait_vm<(S::kAStages - 2) * LA + (S::kBStages - 2) * PB + kA1 + kB1>();
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < NR; ++r) frag(r, 0, S::kB, 0, 0, 0);
@@ -459,18 +461,18 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void tile_kernel(const MxGem
       else return fast_gelu(acc[i][j][u]);
     };
 #pragma unroll
-    for (int b = 0; b < TM * TC; b += 2) {
+    for (int b = 0; b < TM * TC; b += 2) {   // (a wave's only block: both halves make it, one writes it)
       float v[32];
 #pragma unroll
       for (int u = 0; u < 16; ++u) {
-        const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(value(b, u)), __float_as_uint(value(b + 1, u)), false, false);
+        const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(value(b, u)), __float_as_uint(value(min(b + 1, TM * TC - 1), u)), false, false);
         v[8 * (u / 4) + u % 4] = __uint_as_float(t[0]);
         v[8 * (u / 4) + 4 + u % 4] = __uint_as_float(t[1]);
       }
       const mx::Operand o = mx::encode_block<kBits>(v);
-      const int mine = b + half, i = mine / TC, j = mine % TC;
+      const int mine = TM * TC == 1 ? 0 : b + half, i = mine / TC, j = mine % TC;
       const int r = (wm * TM + i) * 32 + lr, col = n0 + (wn * TC + j) * 32;
-      if (r < n && col < g.N) store_block<kBits>(o, row0 + r, g.M, col / mx::kBlock, static_cast<uint8_t*>(g.C), g.C2, g.Cs);
+      if (r < n && col < g.N && (TM * TC > 1 || half == 0)) store_block<kBits>(o, row0 + r, g.M, col / mx::kBlock, static_cast<uint8_t*>(g.C), g.C2, g.Cs);
     }
   } else {
 #pragma unroll
@@ -651,18 +653,19 @@ struct MxLayout {
 // Rows of a tile, from the rows and the rows an expert has on average, fitted to
 // sweeps over 160 experts of 5120 x 1536, 64 of 2048 x 1408, 16 of 6144 x 10752, 8 of
 // 4096 x 14336 and 32 of 1024 x 4096 (GELU), us a call in 6 bits:
-//   up to 128 rows the stream: 64 rows at 8 experts 177 against 194 in 64-row tiles, 128
-//     rows at 32 experts 35 against 35; at 256 rows and 16 experts 460 against 413.
-//   64-row tiles (two blocks on a CU, so one's fill and epilogue run beside the other's
-//     products) while products are few or K is short: rows * H^2 <= 2^30.  38 rows an
-//     expert at H = 5120 512 against 514 in 128-row tiles; 250 at H = 1024 104 against
-//     129; but 76 at H = 5120 722 against 687.
-//   256-row tiles from 128 rows an expert: at H = 6144 544 against 601 in 128-row tiles.
+//   up to 24 rows the stream, which splits K: one token of two experts at H = 4096 39
+//     against 62 in 64-row tiles, 18 rows at H = 5120 41 against 46; but 36 rows 55
+//     against 52, 64 rows at H = 4096 176 against 145.
+//   64-row tiles up to 64 rows an expert: 38 at H = 5120 496 against 511 in 128-row tiles;
+//     76 there 691 against 654, 64 at H = 6144 470 against 454, at H = 4096 220 against 234.
+//   256-row tiles where rows and K make up for one block a CU, from 2^19 rows * H an expert
+//     on: 131 rows at H = 5120 794 against 827 in 128-row tiles, 256 at H = 4096 349 against
+//     407; 76 at H = 5120 677 against 654, 250 at H = 1024 123 against 106.
 int rows_per_tile(int64_t M, int E, int H) {
   const int64_t avg = M / E;
-  if (M <= 128) return kStreamRows;
-  if (avg * H * H <= (int64_t(1) << 30)) return 64;
-  return avg < 128 ? 128 : 256;
+  if (M <= 24) return kStreamRows;
+  if (avg <= 64) return 64;
+  return avg * H < (int64_t(1) << 19) ? 128 : 256;
 }
 
 // Whatever E a call gives, the list has room for the smallest tiles.
@@ -713,8 +716,7 @@ int launch_stream(MxGemm p, int64_t row_tiles, hipStream_t s, const char* what) 
 template <int kBits, int EPI>
 int launch_product(MxGemm p, int bm, int64_t row_tiles, hipStream_t s, const char* what) {
   if (bm == kStreamRows) return launch_stream<kBits, EPI>(p, row_tiles, s, what);
-  const int64_t cols = 256 / mats(EPI);
-  p.n_col_tiles = static_cast<int>(ceil_div(p.N, cols));
+  p.n_col_tiles = static_cast<int>(ceil_div(p.N, (bm == 256 ? 256 : 128) / mats(EPI)));
   const int64_t blocks = row_tiles * p.n_col_tiles;
   if (blocks >= (int64_t(1) << 24)) return moe::fail(MOE_ERR_UNSUPPORTED, "moe_mx_expert_ffn: %lld blocks in one launch", (long long)blocks);
   const unsigned grid = static_cast<unsigned>(blocks);

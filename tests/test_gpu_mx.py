@@ -326,6 +326,10 @@ CASES = [
     ([126, 125, 130, 123], 2944, 384),
     ([300, 256, 511, 0], 2176, 640),
     ([257, 300], 2048, 128),
+    ([16, 0, 7, 1], 640, 256),
+    ([18, 5], 2048, 128),
+    ([1, 0, 3, 1] * 8, 256, 384),
+    ([64, 50, 65, 77], 1152, 256),
 ]
 
 
@@ -345,7 +349,7 @@ def test_ffn(fmt, act, dtype, counts, H, I):
 
 
 @pytest.mark.parametrize("fmt", X_FORMATS)
-@pytest.mark.parametrize("counts", [[3, 0, 5, 9], [70, 2, 31, 90], [60, 100, 70, 50], [200, 150, 300, 129]])
+@pytest.mark.parametrize("counts", [[3, 0, 5, 9], [30, 2, 21, 50], [70, 2, 31, 90], [60, 100, 70, 50], [200, 150, 300, 129]])
 def test_ffn_gathers_rows(fmt, counts):
     """Rows by a map: repeated, unordered, out of range (zero rows); replica slots and spare slots; y whole."""
     M, T = sum(counts), 50
