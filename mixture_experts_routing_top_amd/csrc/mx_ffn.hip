@@ -188,19 +188,18 @@ __device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t r, int off) {
   return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
-// The block's place: XCD-contiguous runs of tiles, eight row tiles by the columns
-// (gemm.h).  False past the last tile.
-__device__ __forceinline__ bool place(int total_m, int n_col_tiles, int b, int* mt, int* nt) {
-  const int total = total_m * n_col_tiles;
-  if (b >= total) return false;
-  const int xcd = b & 7, q = total >> 3, rem = total & 7;
-  const int l = xcd * q + min(xcd, rem) + (b >> 3);
+// Tile l of total_m x n_col_tiles: eight row tiles by the columns (gemm.h).
+__device__ __forceinline__ void tile_at(int l, int total_m, int n_col_tiles, int* mt, int* nt) {
   const int grp = l / (kGroupM * n_col_tiles);
   const int gsz = min(kGroupM, total_m - grp * kGroupM);
   const int li = l - grp * kGroupM * n_col_tiles;
   *mt = grp * kGroupM + li % gsz;
   *nt = li / gsz;
-  return true;
+}
+// Block b's of `total` tiles, each XCD's in a run.
+__device__ __forceinline__ int xcd_run(int b, int total) {
+  const int xcd = b & 7, q = total >> 3, rem = total & 7;
+  return xcd * q + min(xcd, rem) + (b >> 3);
 }
 
 // z Phi(z), the exact GELU: Phi(-|z|) = e^(-z^2 / 2) P(t) / 2, t = 1 / (1 + p |z| / sqrt 2),
@@ -250,8 +249,9 @@ __device__ __forceinline__ void load_lds4(const u32x4& r, int off, unsigned lds_
 }
 #pragma clang diagnostic pop
 
+// The product of rows row0 and n - 1 on with output columns n0 on.
 template <int kBits, int EPI, int BM>
-__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void tile_kernel(const MxGemm g) {
+__device__ __forceinline__ void tile_body(const MxGemm& g, char* lds, int e, int64_t row0, int n, int n0) {
   using S = TileShape<kBits, BM>;
   constexpr int BN = S::BN;
   constexpr int TM = BM / 2 / 32, TN = BN / 2 / 32;               // 32 x 32 tiles a wave, of 2 x 2 waves
@@ -260,14 +260,6 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void tile_kernel(const MxGe
   constexpr int PA2 = (S::kA2Bytes + 4095) / 4096;
   constexpr int LA = PA + PA2 + 1;                                // loads of a step of A, its scales with them
   constexpr int NSUB = BN / NMAT;                               // output columns a block
-  __shared__ __align__(1024) char lds[S::kLds];
-  int mt, nt;
-  if (!place(*g.n_tiles, g.n_col_tiles, blockIdx.x, &mt, &nt)) return;
-  const int4 tile = g.tiles[mt];
-  const int e = __builtin_amdgcn_readfirstlane(tile.x);
-  const int64_t row0 = __builtin_amdgcn_readfirstlane(tile.y);
-  const int n = __builtin_amdgcn_readfirstlane(tile.z) - static_cast<int>(row0);
-  const int n0 = nt * NSUB;
   const int K = g.K, KT = K / kStepK;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / 2, wn = wave % 2;
@@ -506,6 +498,37 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void tile_kernel(const MxGe
   }
 }
 
+// A 256-row tile fills a CU: where the last round of them would leave half the CUs or more
+// idle, it is cut into quarters (of 128 rows by half the columns).  4 rounds and a quarter
+// of down tiles (16384 rows of 8 experts, K = 14336, 6 bits) 625 us whole, 572 so.
+constexpr int kCus = 256;
+
+template <int kBits, int EPI, int BM>
+__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void tile_kernel(const MxGemm g) {
+  __shared__ __align__(1024) char lds[TileShape<kBits, BM>::kLds];
+  constexpr int kCols = TileShape<kBits, BM>::BN / mats(EPI);
+  const int total_m = *g.n_tiles, total = total_m * g.n_col_tiles, b = blockIdx.x;
+  int rest = 0;
+  if constexpr (BM == 256) rest = total % kCus <= kCus / 2 ? total % kCus : 0;
+  const int whole = total - rest;
+  if (b >= whole + 4 * rest) return;
+  const int quarter = b < whole ? 0 : (b - whole) / rest;   // (a tile's on one XCD where rest is a multiple of 8)
+  int mt, nt;
+  tile_at(b < whole ? xcd_run(b, whole) : b - quarter * rest, total_m, g.n_col_tiles, &mt, &nt);
+  const int4 tile = g.tiles[mt];
+  const int e = __builtin_amdgcn_readfirstlane(tile.x);
+  const int64_t row0 = __builtin_amdgcn_readfirstlane(tile.y);
+  const int n = __builtin_amdgcn_readfirstlane(tile.z) - static_cast<int>(row0);
+  if constexpr (BM == 256)
+    if (b >= whole) {
+      const int down = quarter / 2 * 128, right = quarter % 2 * (kCols / 2);
+      if (down < n && nt * kCols + right < g.N)
+        tile_body<kBits, EPI, 128>(g, lds, e, row0 + down, min(n - down, 128), nt * kCols + right);
+      return;
+    }
+  tile_body<kBits, EPI, BM>(g, lds, e, row0, n, nt * kCols);
+}
+
 // ---- few rows an expert ------------------------------------------------------------
 // At most 16 rows by four 16-row weight tiles (two of the gate and two of the up
 // weights, or 64 columns of y).  Wave w takes the w-th part of K, through a ring of its
@@ -717,7 +740,7 @@ template <int kBits, int EPI>
 int launch_product(MxGemm p, int bm, int64_t row_tiles, hipStream_t s, const char* what) {
   if (bm == kStreamRows) return launch_stream<kBits, EPI>(p, row_tiles, s, what);
   p.n_col_tiles = static_cast<int>(ceil_div(p.N, (bm == 256 ? 256 : 128) / mats(EPI)));
-  const int64_t blocks = row_tiles * p.n_col_tiles;
+  const int64_t blocks = row_tiles * p.n_col_tiles + (bm == 256 ? 3 * (kCus / 2) : 0);   // (and quarters)
   if (blocks >= (int64_t(1) << 24)) return moe::fail(MOE_ERR_UNSUPPORTED, "moe_mx_expert_ffn: %lld blocks in one launch", (long long)blocks);
   const unsigned grid = static_cast<unsigned>(blocks);
   if (bm == 64) tile_kernel<kBits, EPI, 64><<<grid, 256, 0, s>>>(p);
