@@ -571,6 +571,8 @@ def moe_backward_mx(x, y_perm, perm_src, topk_w, inv_pos, expert_off, w_gate, w_
         _out(t, shape, dtype, dev, name)
     if check is not None:
         _out(check, (1,), torch.int32, dev, "check")
+    if isinstance(workspace, torch.Tensor) and workspace.device != dev:
+        raise ValueError(f"backward workspace: expected on {dev}, got {workspace.device}")
     o = dict(out or {})
     need = moe_backward_mx_workspace_bytes(dt, T, k, H, I, E, act)
     shapes = {"d_x": ((T, H), dt), "d_topk_w": ((T, k), torch.float32), "d_w_gate": ((E, I, H), dt),

@@ -5,7 +5,11 @@
 // 8-bit blocks.
 //
 // All three are bound by memory: every value is read once and written once, 16 bytes
-// of them a lane, in accesses that a wave makes to one run of addresses.  mx.h has the format and the split of a row over lanes.
+// of them a lane, in accesses that a wave makes to one run of addresses.  mx.h has the
+// format and the split of a row over lanes.  Measured out of cache, a launch included:
+// 28672 x 4096 bf16 to 8 bits 63 us (5.7 TB/s) and back 63, to 4 bits 51 (5.8) and back 60;
+// float to 4 bits 98 (5.4) and back 91 (5.8); e2m3 has no conversion for single values
+// and takes some 25 instructions a value: 68 (4.8).
 #include <type_traits>
 
 #include "common.h"
@@ -20,6 +24,71 @@ using namespace rows;
 // Values a lane: 16 bytes, but eight floats where four e2m3 codes would end inside a byte.
 template <bool kBf16, int kBits>
 constexpr int kLane = kBf16 || kBits == mx::kF6 ? 8 : 4;
+
+// Whole rows (kFlat: K a multiple of 32, and no row map): values, codes and scales are three
+// flat runs, and a unit's places its number times a constant (28672 x 4096 bf16 to 4 bits
+// 52 us; 28671 x 4095 by rows 70).
+template <bool kBf16, int kBits, int kUnits>
+__global__ __launch_bounds__(256) void quantize_flat_kernel(const void* __restrict__ x, int64_t n_units,
+                                                            uint8_t* __restrict__ q, uint8_t* __restrict__ scale,
+                                                            int32_t* __restrict__ check) {
+  constexpr int V = kLane<kBf16, kBits>, P = mx::kBlock / V, kBytes = V * kBits / 8;
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * (256 * kUnits);
+  const uint32_t left = static_cast<uint32_t>(min<int64_t>(n_units - base, 256 * kUnits));
+  const char* const xb = static_cast<const char*>(x) + base * (V * (kBf16 ? 2 : 4));
+  uint8_t* const qb = q + base * kBytes;
+  uint8_t* const sb = scale + base / P;
+  float v[kUnits][V];
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) {
+    const uint32_t unit = j * 256 + threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < V; ++u) v[j][u] = 0.f;
+    if (unit < left) mx::load_values<kBf16, V>(xb, unit * V, V, v[j]);
+  }
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) {
+    const uint32_t unit = j * 256 + threadIdx.x, byte = mx::shared_scale<kBits, V>(v[j]);
+    bad |= byte == 255;
+    const uint2 c = mx::encode<kBits, V>(v[j], byte);
+    if (unit >= left) continue;
+    __builtin_memcpy(qb + unit * kBytes, &c, kBytes);
+    if (unit % P == 0) sb[unit / P] = static_cast<uint8_t>(byte);
+  }
+  if (check) raise_check(check, bad, MOE_CHECK_BLOCKS);
+}
+
+template <bool kBf16, int kBits, int kUnits>
+__global__ __launch_bounds__(256) void dequantize_flat_kernel(const uint8_t* __restrict__ q,
+                                                              const uint8_t* __restrict__ scale, int64_t n_units,
+                                                              void* __restrict__ out) {
+  constexpr int V = kLane<kBf16, kBits>, P = mx::kBlock / V, kBytes = V * kBits / 8;
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * (256 * kUnits);
+  const uint32_t left = static_cast<uint32_t>(min<int64_t>(n_units - base, 256 * kUnits));
+  const uint8_t* const qb = q + base * kBytes;
+  const uint8_t* const sb = scale + base / P;
+  char* const ob = static_cast<char*>(out) + base * (V * (kBf16 ? 2 : 4));
+  uint2 c[kUnits];
+  uint32_t byte[kUnits];
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) {
+    const uint32_t unit = j * 256 + threadIdx.x;
+    c[j] = make_uint2(0, 0);
+    byte[j] = 0;
+    if (unit >= left) continue;
+    __builtin_memcpy(&c[j], qb + unit * kBytes, kBytes);
+    byte[j] = sb[unit / P];
+  }
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) {
+    const uint32_t unit = j * 256 + threadIdx.x;
+    if (unit >= left) continue;
+    float v[V];
+    mx::decode<kBits, V>(c[j], byte[j], v);
+    mx::store_values<kBf16, V>(ob, unit * V, V, v);
+  }
+}
 
 template <bool kBf16, int kBits, int kUnits>
 __global__ __launch_bounds__(256) void quantize_kernel(const void* __restrict__ x, int64_t R, int K, uint32_t blocks,
@@ -114,7 +183,10 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* __restri
 
 // d_y[inv[t,i]] = w[t,i] d_out[t] and d_w[t,i] = <d_out[t], y[inv[t,i]]>.  kWaves
 // waves a token (kWaves = 1: four tokens a block), eight values of the row and of each
-// of its KK expert rows a lane and step, all loads of a step before its sums.
+// of its KK expert rows a lane and step, all loads of a step before its sums.  Bound by
+// memory: 8192 tokens of two kept rows, H = 4096, 271 MB in 46 us (5.8 TB/s); 16001 of six,
+// H = 5120, 1.66 GB in 332 (5.0; the rows are written in the experts' order, a token's far
+// apart).
 template <bool kBf16, bool kKept, int kWaves, int KK>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const void* __restrict__ d_out, const void* __restrict__ y,
                                                                const uint8_t* __restrict__ y_scale, int64_t M,
@@ -203,34 +275,49 @@ int check_format(const char* who, moe_dtype dt, moe_mx_format fmt, int64_t R, in
   return MOE_OK;
 }
 
-// Units a thread: four once that still fills the card several times over, so that
-// more loads are in flight; one for a short call.
-constexpr int kManyUnits = 4;
-bool many(int64_t units) { return units >= int64_t(256) * 256 * kManyUnits * 4; }
+// Units a thread: 16 values' once that still fills the card several times over, so that
+// more loads are in flight; one for a short call.  (28672 x 4096 bf16 to 8 bits 62.6 us with
+// two units, 68 with four; float to 4 bits 97.8 with four, back 91 against 98 with two.)
+template <bool kBf16, int kBits>
+constexpr int kManyUnits = 16 / kLane<kBf16, kBits>;
+template <bool kBf16, int kBits>
+bool many(int64_t units) { return units >= int64_t(256) * 256 * 4 * kManyUnits<kBf16, kBits>; }
+
+template <bool kBf16, int kBits, int kUnits>
+void launch_quantize_units(const void* x, int64_t R, int K, int64_t units, uint8_t* q, uint8_t* scale, int32_t* check,
+                           hipStream_t s) {
+  const unsigned grid = static_cast<unsigned>(ceil_div(units, 256 * kUnits));
+  if (K % mx::kBlock == 0)
+    quantize_flat_kernel<kBf16, kBits, kUnits><<<grid, 256, 0, s>>>(x, units, q, scale, check);
+  else
+    quantize_kernel<kBf16, kBits, kUnits><<<grid, 256, 0, s>>>(x, R, K, static_cast<uint32_t>(ceil_div(K, mx::kBlock)), q,
+                                                               scale, check);
+}
 
 template <bool kBf16, int kBits>
 void launch_quantize(const void* x, int64_t R, int K, uint8_t* q, uint8_t* scale, int32_t* check, hipStream_t s) {
-  const uint32_t blocks = static_cast<uint32_t>(ceil_div(K, mx::kBlock));
-  const int64_t units = R * blocks * (mx::kBlock / kLane<kBf16, kBits>);
-  if (many(units))
-    quantize_kernel<kBf16, kBits, kManyUnits><<<static_cast<unsigned>(ceil_div(units, 256 * kManyUnits)), 256, 0, s>>>(
-        x, R, K, blocks, q, scale, check);
+  const int64_t units = R * ceil_div(K, mx::kBlock) * (mx::kBlock / kLane<kBf16, kBits>);
+  if (many<kBf16, kBits>(units)) launch_quantize_units<kBf16, kBits, kManyUnits<kBf16, kBits>>(x, R, K, units, q, scale, check, s);
+  else launch_quantize_units<kBf16, kBits, 1>(x, R, K, units, q, scale, check, s);
+}
+
+template <bool kBf16, int kBits, int kUnits>
+void launch_dequantize_units(const uint8_t* q, const uint8_t* scale, int64_t R, int K, const int32_t* rows,
+                             int64_t n_rows, int64_t units, void* out, int32_t* check, hipStream_t s) {
+  const unsigned grid = static_cast<unsigned>(ceil_div(units, 256 * kUnits));
+  if (!rows && K % mx::kBlock == 0)
+    dequantize_flat_kernel<kBf16, kBits, kUnits><<<grid, 256, 0, s>>>(q, scale, units, out);
   else
-    quantize_kernel<kBf16, kBits, 1><<<static_cast<unsigned>(ceil_div(units, 256)), 256, 0, s>>>(x, R, K, blocks, q, scale,
-                                                                                               check);
+    dequantize_kernel<kBf16, kBits, kUnits><<<grid, 256, 0, s>>>(q, scale, R, K, static_cast<uint32_t>(ceil_div(K, mx::kBlock)),
+                                                                 rows, n_rows, out, check);
 }
 
 template <bool kBf16, int kBits>
 void launch_dequantize(const uint8_t* q, const uint8_t* scale, int64_t R, int K, const int32_t* rows, int64_t n_rows,
                        void* out, int32_t* check, hipStream_t s) {
-  const uint32_t blocks = static_cast<uint32_t>(ceil_div(K, mx::kBlock));
-  const int64_t units = n_rows * blocks * (mx::kBlock / kLane<kBf16, kBits>);
-  if (many(units))
-    dequantize_kernel<kBf16, kBits, kManyUnits><<<static_cast<unsigned>(ceil_div(units, 256 * kManyUnits)), 256, 0, s>>>(
-        q, scale, R, K, blocks, rows, n_rows, out, check);
-  else
-    dequantize_kernel<kBf16, kBits, 1><<<static_cast<unsigned>(ceil_div(units, 256)), 256, 0, s>>>(
-        q, scale, R, K, blocks, rows, n_rows, out, check);
+  const int64_t units = n_rows * ceil_div(K, mx::kBlock) * (mx::kBlock / kLane<kBf16, kBits>);
+  if (many<kBf16, kBits>(units)) launch_dequantize_units<kBf16, kBits, kManyUnits<kBf16, kBits>>(q, scale, R, K, rows, n_rows, units, out, check, s);
+  else launch_dequantize_units<kBf16, kBits, 1>(q, scale, R, K, rows, n_rows, units, out, check, s);
 }
 
 template <bool kBf16, bool kKept, int KK>
