@@ -450,7 +450,7 @@ int moe_combine(const void* y_perm, moe_dtype dt, int64_t M, const int32_t* inv_
  * inv_pos entries outside [0, M) get d_topk_w 0 and write no row (MOE_CHECK_ROWS);
  * rows that no entry names are left as they are, and a row that two entries name
  * holds either's.  d_y may not be y or d_out.
- * Limits: 1 <= k <= 8, H a multiple of 8, T*k < 2^31; d_out, y and d_y 16-byte
+ * Limits: 1 <= k <= 8, H a multiple of 8, T at most 2^25; d_out, y and d_y 16-byte
  * aligned.  The dispatch's own gradient, d_x[t] = sum_i d_x_perm[inv_pos[t, i]],
  * is moe_combine with unit weights.
  */
@@ -480,7 +480,7 @@ int moe_combine_backward(const void* d_out, moe_dtype dt, const void* y, const u
  * more).  rows int32 [n_rows], e.g. moe_dispatch's perm_src: x_perm comes back from
  * the tokens that were kept.  Entries outside [0, R) give zero rows
  * (MOE_CHECK_ROWS).
- * Limits: 1 <= K <= 2^28, at most 2^31 blocks.
+ * Limits: 1 <= K <= 2^28, at most 2^30 blocks (of x and of out).
  */
 int moe_mx_quantize(const void* x, moe_dtype dt, int64_t R, int64_t K, moe_mx_format fmt, uint8_t* q, uint8_t* scale,
                     int32_t* check, void* stream);
@@ -504,7 +504,8 @@ int moe_mx_dequantize(const uint8_t* q, const uint8_t* scale, moe_mx_format fmt,
  *   workspace  moe_mx_expert_ffn_workspace_bytes(M, ...) bytes, rewritten by every
  *            call: two calls in flight need two.
  * Limits: H and I multiples of 128 up to 2^22, H*I/2 below 0x7e000000, M times the
- * larger of H and I at most 2^36; 1 <= E <= max_slots.
+ * larger of H and I at most 2^36; 1 <= E <= max_slots, and a launch's tiles (rows by 64,
+ * 128 or 256, one more a slot, times columns by as many) below 2^24.
  * All tensors 16-byte aligned.
  * check: MOE_CHECK_SLOTS, MOE_CHECK_BLOCKS (in x).
  */
@@ -581,7 +582,7 @@ int moe_backward_gated(const void* x_perm, const void* y_perm, moe_dtype dt, int
  * 2^-10 of its block's scale where that is more.  The weights stay as they are.  The
  * workspace holds x_perm too.  With a check word, MOE_CHECK_ROWS for an entry of
  * perm_src or inv_pos out of range (its row counts as zero).
- * Limits: those of moe_backward, and T*k*H at most 2^36.
+ * Limits: those of moe_backward, T at most 2^25 and T*k*H at most 2^35.
  */
 size_t moe_backward_mx_workspace_bytes(moe_dtype dt, int64_t T, int k, int H, int I, int E, moe_act act); /* [host] */
 int moe_backward_mx(const uint8_t* x, const uint8_t* x_scale, const uint8_t* y_perm, const uint8_t* y_scale,

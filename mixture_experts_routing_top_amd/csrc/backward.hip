@@ -527,8 +527,8 @@ int backward(const char* who, const Kept* kept, const void* x_perm, const void* 
     return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
   if (T > 0 && (!topk_w || !inv_pos || !d_out || !d_x || !(d_logits || d_topk_w)))
     return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
-  if (kept && T * k > (int64_t(1) << 31) / (H / 32))
-    return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^31 blocks of 32 values", who);
+  if (kept && (T > (int64_t(1) << 25) || T * k > (int64_t(1) << 30) / (H / 32)))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^25 tokens or 2^30 blocks of 32 values", who);
   const void* ptrs[] = {x_perm, y_perm, w_gate, w_up, w_down, d_out, d_x, d_w_gate, d_w_up, d_w_down, workspace};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return fail(MOE_ERR_INVALID_ARG, "%s: operands must be 16-byte aligned", who);

@@ -270,8 +270,8 @@ int check_format(const char* who, moe_dtype dt, moe_mx_format fmt, int64_t R, in
   if (fmt != MOE_MX_FP4 && fmt != MOE_MX_FP8 && fmt != MOE_MX_FP6) return fail(MOE_ERR_INVALID_ARG, "%s: unknown format %d", who, (int)fmt);
   if (R < 0) return fail(MOE_ERR_INVALID_ARG, "%s: negative number of rows", who);
   if (K < 1 || K > (1 << 28)) return fail(MOE_ERR_INVALID_ARG, "%s: K=%lld outside [1, 2^28]", who, (long long)K);
-  if (R > (int64_t(1) << 31) / ceil_div(K, mx::kBlock))
-    return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^31 blocks of 32 values", who);
+  if (R > (int64_t(1) << 30) / ceil_div(K, mx::kBlock))   // (a launch has fewer than 2^32 threads)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^30 blocks of 32 values", who);
   return MOE_OK;
 }
 
@@ -388,6 +388,7 @@ extern "C" int moe_combine_backward(const void* d_out, moe_dtype dt, const void*
   if (T < 0 || M < 0 || T * k >= (int64_t(1) << 31)) return fail(MOE_ERR_INVALID_ARG, "moe_combine_backward: bad T or M");
   if (H < 8 || H % 8 || H > (1 << 28))
     return fail(MOE_ERR_INVALID_ARG, "moe_combine_backward: H must be a positive multiple of 8 (H=%d)", H);
+  if (T > (int64_t(1) << 25)) return fail(MOE_ERR_UNSUPPORTED, "moe_combine_backward: more than 2^25 tokens");
   if (T == 0) return MOE_OK;
   if (!d_out || !inv_pos || !topk_w || !d_topk_w || (M > 0 && (!y || !d_y)))
     return fail(MOE_ERR_INVALID_ARG, "moe_combine_backward: null pointer");

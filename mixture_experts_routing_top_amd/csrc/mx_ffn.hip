@@ -721,7 +721,6 @@ int launch_stream(MxGemm p, int64_t row_tiles, hipStream_t s, const char* what) 
   const int cols = narrow ? kWide / 2 : kWide;
   p.n_col_tiles = p.N / cols;
   const int64_t blocks = row_tiles * p.n_col_tiles;
-  if (blocks >= (int64_t(1) << 23)) return moe::fail(MOE_ERR_UNSUPPORTED, "moe_mx_expert_ffn: %lld blocks in one launch", (long long)blocks);
   const unsigned grid = static_cast<unsigned>(blocks);
   const bool deep = blocks <= 256 && p.K / kStepK >= 16;
   if constexpr (kCanNarrow) {
@@ -736,13 +735,17 @@ int launch_stream(MxGemm p, int64_t row_tiles, hipStream_t s, const char* what) 
   return moe::hip_status(hipGetLastError(), what);
 }
 
+// Blocks of a tile_kernel launch (64 rows and up), the last round's quarters among them.
+int tile_cols(int bm, int N, int n_mat) { return static_cast<int>(ceil_div(N, (bm == 256 ? 256 : 128) / n_mat)); }
+int64_t tile_blocks(int bm, int64_t row_tiles, int n_col_tiles) {
+  return row_tiles * n_col_tiles + (bm == 256 ? 3 * (kCus / 2) : 0);
+}
+
 template <int kBits, int EPI>
 int launch_product(MxGemm p, int bm, int64_t row_tiles, hipStream_t s, const char* what) {
   if (bm == kStreamRows) return launch_stream<kBits, EPI>(p, row_tiles, s, what);
-  p.n_col_tiles = static_cast<int>(ceil_div(p.N, (bm == 256 ? 256 : 128) / mats(EPI)));
-  const int64_t blocks = row_tiles * p.n_col_tiles + (bm == 256 ? 3 * (kCus / 2) : 0);   // (and quarters)
-  if (blocks >= (int64_t(1) << 24)) return moe::fail(MOE_ERR_UNSUPPORTED, "moe_mx_expert_ffn: %lld blocks in one launch", (long long)blocks);
-  const unsigned grid = static_cast<unsigned>(blocks);
+  p.n_col_tiles = tile_cols(bm, p.N, mats(EPI));
+  const unsigned grid = static_cast<unsigned>(tile_blocks(bm, row_tiles, p.n_col_tiles));
   if (bm == 64) tile_kernel<kBits, EPI, 64><<<grid, 256, 0, s>>>(p);
   else if (bm == 128) tile_kernel<kBits, EPI, 128><<<grid, 256, 0, s>>>(p);
   else tile_kernel<kBits, EPI, 256><<<grid, 256, 0, s>>>(p);
@@ -807,6 +810,11 @@ extern "C" int moe_mx_expert_ffn(const void* x, const int32_t* row_src, int64_t 
   int32_t* const n_tiles = reinterpret_cast<int32_t*>(ws + w.n_tiles);
   const int bm = rows_per_tile(M, E, H);
   const int64_t row_tiles = M / bm + std::min<int64_t>(M, max_slots);
+  if (bm != kStreamRows) {
+    const int64_t most = std::max(tile_blocks(bm, row_tiles, tile_cols(bm, I, act == MOE_SWIGLU ? 2 : 1)),
+                                  tile_blocks(bm, row_tiles, tile_cols(bm, H, 1)));
+    if (most >= (int64_t(1) << 24)) return fail(MOE_ERR_UNSUPPORTED, "%s: %lld tiles in one launch", who, (long long)most);
+  }
   const dim3 grid(static_cast<unsigned>(ceil_div(M * 4, 256) + 1), H / kStepK);
   auto prepare = [&](auto kernel) {
     kernel<<<grid, 256, 0, s>>>(x, row_src, n_src, H, at(w.xq), at(w.xq2), at(w.xs), slot_off, slot_expert, n_slots,

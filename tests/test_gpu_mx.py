@@ -348,6 +348,19 @@ def test_ffn(fmt, act, dtype, counts, H, I):
     _assert_ffn(y, om.values(_f64(x), fmt), list(range(M)), table, wts, act, fmt, dtype)
 
 
+@pytest.mark.parametrize("act,fmt,dtype", [("swiglu", "fp6", torch.bfloat16), ("gelu", "fp4", torch.float32),
+                                           ("gelu", "fp6", torch.bfloat16), ("swiglu", "fp4", torch.float32)])
+def test_ffn_whole_and_quartered_tiles(act, fmt, dtype):
+    """256-row tiles, 9 of rows: 261 of SwiGLU's h (a round of 256, the rest in quarters), 135 of GELU's (the last
+    columns half a tile) and 144 of y."""
+    counts, H, I = [300, 300, 300, 300, 140], 4096, 3712
+    wts = (_weights(5, I, H, 1), _weights(5, I, H, 2) if act == "swiglu" else None, _weights(5, H, I, 3))
+    x = _rows((sum(counts), H), dtype, 5)
+    table = _table(counts)
+    y = moe.moe_mx_expert_ffn(x, *table, *wts, act, fmt)
+    _assert_ffn(y, om.values(_f64(x), fmt), range(sum(counts)), table, wts, act, fmt, dtype)
+
+
 @pytest.mark.parametrize("fmt", X_FORMATS)
 @pytest.mark.parametrize("counts", [[3, 0, 5, 9], [30, 2, 21, 50], [70, 2, 31, 90], [60, 100, 70, 50], [200, 150, 300, 129]])
 def test_ffn_gathers_rows(fmt, counts):

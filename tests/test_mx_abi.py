@@ -32,7 +32,10 @@ def _backward(x=P, xs=P, y=P, ys=P, dt=1, T=8, k=2, H=64, I=64, E=4, src=P, w=P,
     (_backward(dt=2), -1, "dtype"), (_backward(act=2), -1, "activation"), (_backward(E=0), -1, "E=0"),
     (_backward(E=300), -2, "E=300"), (_backward(k=5), -1, "k=5"), (_backward(k=0), -1, "k=0"), (_backward(T=-1), -1, "T"),
     (_backward(H=96), -2, "multiples of 64"), (_backward(I=32), -2, "multiples of 64"),
-    (_backward(T=1 << 20, k=2, H=1 << 17), -2, "2\\^31 blocks"),
+    (_ffn(M=(1 << 14) - 1, I=1 << 22, slots=1 << 20), -2, "tiles in one launch"),
+    (_combine(T=(1 << 25) + 1, M=1 << 27), -2, "2\\^25 tokens"),
+    (_backward(T=(1 << 25) + 1, k=1, dt=0), -2, "too large|2\\^25"),
+    (_backward(T=1 << 20, k=2, H=1 << 17), -2, "2\\^30 blocks"),
     (_backward(wu=N), -1, "w_up"), (_backward(act=1), -1, "GELU"), (_backward(size=100), -3, "workspace"),
     (_backward(ws=N), -1, "null"), (_backward(x=N), -1, "null"), (_backward(xs=N), -1, "null"), (_backward(y=N), -1, "null"),
     (_backward(ys=N), -1, "null"), (_backward(src=N), -1, "null"), (_backward(w=N), -1, "null"),
@@ -45,7 +48,7 @@ def _backward(x=P, xs=P, y=P, ys=P, dt=1, T=8, k=2, H=64, I=64, E=4, src=P, w=P,
     (("moe_mx_quantize", (P, 1, -1, 64, 0, P, P, N, N)), -1, "rows"),
     (("moe_mx_quantize", (P, 1, 4, 0, 0, P, P, N, N)), -1, "K=0"),
     (("moe_mx_quantize", (P, 1, 4, 1 << 29, 0, P, P, N, N)), -1, "K="),
-    (("moe_mx_quantize", (P, 1, 1 << 32, 64, 0, P, P, N, N)), -2, "2\\^31 blocks"),
+    (("moe_mx_quantize", (P, 1, 1 << 32, 64, 0, P, P, N, N)), -2, "2\\^30 blocks"),
     (("moe_mx_quantize", (N, 1, 4, 64, 0, P, P, N, N)), -1, "null"),
     (("moe_mx_quantize", (P, 1, 4, 64, 0, P, N, N, N)), -1, "null"),
     (("moe_mx_quantize", (N, 1, 0, 64, 0, N, N, N, N)), 0, ""),
