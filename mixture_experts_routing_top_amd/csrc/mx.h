@@ -152,8 +152,6 @@ __device__ __forceinline__ void load_values(const void* p, uint32_t i, int n, fl
       for (int u = 0; u < 4; ++u) v[u] = u < n ? q[u] : 0.f;
   }
 }
-// Stores of whole pieces go past the caches: they are not read again soon.
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
 template <bool kBf16, int V>
 __device__ __forceinline__ void store_values(void* p, uint32_t i, int n, const float (&v)[V]) {
   if (n < V) {
@@ -168,10 +166,7 @@ __device__ __forceinline__ void store_values(void* p, uint32_t i, int n, const f
     if constexpr (!kBf16) w[u] = __float_as_uint(v[u]);
     else if (u % 2 == 0) w[u / 2] = pack_bf16(v[u], v[u + 1]);
   }
-  u32x4* q = reinterpret_cast<u32x4*>(static_cast<char*>(p) + static_cast<uint64_t>(i) * (kBf16 ? 2 : 4));
-#pragma unroll
-  for (int u = 0; u < (kBf16 ? V / 2 : V); u += 4)
-    __builtin_nontemporal_store((u32x4{w[u], w[u + 1], w[u + 2], w[u + 3]}), q + u / 4);
+  __builtin_memcpy(static_cast<char*>(p) + static_cast<uint64_t>(i) * (kBf16 ? 2 : 4), w, sizeof(w));
 }
 
 // The scale byte of the block that this lane's V values are a part of (its lanes together).

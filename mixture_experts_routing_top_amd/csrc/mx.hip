@@ -184,9 +184,9 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* __restri
 // d_y[inv[t,i]] = w[t,i] d_out[t] and d_w[t,i] = <d_out[t], y[inv[t,i]]>.  kWaves
 // waves a token (kWaves = 1: four tokens a block), eight values of the row and of each
 // of its KK expert rows a lane and step, all loads of a step before its sums.  Bound by
-// memory: 8192 tokens of two kept rows, H = 4096, 271 MB in 46 us (5.8 TB/s); 16001 of six,
-// H = 5120, 1.66 GB in 332 (5.0; the rows are written in the experts' order, a token's far
-// apart).
+// memory: 8192 tokens of two kept rows, H = 4096, 271 MB in 58 us (4.7 TB/s; 46 where the
+// output takes the last call's place); 16001 of six, H = 5120, 1.66 GB in 332 (5.0; the rows
+// are written in the experts' order, a token's far apart).
 template <bool kBf16, bool kKept, int kWaves, int KK>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const void* __restrict__ d_out, const void* __restrict__ y,
                                                                const uint8_t* __restrict__ y_scale, int64_t M,
