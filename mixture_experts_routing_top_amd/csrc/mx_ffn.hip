@@ -22,8 +22,8 @@
 // instructions reach alone under the power limit (5.26 and 6.1 PFLOP/s), and a tile's
 // epilogue, beside which nothing runs, is 6 to 7 of its 41 us.  4001 tokens, two of 32 GELU
 // experts of 1024 x 4096, 114 us: 8 K steps a tile, vector issue and fills.  Few rows an
-// expert are the weights' bytes: 61 tokens, six of 160 experts of 5120 x 1536, 176 us (4.7
-// TB/s), 1021 tokens in 4 bits 488, one token 29.
+// expert are the weights' bytes: 61 tokens, six of 160 experts of 5120 x 1536, 160 us (5
+// TB/s), 1021 tokens in 4 bits 462, one token 29.
 //
 // Why 6 bits and not 8.  Lane group g (lane / rows) of an operand holds K = 32 g ..
 // 32 g + 31 and their scale.  The instruction sums eight products at a time, each
@@ -70,6 +70,7 @@ struct MxGemm {
   int n_col_tiles;
   void* C;             // y [M, N], or h's codes
   uint8_t *C2, *Cs;    // h's second plane and scales
+  int big;             // the experts' weights are far more than the last-level cache holds
 };
 
 // A block's codes and scale to their places in planes of M rows.
@@ -257,8 +258,9 @@ __device__ __forceinline__ void load_lds4(const u32x4& r, int off, unsigned lds_
 }
 #pragma clang diagnostic pop
 
-// The product of rows row0 and n - 1 on with output columns n0 on.
-template <int kBits, int EPI, int BM>
+// The product of rows row0 and n - 1 on with output columns n0 on.  kOnce: no other tile
+// reads these weights, and their lines are the first that the caches give up.
+template <int kBits, int EPI, int BM, bool kOnce>
 __device__ __forceinline__ void tile_body(const MxGemm& g, char* lds, int e, int64_t row0, int n, int n0) {
   using S = TileShape<kBits, BM>;
   constexpr int BN = S::BN;
@@ -309,7 +311,7 @@ __device__ __forceinline__ void tile_body(const MxGemm& g, char* lds, int e, int
   // Load p of stage ks of the weights; the scales of group kg (512 K values).
   auto issue_b = [&](int p, int ks, int stage) {
     const unsigned past = ks * 256 < K ? 0u : static_cast<unsigned>(kGatherOut);
-    load_lds(NMAT == 2 && p >= PB / 2 ? rb1 : rb0, offb + p % (PB / NMAT) * b_pass + ks * 128 + past,
+    load_lds_hint<kOnce>(NMAT == 2 && p >= PB / 2 ? rb1 : rb0, offb + p % (PB / NMAT) * b_pass + ks * 128 + past,
              lds0 + stage + (p * 4 + wave) * 1024);
   };
   auto issue_scales = [&](int kg) {
@@ -511,7 +513,7 @@ __device__ __forceinline__ void tile_body(const MxGemm& g, char* lds, int e, int
 // of down tiles (16384 rows of 8 experts, K = 14336, 6 bits) 625 us whole, 572 so.
 constexpr int kCus = 256;
 
-template <int kBits, int EPI, int BM>
+template <int kBits, int EPI, int BM, bool kBig>
 __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void tile_kernel(const MxGemm g) {
   __shared__ __align__(1024) char lds[TileShape<kBits, BM>::kLds];
   constexpr int kCols = TileShape<kBits, BM>::BN / mats(EPI);
@@ -531,10 +533,19 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void tile_kernel(const MxGe
     if (b >= whole) {
       const int down = quarter / 2 * 128, right = quarter % 2 * (kCols / 2);
       if (down < n && nt * kCols + right < g.N)
-        tile_body<kBits, EPI, 128>(g, lds, e, row0 + down, min(n - down, 128), nt * kCols + right);
+        tile_body<kBits, EPI, 128, false>(g, lds, e, row0 + down, min(n - down, 128), nt * kCols + right);
       return;
     }
-  tile_body<kBits, EPI, BM>(g, lds, e, row0, n, nt * kCols);
+  // An expert with one row tile (its tiles follow one another in the list): 61 tokens of 160
+  // experts 173 us without the hint, 160 with it; where other tiles read the same lines again
+  // it costs (1021 tokens 473, with it for every tile 487, so 461), and also where all the
+  // weights may wait in the last-level cache for the next call (2000 GELU tokens of 32 experts
+  // of 1024 x 4096, 142 MB, over and over: 63 us without it, 78 with it).
+  if constexpr (kBig) {
+    const bool alone = (mt == 0 || g.tiles[mt - 1].x != e) && (mt + 1 == total_m || g.tiles[mt + 1].x != e);
+    if (__builtin_amdgcn_readfirstlane(alone)) return tile_body<kBits, EPI, BM, true>(g, lds, e, row0, n, nt * kCols);
+  }
+  tile_body<kBits, EPI, BM, false>(g, lds, e, row0, n, nt * kCols);
 }
 
 // ---- few rows an expert ------------------------------------------------------------
@@ -754,9 +765,11 @@ int launch_product(MxGemm p, int bm, int64_t row_tiles, hipStream_t s, const cha
   if (bm == kStreamRows) return launch_stream<kBits, EPI>(p, row_tiles, s, what);
   p.n_col_tiles = tile_cols(bm, p.N, mats(EPI));
   const unsigned grid = static_cast<unsigned>(tile_blocks(bm, row_tiles, p.n_col_tiles));
-  if (bm == 64) tile_kernel<kBits, EPI, 64><<<grid, 256, 0, s>>>(p);
-  else if (bm == 128) tile_kernel<kBits, EPI, 128><<<grid, 256, 0, s>>>(p);
-  else tile_kernel<kBits, EPI, 256><<<grid, 256, 0, s>>>(p);
+  if (bm == 64 && p.big) tile_kernel<kBits, EPI, 64, true><<<grid, 256, 0, s>>>(p);
+  else if (bm == 64) tile_kernel<kBits, EPI, 64, false><<<grid, 256, 0, s>>>(p);
+  else if (bm == 128 && p.big) tile_kernel<kBits, EPI, 128, true><<<grid, 256, 0, s>>>(p);
+  else if (bm == 128) tile_kernel<kBits, EPI, 128, false><<<grid, 256, 0, s>>>(p);
+  else tile_kernel<kBits, EPI, 256, false><<<grid, 256, 0, s>>>(p);
   return moe::hip_status(hipGetLastError(), what);
 }
 
@@ -833,6 +846,7 @@ extern "C" int moe_mx_expert_ffn(const void* x, const int32_t* row_src, int64_t 
   else prepare(fp6 ? prepare_kernel<false, mx::kF6> : prepare_kernel<false, mx::kF4>);
   if (int rc = hip_status(hipGetLastError(), "moe_mx_expert_ffn prepare launch")) return rc;
   MxGemm up{};
+  up.big = static_cast<int64_t>(E) * H * I * (act == MOE_SWIGLU ? 3 : 2) * 17 / 32 > (int64_t(1) << 29);   // (twice its 256 MB)
   up.A = at(w.xq);
   up.A2 = at(w.xq2);
   up.As = at(w.xs);

@@ -361,6 +361,24 @@ def test_ffn_whole_and_quartered_tiles(act, fmt, dtype):
     _assert_ffn(y, om.values(_f64(x), fmt), range(sum(counts)), table, wts, act, fmt, dtype)
 
 
+@pytest.mark.parametrize("act", ["swiglu", "gelu"])
+def test_ffn_of_experts_past_the_cache(act):
+    """160 experts, 1.07 GB of them (GELU 0.71), of which four have rows (one and two tiles): as the four alone."""
+    E, H, I, counts, live = 160, 2048, 2048, [7, 0, 90, 30], [3, 50, 51, 159]
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    raw = lambda n, k: (torch.randint(0, 256, (E, n, k // 2), generator=gen, device="cuda", dtype=torch.uint8),  # noqa: E731
+                        torch.randint(116, 121, (E, n, k // 32), generator=gen, device="cuda", dtype=torch.uint8))
+    wts = [raw(I, H), raw(I, H) if act == "swiglu" else None, raw(H, I)]
+    few = [None if w is None else tuple(t[live].contiguous() for t in w) for w in wts]
+    x = _rows((sum(counts), H), torch.bfloat16, 3)
+    off, experts, n = _table(counts)
+    all_counts = [0] * E
+    for e, c in zip(live, counts):
+        all_counts[e] = c
+    y = moe.moe_mx_expert_ffn(x, *_table(all_counts), *wts, act)
+    assert bool(y.isfinite().all()) and torch.equal(y, moe.moe_mx_expert_ffn(x, off, experts, n, *few, act))
+
+
 @pytest.mark.parametrize("fmt", X_FORMATS)
 @pytest.mark.parametrize("counts", [[3, 0, 5, 9], [30, 2, 21, 50], [70, 2, 31, 90], [60, 100, 70, 50], [200, 150, 300, 129]])
 def test_ffn_gathers_rows(fmt, counts):
