@@ -211,15 +211,20 @@ __device__ __forceinline__ int xcd_run(int b, int total) {
   return xcd * q + min(xcd, rem) + (b >> 3);
 }
 
-// z Phi(z), the exact GELU: Phi(-|z|) = e^(-z^2 / 2) P(t) / 2, t = 1 / (1 + p |z| / sqrt 2),
-// Abramowitz and Stegun 7.1.26, off by at most 0.75e-7 |z|; thirteen instructions and two
-// of the quarter rate, a third of what erff takes.
+// z Phi(z), the exact GELU: Phi(-|z|) = R(t) 2^(-z^2 log2(e) / 2), t = 1 / (1 + 0.3 |z|), R a
+// polynomial fitted here (least largest relative error over |z| <= 13.2: 1.5e-7).  h is off
+// by at most (16 + z^2) 2^-24 of itself, the exponent's rounding being the z^2: a negative
+// z's h is a tail of its own and not 1 + erf, which has cancelled by then.  Sixteen
+// instructions and two of the quarter rate, half of what erff takes.
 __device__ __forceinline__ float fast_gelu(float z) {
-  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3275911f * 0.70710678f, 1.f));
-  float p = fmaf(t, 0.5f * 1.061405429f, -0.5f * 1.453152027f);
-  p = fmaf(p, t, 0.5f * 1.421413741f);
-  p = fmaf(p, t, -0.5f * 0.284496736f);
-  p = fmaf(p, t, 0.5f * 0.254829592f) * t;
+  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3f, 1.f));
+  float p = fmaf(t, 0.0361417732f, -0.159168098f);
+  p = fmaf(p, t, 0.209781963f);
+  p = fmaf(p, t, -0.0568914098f);
+  p = fmaf(p, t, 0.130297077f);
+  p = fmaf(p, t, 0.099370426f);
+  p = fmaf(p, t, 0.120845415f);
+  p = fmaf(p, t, 0.119622796f) * t;
   const float tail = p * __builtin_amdgcn_exp2f(z * z * -0.72134752f);
   return fmaxf(z, 0.f) - fabsf(z * tail);
 }
