@@ -232,14 +232,15 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const void* __res
 #pragma unroll
     for (int i = 0; i < KK; ++i) {
       float v[8], s = 0.f, p[8];
-      if constexpr (kKept) mx::decode8_fp8(q[i], 1.f, v);
+      // (the values, exact, and not the codes: a block's largest code is 224 to 448 whatever its scale is)
+      if constexpr (kKept) mx::decode8_fp8(q[i], mx::scale_value(byte[i]), v);
       else unpack8<kBf16>(yr[i], v);
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         s = fmaf(o[u], v[u], s);
         p[u] = w[i] * o[u];
       }
-      acc[i] = fmaf(s, kKept ? mx::scale_value(byte[i]) : 1.f, acc[i]);
+      acc[i] += s;
       if (there[i]) mx::store_values<kBf16, 8>(static_cast<char*>(d_y) + at[i] * H * (kBf16 ? 2 : 4), c * 8, 8, p);
     }
   }
