@@ -581,7 +581,9 @@ int moe_backward_gated(const void* x_perm, const void* y_perm, moe_dtype dt, int
  * blocks stand for, x_perm's in `dt`: each is off by at most 2^-4 of itself, or by
  * 2^-10 of its block's scale where that is more.  The weights stay as they are.  The
  * workspace holds x_perm too.  With a check word, MOE_CHECK_ROWS for an entry of
- * perm_src or inv_pos out of range (its row counts as zero).
+ * perm_src or inv_pos out of range.  A row whose perm_src is out of range has x zero,
+ * and a row that no entry of inv_pos names d_y zero: its (token, slot) adds nothing to
+ * any gradient, and has d_topk_w 0.
  * Limits: those of moe_backward, T at most 2^25 and T*k*H at most 2^35.
  */
 size_t moe_backward_mx_workspace_bytes(moe_dtype dt, int64_t T, int k, int H, int I, int E, moe_act act); /* [host] */

@@ -236,6 +236,26 @@ __global__ void bwd_setup_kernel(const int32_t* __restrict__ off, int E, int64_t
     ones[i] = 1.f;
 }
 
+// moe_backward_mx: d_y rows that no entry of inv_pos names (one of them out of range, or two
+// with one row) are zero, and not what the workspace held: cleared before the combine's
+// gradient writes the named ones.  A row's token is perm_src's; a row that another token
+// names all the same is written right after.  A lane a row; 4 (k + 1) bytes a row, 4.6 us
+// for 16384 rows, beside 13 ms.
+__global__ __launch_bounds__(256) void clear_unnamed_kernel(const int32_t* __restrict__ perm_src,
+                                                            const int32_t* __restrict__ inv_pos, int64_t T, int k,
+                                                            int64_t M, int chunks, uint4* __restrict__ dy) {
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * 256 + (threadIdx.x & ~63u), row = first + (threadIdx.x & 63);
+  bool unnamed = row < M;
+  if (unnamed) {
+    const int64_t t = perm_src[row];
+    if (t >= 0 && t < T)
+      for (int i = 0; i < k; ++i) unnamed &= inv_pos[t * k + i] != row;
+  }
+  for (uint64_t m = __ballot(unnamed); m != 0; m &= m - 1)
+    for (int c = threadIdx.x & 63; c < chunks; c += 64)
+      dy[(first + __ffsll(static_cast<unsigned long long>(m)) - 1) * chunks + c] = make_uint4(0, 0, 0, 0);
+}
+
 // blocks of a weight-gradient launch: 8 equal shares of each expert's
 // (256-row x 256-column) tiles
 unsigned wgrad_grid(int E, int64_t rows, int col_tiles) {
@@ -334,6 +354,10 @@ int run_backward(const Kept* kept, const void* x_perm, const void* y_perm, int64
     if (int rc = moe_mx_dequantize(kept->x, kept->x_scale, MOE_MX_FP8, n_tok, H, kept->perm_src, M, kDt,
                                    at(kept_rows_at(L)), kept->check, s))
       return rc;
+    if (M > 0)
+      clear_unnamed_kernel<<<static_cast<unsigned>(ceil_div(M, 256)), 256, 0, s>>>(
+          kept->perm_src, inv_pos, n_tok, k, M, chunks, reinterpret_cast<uint4*>(dy));
+    if (int rc = check("moe_backward_mx clear")) return rc;
     if (int rc = moe_combine_backward(d_out, kDt, kept->y, kept->y_scale, M, inv_pos, topk_w, n_tok, k, H, dy, d_topk_w,
                                       kept->check, s))
       return rc;
