@@ -406,7 +406,8 @@ PyObject* mx_dequantize(PyObject*, Args a, Py_ssize_t n) {
   TORCH_CHECK_VALUE(q.dim() >= 1 && q.scalar_type() == at::kByte, "q: expected uint8 codes");
   const int64_t bytes = q.size(-1);
   const int64_t K = a[4] == Py_None ? bytes * 8 / code_bits(fmt) : whole(a[4]);
-  TORCH_CHECK_VALUE(K >= 1 && code_bytes(fmt, K) == bytes, "q: rows of ", bytes, " bytes do not hold ", K, " values");
+  // (bounded first: of 2^61 values the bytes would come to 0, those of rows that hold none)
+  TORCH_CHECK_VALUE(K >= 1 && K < INT64_MAX / 8 && code_bytes(fmt, K) == bytes, "q: rows of ", bytes, " bytes do not hold ", K, " values");
   const int64_t R = q.numel() / bytes;
   std::vector<int64_t> shape = q.sizes().vec(), blocks = shape;
   blocks.back() = blocks_of(K);
