@@ -448,8 +448,8 @@ int moe_combine(const void* y_perm, moe_dtype dt, int64_t M, const int32_t* inv_
  *   y        the expert outputs [M, H] in `dt` (y_scale NULL), or as moe_mx_quantize
  *            keeps them in MOE_MX_FP8: codes [M, H] and y_scale [M, ceil(H / 32)].
  * inv_pos entries outside [0, M) get d_topk_w 0 and write no row (MOE_CHECK_ROWS);
- * rows that no entry names are left as they are, and a row that two entries name
- * holds either's.  d_y may not be y or d_out.
+ * rows that no entry names are left as they are, and a row that two tokens name holds
+ * pieces of either's.  d_y may not be y or d_out.
  * Limits: 1 <= k <= 8, H a multiple of 8, T at most 2^25; d_out, y and d_y 16-byte
  * aligned.  The dispatch's own gradient, d_x[t] = sum_i d_x_perm[inv_pos[t, i]],
  * is moe_combine with unit weights.
@@ -497,15 +497,17 @@ int moe_mx_dequantize(const uint8_t* q, const uint8_t* scale, moe_mx_format fmt,
  *   x, row_src, n_src, the slot table, y_perm   as in moe_expert_ffn; x and y_perm
  *            in `dt`.  Row_src NULL: n_src is taken as M.
  * Products are exact on the scaled matrix instructions and summed in fp32; h is formed
- * in fp32 and quantised from there, y is rounded once.  No host sync.  How rows
+ * in fp32 (GELU's within (16 + z^2) 2^-24 of itself) and quantised from there, y is
+ * rounded once; an h past float's range makes its row of y NaN.  No host sync.  How rows
  * are tiled hangs on M / E, and an h next to a rounding's border may fall on its other
  * side in another tiling.  A row whose x holds a NaN or an infinity is NaN, alone.
  * Slots are tiled one by one (replicas of one expert are not merged).
  *   workspace  moe_mx_expert_ffn_workspace_bytes(M, ...) bytes, rewritten by every
  *            call: two calls in flight need two.
  * Limits: H and I multiples of 128 up to 2^22, H*I/2 below 0x7e000000, M times the
- * larger of H and I at most 2^36; 1 <= E <= max_slots, and a launch's tiles (rows by 64,
- * 128 or 256, one more a slot, times columns by as many) below 2^24.
+ * larger of H and I below 2^36; 1 <= E <= max_slots, and a launch's tiles below 2^24:
+ * (M / 64, M / 128 or M / 256, and one for each slot or row, whichever are fewer) times
+ * H / 128 or, of h, I / 128, twice that for SwiGLU (half of each for 256-row tiles).
  * All tensors 16-byte aligned.
  * check: MOE_CHECK_SLOTS, MOE_CHECK_BLOCKS (in x).
  */

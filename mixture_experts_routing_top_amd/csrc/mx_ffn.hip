@@ -7,23 +7,28 @@
 // Three launches:
 //   prepare:  the rows of x quantised, one block a lane, and in block 0 the list of
 //             row tiles from the slot table;
-//   gate/up:  per tile and 128 (or 32) columns of h, gate and up side by side; the
+//   gate/up:  per row tile and its columns of h, gate and up side by side; the
 //             epilogue trades accumulators between lanes until each holds 32
 //             adjacent columns of a row, quantises them in registers and writes
 //             their codes;
 //   down:     y = Q(h) Wd^T.
+// A tile's weight rows, half of them the gate's and half the up weights' for SwiGLU:
+// 256 beside 256 rows of A, 128 beside 64 or 128, 64 (or 32) beside the stream's 16.
 // Two kernels multiply.  tile_kernel: BM rows x 128 or 256 weight rows a block, operands
 // straight into LDS, 32x32x64 instructions.  stream_kernel: at most 16 rows by 64
 // weight rows a block, K split over the block's waves: for few rows the time is the
 // weights' bytes.
 //
 // Measured, and what bounds it: 8192 tokens, two of 8 experts of 4096 x 14336, in 6 bits
-// 1.73 ms, 3.3 PFLOP/s (in 4 bits 1.57, 3.7): the K loop runs at 83 % of what the
-// instructions reach alone under the power limit (5.26 and 6.1 PFLOP/s), and a tile's
-// epilogue, beside which nothing runs, is 6 to 7 of its 41 us.  4001 tokens, two of 32 GELU
-// experts of 1024 x 4096, 114 us: 8 K steps a tile, vector issue and fills.  Few rows an
-// expert are the weights' bytes: 61 tokens, six of 160 experts of 5120 x 1536, 160 us (5
-// TB/s), 1021 tokens in 4 bits 462, one token 29.
+// 1.72 ms, 3.35 PFLOP/s (in 4 bits 1.57, 3.7): gate/up 1.23 and down 0.57.  The K loop runs at
+// some 83 % of what the instructions reach alone under the power limit (5.1 to 5.3 PFLOP/s,
+// 4 by 4 bits 5.6 to 6.1, from card to card), and beside a tile's epilogue, 6 to 7 us of a
+// gate/up tile's 41 (32 K steps; a down tile has 112), nothing runs.  4001 tokens, two of 32
+// GELU experts of 1024 x 4096, 115 us: gate/up 67, 8 K steps a tile beside the GELU's vector
+// issue, and down 52, two rounds of tiles for 1.25.  Few rows an expert are the weights'
+// bytes: 61 tokens, six of 160 experts of 5120 x 1536, 150 to 160 us (5 TB/s), 1021 tokens in
+// 4 bits 463 to 477, one token 29.  Float rows for bf16 ones add the bytes of x and y (8192
+// tokens 1.78 ms, 4001 of the GELU experts 125 us).
 //
 // Why 6 bits and not 8.  Lane group g (lane / rows) of an operand holds K = 32 g ..
 // 32 g + 31 and their scale.  The instruction sums eight products at a time, each
@@ -214,8 +219,8 @@ __device__ __forceinline__ int xcd_run(int b, int total) {
 // z Phi(z), the exact GELU: Phi(-|z|) = R(t) 2^(-z^2 log2(e) / 2), t = 1 / (1 + 0.3 |z|), R a
 // polynomial fitted here (least largest relative error over |z| <= 13.2: 1.5e-7).  h is off
 // by at most (16 + z^2) 2^-24 of itself, the exponent's rounding being the z^2: a negative
-// z's h is a tail of its own and not 1 + erf, which has cancelled by then.  Sixteen
-// instructions and two of the quarter rate, half of what erff takes.
+// z's h is a tail of its own and not 1 + erf, which has cancelled by then.  Fifteen
+// instructions and two of the quarter rate, where erff takes some 36.
 __device__ __forceinline__ float fast_gelu(float z) {
   const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3f, 1.f));
   float p = fmaf(t, 0.0361417732f, -0.159168098f);
@@ -545,7 +550,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void tile_kernel(const MxGe
   // experts 173 us without the hint, 160 with it; where other tiles read the same lines again
   // it costs (1021 tokens 473, with it for every tile 487, so 461), and also where all the
   // weights may wait in the last-level cache for the next call (2000 GELU tokens of 32 experts
-  // of 1024 x 4096, 142 MB, over and over: 63 us without it, 78 with it).
+  // of 1024 x 4096, 142 MB, over and over: 65 us without it, 75 with it).
   if constexpr (kBig) {
     const bool alone = (mt == 0 || g.tiles[mt - 1].x != e) && (mt + 1 == total_m || g.tiles[mt + 1].x != e);
     if (__builtin_amdgcn_readfirstlane(alone)) return tile_body<kBits, EPI, BM, true>(g, lds, e, row0, n, nt * kCols);
@@ -707,7 +712,7 @@ struct MxLayout {
 //     76 there 691 against 654, 64 at H = 6144 470 against 454, at H = 4096 220 against 234.
 //   256-row tiles where rows and K make up for one block a CU, from 2^19 rows * H an expert
 //     on: 131 rows at H = 5120 794 against 827 in 128-row tiles, 256 at H = 4096 349 against
-//     407; 76 at H = 5120 677 against 654, 250 at H = 1024 123 against 106.
+//     407; 76 at H = 5120 677 against 654, 250 at H = 1024 122 against 117.
 int rows_per_tile(int64_t M, int E, int H) {
   const int64_t avg = M / E;
   if (M <= 24) return kStreamRows;
@@ -735,8 +740,12 @@ MxLayout mx_layout(int64_t M, int H, int I, int max_slots, moe_mx_format fmt) {
 }
 
 // Few rows.  Narrow blocks (32 columns instead of 64) where the wide ones come to fewer
-// than 7 for every 4 CUs: 4096 columns and two experts 16.4 against 23 us; 5120 and six,
-// 480 blocks, 8.9 against 7.8.  Eight waves a block where each CU has one block at most.
+// than 7 for every 4 CUs.  Whole calls, narrow against wide, by wide blocks of the down
+// product: K = 1536 128 blocks 15.8 us against 16.4, 256 equal, 400 23.0 against 22.1, 512 25.2
+// against 24.2; K = 14336 64 blocks 32.6 against 41.4, 128 48.8 against 57.1, 256 equal, 384
+// 113.1 against 122.2, 448 134.4 against 135.4.  (A long K wins where the blocks are few or
+// just past one a CU, a short one loses up to 1 us there.)  Eight waves a block where each CU
+// has one block at most.
 template <int kBits, int EPI>
 int launch_stream(MxGemm p, int64_t row_tiles, hipStream_t s, const char* what) {
   constexpr int kWide = 64 / mats(EPI);

@@ -61,3 +61,21 @@ def test_blocks_marked_nan(fmt, counts, H):
             assert np.array_equal(np.isnan(_f64(y)), bad)
             good = torch.from_numpy(~bad).cuda()
             assert torch.equal(y[good], want[good])
+
+
+@pytest.mark.parametrize("act", ["swiglu", "gelu"])
+@pytest.mark.parametrize("fmt", X_FORMATS)
+@pytest.mark.parametrize("counts,H", TILES)
+def test_h_past_the_range(fmt, act, counts, H):
+    """Sums or an h that float32 does not hold: that row of y is NaN, the others as they were, and x is clean."""
+    E, M, I = len(counts), sum(counts), 128
+    wts = (_weights(E, I, H, 1), _weights(E, I, H, 2) if act == "swiglu" else None, _weights(E, H, I, 3))
+    x, table = _rows((M, H), torch.float32, 5), _table(counts)
+    x[1] = 0
+    want = moe.moe_mx_expert_ffn(x, *table, *wts, act, fmt)
+    x[1] = 3e38 * torch.sign(x[2])
+    check = moe.new_check_word()
+    y = moe.moe_mx_expert_ffn(x, *table, *wts, act, fmt, check=check)
+    assert moe.moe_check_device_error(check) == 0
+    others = torch.arange(M, device="cuda") != 1
+    assert bool(y[1].isnan().all()) and torch.equal(y[others], want[others])
