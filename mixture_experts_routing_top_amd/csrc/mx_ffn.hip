@@ -20,7 +20,7 @@
 // weights' bytes.
 //
 // Measured, and what bounds it: 8192 tokens, two of 8 experts of 4096 x 14336, in 6 bits
-// 1.72 ms, 3.35 PFLOP/s (in 4 bits 1.57, 3.7): gate/up 1.23 and down 0.57.  The K loop runs at
+// 1.72 ms, 3.35 PFLOP/s (in 4 bits 1.57, 3.7): gate/up 1.15 and down 0.55.  The K loop runs at
 // some 83 % of what the instructions reach alone under the power limit (5.1 to 5.3 PFLOP/s,
 // 4 by 4 bits 5.6 to 6.1, from card to card), and beside a tile's epilogue, 6 to 7 us of a
 // gate/up tile's 41 (32 K steps; a down tile has 112), nothing runs.  4001 tokens, two of 32
