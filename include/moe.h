@@ -509,7 +509,8 @@ int moe_mx_dequantize(const uint8_t* q, const uint8_t* scale, moe_mx_format fmt,
  * (M / 64, M / 128 or M / 256, and one for each slot or row, whichever are fewer) times
  * H / 128 or, of h, I / 128, twice that for SwiGLU (half of each for 256-row tiles).
  * All tensors 16-byte aligned.
- * check: MOE_CHECK_SLOTS, MOE_CHECK_BLOCKS (in x).
+ * check: MOE_CHECK_SLOTS, MOE_CHECK_BLOCKS (in x: any of the M rows, also those of no slot,
+ * whose rows of y are left as they are).
  */
 size_t moe_mx_expert_ffn_workspace_bytes(int64_t M, int H, int I, int max_slots, moe_mx_format x_format); /* [host] */
 int moe_mx_expert_ffn(const void* x, const int32_t* row_src, int64_t n_src, moe_dtype dt, int64_t M, int H, int I,

@@ -37,6 +37,27 @@ def test_ffn_reads_only_what_it_wrote(fmt, act, counts, H, I):
     assert all(torch.equal(got[0].view(torch.int16), g.view(torch.int16)) for g in got[1:])
 
 
+# rows before the first slot, behind the last one and (from an expert out of range on) of a slot that is skipped
+@pytest.mark.parametrize("off,H,tail", [([2, 5, 9], 384, 4), ([3, 40, 41], 384, 30), ([70, 150, 290], 640, 60),
+                                        ([5, 300, 520], 2176, 290)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("fmt", X_FORMATS)
+def test_ffn_leaves_rows_of_no_slot(fmt, dtype, off, H, tail):
+    I, M = 256, off[-1] + tail
+    x = _rows((M, H), dtype, H)
+    wts = (_weights(2, I, H, 1), _weights(2, I, H, 2), _weights(2, H, I, 3))
+    dev = dict(dtype=torch.int32, device="cuda")
+    for experts in ([1, 0], [1, 2]):
+        table = torch.tensor(off, **dev), torch.tensor(experts, **dev), torch.tensor([2], **dev)
+        want = moe.moe_mx_expert_ffn(x, *table, *wts, x_format=fmt)
+        there = torch.zeros(M, dtype=torch.bool, device="cuda")
+        there[off[0]:off[2] if experts[1] == 0 else off[1]] = True
+        rows = torch.where(there[:, None], x, torch.full_like(x, float("nan")))   # (their x is nobody's)
+        y = moe.moe_mx_expert_ffn(rows, *table, *wts, x_format=fmt, y_perm=torch.full_like(x, 7.0))
+        assert bool(want[there].isfinite().all())
+        assert torch.equal(y[there], want[there]) and bool((y[~there] == 7).all())
+
+
 @pytest.mark.parametrize("act", ["swiglu", "gelu"])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("size", [(1, 4, 64, 64, 1), (37, 6, 128, 192, 2), (700, 8, 576, 64, 8)])
